@@ -24,6 +24,9 @@ IDX_HEADS, IDX_DIM = 64, 128
 MAX_TOKENS_PER_SEQ, MAX_TOPK, MAX_SWA_WINDOW = 128, 2048, 512
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_BAD_INDEX = range(7)
+FORMAT_FP8, FORMAT_FP4 = range(2)
+FP4_RECORD_BYTES = 384
+FORMAT_BYTES = (RECORD_BYTES, FP4_RECORD_BYTES)
 OP_INDEXER, OP_TOPK, OP_ATTENTION, OP_HCA_ATTENTION, OP_DECODE_STEP = range(5)
 
 EXPORTED = ["csa_workspace_bytes", "csa_indexer_logits", "csa_topk", "csa_gather_swa",
@@ -32,7 +35,8 @@ EXPORTED = ["csa_workspace_bytes", "csa_indexer_logits", "csa_topk", "csa_gather
             "csa_status_string", "csa_version", "csa_kernel_launches",
             "csa_sink_attention_decode_noalloc", "csa_pipeline_staging_bytes", "csa_pipeline_create",
             "csa_decode_step_host", "csa_pipeline_wait", "csa_pipeline_sync", "csa_pipeline_destroy",
-            "csa_sink_attention_decode_ex", "hca_sink_attention_decode_ex", "csa_decode_step_ex"]
+            "csa_sink_attention_decode_ex", "hca_sink_attention_decode_ex", "csa_decode_step_ex",
+            "csa_head_norm_rope", "csa_head_norm_rope_e4m3", "csa_cache_append", "csa_cache_read"]
 PIPELINE_MAX_DEPTH = 4
 
 
@@ -51,6 +55,16 @@ class csa_cache_desc(C.Structure):
 class csa_attention_epilogue(C.Structure):
     _fields_ = [("inverse_rope", C.c_int32), ("rope_theta", C.c_float), ("out_fp4", C.c_void_p),
                 ("out_fp4_scale", C.c_void_p)]
+
+
+class csa_norm_rope(C.Structure):
+    _fields_ = [("norm", C.c_int32), ("eps", C.c_float), ("weight", C.c_void_p), ("rope_dim", C.c_int32),
+                ("rope_theta", C.c_float)]
+
+
+class csa_index_append(C.Structure):
+    _fields_ = [("key", C.c_void_p), ("seq_stride", C.c_int64), ("token_stride", C.c_int64), ("k_idx", C.c_void_p),
+                ("k_idx_scale", C.c_void_p), ("Ncap", C.c_int32)]
 
 
 _lib = None
@@ -122,6 +136,16 @@ def load(path: str | None = None):
         lib.csa_read_device_error.restype = st
         lib.csa_debug_set_wait_limit_ns.argtypes = [C.c_uint64]
         lib.csa_debug_set_wait_limit_ns.restype = None
+        i64, NR = C.c_int64, C.POINTER(csa_norm_rope)
+        lib.csa_head_norm_rope.argtypes = [P, i32, i64, i64, i64, P, i32, i32, i32, i32, NR, P, P, P]
+        lib.csa_head_norm_rope.restype = st
+        lib.csa_head_norm_rope_e4m3.argtypes = [P, i32, i64, i64, i64, P, i32, i32, i32, i32, NR, P, P, P, P]
+        lib.csa_head_norm_rope_e4m3.restype = st
+        lib.csa_cache_append.argtypes = [csa_cache_desc, i32, i32, P, i32, i64, i64, P, P, i32, i32, i32, NR,
+                                         C.POINTER(csa_index_append), P, P]
+        lib.csa_cache_append.restype = st
+        lib.csa_cache_read.argtypes = [csa_cache_desc, i32, i32, P, P, i32, i32, P, P, P]
+        lib.csa_cache_read.restype = st
         _lib = lib
         return lib
 
@@ -189,14 +213,20 @@ def _status(status, device) -> int:
 
 
 def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
-               block_table: torch.Tensor | None = None, page_records: int = 0) -> csa_cache_desc:
+               block_table: torch.Tensor | None = None, page_records: int = 0,
+               fmt: int = FORMAT_FP8) -> csa_cache_desc:
     """Describe a cache of latent records: ``records`` is uint8 [n, 592] (or
     [B, Ncap, 592]); contiguous mode uses ``seq_stride``, paged mode a
-    ``block_table`` [B, max_pages] int32 and ``page_records``."""
-    rec = records.reshape(-1, RECORD_BYTES) if records.dim() != 2 else records
+    ``block_table`` [B, max_pages] int32 and ``page_records``. With
+    ``fmt=FORMAT_FP4`` the records are the 384-byte 4-bit ones; the calls below
+    take the format from the description."""
+    if fmt not in (FORMAT_FP8, FORMAT_FP4):
+        raise ValueError(f"unknown record format {fmt}")
+    size = FORMAT_BYTES[fmt]
+    if records.shape[-1] != size:
+        raise ValueError(f"records must be [n, {size}] uint8")
+    rec = records.reshape(-1, size) if records.dim() != 2 else records
     _ptr(rec, "records", torch.uint8)
-    if rec.shape[1] != RECORD_BYTES:
-        raise ValueError("records must be [n, 592] uint8")
     d = csa_cache_desc()
     d.base = rec.data_ptr()
     d.n_records = rec.shape[0]
@@ -208,7 +238,15 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
         d.page_records = int(page_records)
         d.max_pages = int(block_table.shape[-1])
     d._keepalive = (rec, block_table)  # noqa: SLF001
+    d._fmt = fmt  # noqa: SLF001
     return d
+
+
+def _format(comp: csa_cache_desc, fmt: int, where: str) -> csa_cache_desc:
+    """The description itself, if it describes records of format ``fmt``."""
+    if getattr(comp, "_fmt", FORMAT_FP8) != fmt:
+        raise ValueError(f"{where} reads {FORMAT_BYTES[fmt]}-byte records; the cache holds the other format")
+    return comp
 
 
 def csa_workspace_bytes(op: int, B: int, T: int, Ncap: int, k: int) -> int:
@@ -272,7 +310,7 @@ def csa_gather_swa(comp: csa_cache_desc, swa_ring, W: int, topk_idx, topk_cnt, q
         kv_out = torch.empty((B, T, k + W, RECORD_BYTES), dtype=torch.uint8, device=dev)
     if kv_cnt is None:
         kv_cnt = torch.empty((B, T), dtype=torch.int32, device=dev)
-    _check(load().csa_gather_swa(comp, _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
+    _check(load().csa_gather_swa(_format(comp, FORMAT_FP8, "csa_gather_swa"), _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
                                  _ptr(topk_idx, "topk_idx", torch.int32), _ptr(topk_cnt, "topk_cnt", torch.int32, (B, T)),
                                  _ptr(q_pos, "q_pos", torch.int32, (B, T)), B, T, k,
                                  _ptr(kv_out, "kv_out", torch.uint8, (B, T, k + W, RECORD_BYTES)),
@@ -316,7 +354,8 @@ def csa_sink_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_des
     if ws is None:
         ws = workspace(OP_ATTENTION, B, T, comp.seq_capacity, k, dev)
     args = [_ptr(q, "q", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(sink, "sink", torch.float32, (HEADS,)),
-            float(softmax_scale), comp, _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
+            float(softmax_scale), _format(comp, FORMAT_FP8, "csa_sink_attention_decode"),
+            _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
             _ptr(topk_idx, "topk_idx", torch.int32, (B, T, k)), _ptr(topk_cnt, "topk_cnt", torch.int32, (B, T)),
             _ptr(q_pos, "q_pos", torch.int32, (B, T)), B, T, k,
             _ptr(out, "out", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(lse, "lse", torch.float32, (B, T, HEADS))]
@@ -343,7 +382,8 @@ def csa_sink_attention_decode_noalloc(q, sink, softmax_scale: float, comp: csa_c
         lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=dev)
     _check(load().csa_sink_attention_decode_noalloc(
         _ptr(q, "q", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(sink, "sink", torch.float32, (HEADS,)),
-        float(softmax_scale), comp, _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
+        float(softmax_scale), _format(comp, FORMAT_FP8, "csa_sink_attention_decode_noalloc"),
+        _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
         _ptr(topk_idx, "topk_idx", torch.int32, (B, T, k)), _ptr(topk_cnt, "topk_cnt", torch.int32, (B, T)),
         _ptr(q_pos, "q_pos", torch.int32, (B, T)), B, T, k,
         _ptr(out, "out", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(lse, "lse", torch.float32, (B, T, HEADS)),
@@ -367,7 +407,7 @@ def hca_sink_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_des
     if ws is None:
         ws = workspace(OP_HCA_ATTENTION, B, T, comp.seq_capacity, 0, dev)
     args = [_ptr(q, "q", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(sink, "sink", torch.float32, (HEADS,)),
-            float(softmax_scale), comp, _ptr(n_comp, "n_comp", torch.int32, (B,)),
+            float(softmax_scale), _format(comp, FORMAT_FP8, "hca_sink_attention_decode"), _ptr(n_comp, "n_comp", torch.int32, (B,)),
             _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
             _ptr(q_pos, "q_pos", torch.int32, (B, T)), B, T, int(m_hca),
             _ptr(out, "out", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(lse, "lse", torch.float32, (B, T, HEADS))]
@@ -401,7 +441,8 @@ def csa_decode_step(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, soft
             _ptr(w_idx, "w_idx", torch.float32, (B, T, IDX_HEADS)), _ptr(k_idx, "k_idx", u8, (B, Ncap, IDX_DIM)),
             _ptr(k_idx_scale, "k_idx_scale", torch.float32, (B, Ncap)),
             _ptr(q, "q", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(sink, "sink", torch.float32, (HEADS,)),
-            float(softmax_scale), comp, _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
+            float(softmax_scale), _format(comp, FORMAT_FP8, "csa_decode_step"),
+            _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
             _ptr(q_pos, "q_pos", torch.int32, (B, T)), _ptr(n_comp, "n_comp", torch.int32, (B,)),
             B, T, Ncap, int(m), int(k),
             _ptr(out, "out", torch.bfloat16, (B, T, HEADS, DIM)), _ptr(lse, "lse", torch.float32, (B, T, HEADS)),
@@ -412,6 +453,139 @@ def csa_decode_step(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, soft
     else:
         _check(load().csa_decode_step_ex(*args, C.byref(epi), *tail), "csa_decode_step_ex")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _dev(t: torch.Tensor, name: str) -> int:
+    """Index of the CUDA device that ``t`` is on, which has to be the current one
+    (the library launches there)."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if i != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{i}, not on the current device: make that device current for the call")
+    return i
+
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """Data pointer of a dense tensor of this dtype and shape on device ``dev``."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}: got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """Data pointer of a floating tensor of this shape whose rows (the last
+    dimension) are dense; the other strides are the caller's to pass on."""
+    if t.get_device() != dev or t.dtype not in _DTYPES or t.shape != shape:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 tensor of shape {tuple(shape)} on cuda:{dev}: got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return t.data_ptr()
+
+
+def _strides(t: torch.Tensor) -> list:
+    """Strides of the leading dimensions; 0 where a dimension has one element
+    (PyTorch leaves any number there)."""
+    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride())]
+
+
+def _how(norm: bool, weight, eps: float, rope_dim: int, rope_theta: float, D: int, dev: int) -> csa_norm_rope:
+    w = _arg(weight, "weight", torch.float32, (D,), dev) if weight is not None else None
+    return csa_norm_rope(1 if norm else 0, eps, w, rope_dim, rope_theta)
+
+
+def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6, rope_dim: int = ROPE,
+                       rope_theta: float = 10000.0, out=None, stream=None, status=None) -> torch.Tensor:
+    """RMS norm of every head of ``x`` [B, T, H, D] (bf16, fp16 or fp32; any
+    strides but a dense last dimension) and the rotation of its last
+    ``rope_dim`` values at ``pos`` [B, T] int32, in one pass; BF16 [B, T, H, D].
+    Rows of tokens with pos < 0 are left as they were: pass an ``out`` of your
+    own with padded batches. ``rope_dim=0`` rotates nothing, ``norm=False``
+    normalises nothing; ``out`` may be ``x``."""
+    B, T, H, D = x.shape
+    dev = _dev(x, "x")
+    if out is None:
+        out = torch.empty((B, T, H, D), dtype=torch.bfloat16, device=x.device)
+    _check(load().csa_head_norm_rope(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+                                     _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
+                                     _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
+                                     _arg(out, "out", torch.bfloat16, (B, T, H, D), dev), _status(status, x.device),
+                                     _stream(stream)), "csa_head_norm_rope")
+    return out
+
+
+def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float = 1e-6, rope_dim: int = ROPE,
+                            rope_theta: float = 10000.0, codes=None, scale=None, stream=None, status=None):
+    """csa_head_norm_rope with E4M3 output: (codes [B, T, H, D] uint8, scale
+    [B, T, H] fp32), the form csa_indexer_logits reads its queries in."""
+    B, T, H, D = x.shape
+    dev = _dev(x, "x")
+    if codes is None:
+        codes = torch.empty((B, T, H, D), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((B, T, H), dtype=torch.float32, device=x.device)
+    _check(load().csa_head_norm_rope_e4m3(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+                                          _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
+                                          _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
+                                          _arg(codes, "codes", torch.uint8, (B, T, H, D), dev),
+                                          _arg(scale, "scale", torch.float32, (B, T, H), dev),
+                                          _status(status, x.device), _stream(stream)), "csa_head_norm_rope_e4m3")
+    return codes, scale
+
+
+def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = False, norm: bool = False, weight=None,
+                     eps: float = 1e-6, rope_theta: float | None = 10000.0, pos_stride: int = 1, key=None,
+                     k_idx=None, k_idx_scale=None, stream=None, status=None) -> None:
+    """Append the latents ``x`` [B, T, 512] (bf16, fp16 or fp32) as entries
+    first[b] .. first[b] + count[b] of their sequences, in the cache's own
+    format, normalised (``norm``) and rotated at entry * pos_stride
+    (``rope_theta=None``: not rotated) on the way. ``ring``: entry modulo the
+    cache's capacity. ``key`` [B, T, 128] adds the entries' indexer keys to
+    ``k_idx`` [B, Ncap, 128] and ``k_idx_scale`` [B, Ncap]. See include/csa.h."""
+    B, T, _ = x.shape
+    dev = _dev(x, "x")
+    idx = None
+    if key is not None:
+        ncap = k_idx.shape[1]
+        if key.dtype != x.dtype:
+            raise ValueError(f"key must have the type of x: got {key.dtype} and {x.dtype}")
+        k_dtype = torch.float8_e4m3fn if k_idx.dtype == torch.float8_e4m3fn else torch.uint8
+        idx = csa_index_append(_rows(key, "key", (B, T, IDX_DIM), dev), *_strides(key),
+                               _arg(k_idx, "k_idx", k_dtype, (B, ncap, IDX_DIM), dev),
+                               _arg(k_idx_scale, "k_idx_scale", torch.float32, (B, ncap), dev), ncap)
+    rope_dim, theta = (0, 0.0) if rope_theta is None else (ROPE, rope_theta)
+    _check(load().csa_cache_append(cache, _fmt_of(cache), 1 if ring else 0, _rows(x, "x", (B, T, DIM), dev),
+                                   _DTYPES[x.dtype], *_strides(x),
+                                   _arg(first, "first", torch.int32, (B,), dev),
+                                   None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
+                                   pos_stride, _how(norm, weight, eps, rope_dim, theta, DIM, dev),
+                                   idx, _status(status, x.device), _stream(stream)), "csa_cache_append")
+
+
+def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = False, out=None, stream=None,
+                   status=None) -> torch.Tensor:
+    """The entries first[b] .. first[b] + count[b] (``count`` None: T of them) of
+    each sequence as BF16 latents [B, T, 512]; rows behind a sequence's count
+    are left as they were (zero in an ``out`` made here)."""
+    dev = _dev(first, "first")
+    B = first.shape[0]
+    if out is None:
+        out = torch.zeros((B, T, DIM), dtype=torch.bfloat16, device=first.device)
+    _check(load().csa_cache_read(cache, _fmt_of(cache), 1 if ring else 0,
+                                 _arg(first, "first", torch.int32, (B,), dev),
+                                 None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
+                                 _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _status(status, first.device),
+                                 _stream(stream)), "csa_cache_read")
+    return out
+
+
+def _fmt_of(cache: csa_cache_desc) -> int:
+    return getattr(cache, "_fmt", FORMAT_FP8)
 
 
 def _hptr(t: torch.Tensor, name: str, dtype, shape):
@@ -455,7 +629,8 @@ def csa_decode_step_host(pipeline: int, B: int, T: int, h_q_idx, h_q_idx_scale, 
         _hptr(h_w_idx, "h_w_idx", torch.float32, (B, T, IDX_HEADS)),
         _hptr(h_q, "h_q", torch.bfloat16, (B, T, HEADS, DIM)), _hptr(h_q_pos, "h_q_pos", torch.int32, (B, T)),
         _ptr(k_idx, "k_idx", u8, (B, Ncap, IDX_DIM)), _ptr(k_idx_scale, "k_idx_scale", torch.float32, (B, Ncap)),
-        _ptr(sink, "sink", torch.float32, (HEADS,)), float(softmax_scale), comp,
+        _ptr(sink, "sink", torch.float32, (HEADS,)), float(softmax_scale),
+        _format(comp, FORMAT_FP8, "csa_decode_step_host"),
         _ptr(swa_ring, "swa_ring", torch.uint8, (B, R, RECORD_BYTES)), R, int(W),
         _ptr(n_comp, "n_comp", torch.int32, (B,)), Ncap, int(m), int(k),
         _hptr(h_out, "h_out", torch.bfloat16, (B, T, HEADS, DIM)), _hptr(h_lse, "h_lse", torch.float32, (B, T, HEADS)),

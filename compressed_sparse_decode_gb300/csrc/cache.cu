@@ -1,0 +1,385 @@
+// cache.cu -- writing latents into a cache and reading them back
+// (csa_cache_append, csa_cache_read): FP8 and 4-bit records, contiguous, paged
+// or ring.
+//
+// One warp a token; lane l holds dims [16 l, 16 l + 16): lanes 0..27 the nope
+// dims (one 4-bit scale block each, eight lanes an FP8 block), lanes 28..31
+// the rope dims. So the 4-bit block maximum needs no shuffle, and a record is
+// written with one vector store a lane.
+#include <cuda_fp4.h>
+
+#include "rows.cuh"
+
+namespace csa {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kNopeLanes = kNope / 16;  // 28
+constexpr uint32_t kAll = 0xffffffffu;
+
+// Which entry token t of sequence b is.
+struct Span {
+    CacheView cache;
+    int ring;
+    const int32_t *first, *count;
+    int B, T;
+};
+
+struct Slot {
+    bool kept;        // the token counts and its entry is inside the cache
+    int64_t entry;    // first + t
+    int64_t record;
+};
+
+// Warp-uniform. Reports what lies outside the cache.
+__device__ __forceinline__ Slot find_slot(const Span &s, int b, int t, int *err, bool reporter) {
+    Slot o;
+    o.kept = false;
+    o.entry = 0;
+    o.record = 0;
+    int n = s.count ? __ldg(s.count + b) : s.T;
+    const int first = __ldg(s.first + b);
+    if (n < 0 || n > s.T) {
+        if (reporter && t == 0) report_error(err, CSA_ERR_BAD_INDEX);
+        n = n < 0 ? 0 : s.T;
+    }
+    if (t >= n) return o;
+    o.entry = (int64_t)first + t;
+    int64_t slot = o.entry;
+    if (s.ring) {
+        if (t < n - s.cache.seq_capacity) return o;  // overwritten by a later token of this call
+        if (first >= 0) slot = o.entry % s.cache.seq_capacity;
+    }
+    const int64_t rec = first >= 0 && slot < s.cache.seq_capacity ? record_index(s.cache, b, (int)slot) : -1;
+    if (rec < 0) {
+        if (reporter) report_error(err, CSA_ERR_BAD_INDEX);
+        return o;
+    }
+    o.kept = true;
+    o.record = rec;
+    return o;
+}
+
+struct AppendParams {
+    Span span;
+    const void *x;
+    int64_t seq_stride, token_stride;
+    int pos_stride;
+    RowOps ops;
+    uint8_t *base;
+    const void *key;  // indexer keys, or null
+    int64_t key_seq_stride, key_token_stride;
+    uint8_t *k_idx;
+    float *k_idx_scale;
+    int idx_cap;
+    int *err;
+};
+
+// 16 values of a nope lane as E2M1 codes of unit s = sb * 2^E.
+__device__ __forceinline__ uint2 fp4_codes(const float (&f)[2][8], float s) {
+    uint32_t w[2];
+    const float inv = 1.f / s;
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        float q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = sticky_quotient(f[o][e], s, inv);
+        w[o] = e2m1x4(q[0], q[1], q[2], q[3]) | (e2m1x4(q[4], q[5], q[6], q[7]) << 16);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Exponent of a 4-bit record: the smallest E with amax <= 6 * 448 * 2^E =
+// 1.3125 * 2^(E + 11), from the bits of amax; at least kFp4MinExponent.
+__device__ __forceinline__ int fp4_exponent(uint32_t amax) {
+    const int ex = (int)(amax >> 23) - 127;
+    const int e = ex - 11 + ((amax & 0x7FFFFFu) > 0x280000u ? 1 : 0);  // 0.3125 * 2^23
+    return amax ? max(e, kFp4MinExponent) : 0;
+}
+
+template <int DT, int FMT, bool KEYS>
+__global__ void __launch_bounds__(kThreads)
+append_kernel(const __grid_constant__ AppendParams P) {
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (token >= P.span.B * P.span.T) return;
+    const int b = token / P.span.T, t = token - b * P.span.T;
+    const Slot slot = find_slot(P.span, b, t, P.err, lane == 0);
+    if (!slot.kept) return;
+    const int64_t p = slot.entry * P.pos_stride;
+
+    Octet<DT> in[2], kin;
+    const int64_t at = b * P.seq_stride + t * P.token_stride + 16 * lane;
+    in[0].load(P.x, at);
+    in[1].load(P.x, at + 8);
+    const bool key_lane = KEYS && lane < kIdxDim / 8;  // 16 lanes hold the key's octets
+    if (key_lane) kin.load(P.key, b * P.key_seq_stride + t * P.key_token_stride + 8 * lane);
+    const bool turn = P.ops.rope_dim > 0;
+    float2 own = make_float2(1.f, 0.f);  // lane i: pair i
+    if (turn) own = turn_cos_sin(p, P.ops.turn[lane]);
+
+    float f[2][8];
+    in[0].floats(f[0]);
+    in[1].floats(f[1]);
+    if (P.ops.norm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(f[o][e], f[o][e], sum);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        const float inv_rms = rsqrtf(sum / kDim + P.ops.eps);
+        scale_octet(f[0], inv_rms, P.ops.weight, 16 * lane);
+        scale_octet(f[1], inv_rms, P.ops.weight, 16 * lane + 8);
+    }
+    const bool rope_lane = lane >= kNopeLanes;
+    if (turn) {
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            float2 cs[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int pair = ((lane - kNopeLanes) & 3) * 8 + 4 * o + e;
+                cs[e].x = __shfl_sync(kAll, own.x, pair);
+                cs[e].y = __shfl_sync(kAll, own.y, pair);
+            }
+            if (rope_lane) turn_octet(f[o], cs);
+        }
+    }
+    const uint32_t amax = rope_lane ? 0u : amax_bits(f[1], amax_bits(f[0]));
+    uint8_t *rec = P.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+    if (FMT == CSA_FORMAT_FP4) {
+        const uint32_t top = __reduce_max_sync(kAll, amax);
+        const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
+        const int E = bad ? 128 : fp4_exponent(top);
+        if (rope_lane) {
+            uint4 *dst = reinterpret_cast<uint4 *>(rec + kFp4RopeOffset + 32 * (lane - kNopeLanes));
+            dst[0] = pack_bf16_octet(f[0]);
+            dst[1] = pack_bf16_octet(f[1]);
+            if (lane == kNopeLanes)
+                *reinterpret_cast<uint32_t *>(rec + kFp4PowerOffset) = (uint32_t)(E + 127);
+        } else {
+            // block scale: e4m3(amax / 6 * 2^-E), its halfway cases decided exactly
+            const float ratio = sticky_quotient(__uint_as_float(amax), 6.f, 1.f / 6.f) *
+                                __uint_as_float((uint32_t)(127 - E) << 23);
+            const uint32_t sb = bad ? 0u : e4m3x4(ratio, 0.f, 0.f, 0.f) & 0xFFu;
+            uint2 codes = make_uint2(0u, 0u);
+            if (sb) {
+                const float unit = e4m3x2_to_float2((uint16_t)sb).x * __uint_as_float((uint32_t)(E + 127) << 23);
+                codes = fp4_codes(f, unit);
+            }
+            *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
+            rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
+        }
+    } else {
+        uint32_t top = amax;  // over the eight lanes of a 128-dim block (rope lanes hold 0)
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+        if (rope_lane) {
+            uint4 *dst = reinterpret_cast<uint4 *>(rec + kRopeOffset + 32 * (lane - kNopeLanes));
+            dst[0] = pack_bf16_octet(f[0]);
+            dst[1] = pack_bf16_octet(f[1]);
+        } else {
+            const float s = e4m3_scale(top), inv = 1.f / s;
+            float q[2][8];
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[o][e] = sticky_quotient(f[o][e], s, inv);
+            *reinterpret_cast<uint4 *>(rec + 16 * lane) =
+                make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
+                           e4m3x4(q[1][0], q[1][1], q[1][2], q[1][3]), e4m3x4(q[1][4], q[1][5], q[1][6], q[1][7]));
+            if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + kScaleOffset + 4 * (lane >> 3)) = s;
+        }
+    }
+    if (KEYS) {
+        float g[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = 0.f;
+        if (key_lane) kin.floats(g);
+        if (turn) {
+            // octets 8..15 are the key's rope dims: pairs 4 (lane - 8) ..
+            float2 cs[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int pair = ((lane - 8) & 7) * 4 + e;
+                cs[e].x = __shfl_sync(kAll, own.x, pair);
+                cs[e].y = __shfl_sync(kAll, own.y, pair);
+            }
+            if (key_lane && lane >= 8) turn_octet(g, cs);
+        }
+        const uint32_t top = __reduce_max_sync(kAll, amax_bits(g));
+        if (slot.entry >= P.idx_cap) {
+            if (lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+        } else if (key_lane) {
+            const float s = e4m3_scale(top), inv = 1.f / s;
+            const int64_t row = (int64_t)b * P.idx_cap + slot.entry;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = quotient(g[e], s, inv);
+            *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
+                make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
+            if (lane == 0) P.k_idx_scale[row] = s;
+        }
+    }
+}
+
+struct ReadParams {
+    Span span;
+    uint4 *out;
+    int *err;
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads)
+read_kernel(const __grid_constant__ ReadParams P) {
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (token >= P.span.B * P.span.T) return;
+    const int b = token / P.span.T, t = token - b * P.span.T;
+    const Slot slot = find_slot(P.span, b, t, P.err, lane == 0);
+    if (!slot.kept) return;
+    const uint8_t *rec = P.span.cache.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+    uint4 lo, hi;
+    if (lane >= kNopeLanes) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(rec + (FMT == CSA_FORMAT_FP4 ? kFp4RopeOffset : kRopeOffset) +
+                                                           32 * (lane - kNopeLanes));
+        lo = src[0];
+        hi = src[1];
+    } else {
+        float f[2][8];
+        if (FMT == CSA_FORMAT_FP4) {
+            const uint2 c = *reinterpret_cast<const uint2 *>(rec + 8 * lane);
+            const float s = e4m3x2_to_float2((uint16_t)rec[kFp4ScaleOffset + lane]).x * fp4_power(rec[kFp4PowerOffset]);
+            const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+            for (int o = 0; o < 2; ++o)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[o] >> (8 * e)), __NV_E2M1);
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                    f[o][2 * e] = v.x * s;
+                    f[o][2 * e + 1] = v.y * s;
+                }
+        } else {
+            const uint4 c = *reinterpret_cast<const uint4 *>(rec + 16 * lane);
+            const float s = *reinterpret_cast<const float *>(rec + kScaleOffset + 4 * (lane >> 3));
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = e4m3x2_to_float2((uint16_t)(w[i] & 0xFFFFu));
+                const float2 v = e4m3x2_to_float2((uint16_t)(w[i] >> 16));
+                f[i >> 1][4 * (i & 1)] = u.x * s;
+                f[i >> 1][4 * (i & 1) + 1] = u.y * s;
+                f[i >> 1][4 * (i & 1) + 2] = v.x * s;
+                f[i >> 1][4 * (i & 1) + 3] = v.y * s;
+            }
+        }
+        lo = pack_bf16_octet(f[0]);
+        hi = pack_bf16_octet(f[1]);
+    }
+    uint4 *dst = P.out + (int64_t)token * (kDim / 8) + 2 * lane;
+    dst[0] = lo;
+    dst[1] = hi;
+}
+
+bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// The checks that both calls share, and their span.
+csa_status_t make_span(const csa_cache_desc &cache, csa_format_t fmt, int ring, const int32_t *first,
+                       const int32_t *count, int B, int T, const int32_t *status, Span *s) {
+    if (fmt != CSA_FORMAT_FP8 && fmt != CSA_FORMAT_FP4) return CSA_ERR_INVALID_ARG;
+    if (!first || misaligned(first) || misaligned(count) || B < 1 || T < 1 || !valid_cache(cache, B) ||
+        !valid_status_word(status))
+        return CSA_ERR_INVALID_ARG;
+    if ((int64_t)B * T > (1 << 24)) return CSA_ERR_UNSUPPORTED;
+    s->cache = make_view(cache);
+    s->ring = ring ? 1 : 0;
+    s->first = first;
+    s->count = count;
+    s->B = B;
+    s->T = T;
+    return CSA_OK;
+}
+
+template <int DT, int FMT>
+cudaError_t launch_append(const AppendParams &P, PdlLaunch &l) {
+    return P.key ? cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, true>, P)
+                 : cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, false>, P);
+}
+
+template <int DT>
+cudaError_t launch_append(const AppendParams &P, csa_format_t fmt, PdlLaunch &l) {
+    return fmt == CSA_FORMAT_FP4 ? launch_append<DT, CSA_FORMAT_FP4>(P, l) : launch_append<DT, CSA_FORMAT_FP8>(P, l);
+}
+
+}  // namespace
+
+}  // namespace csa
+
+extern "C" CSA_API csa_status_t csa_cache_append(csa_cache_desc cache, csa_format_t fmt, int ring, const void *x,
+                                                 csa_dtype_t x_dtype, int64_t x_seq_stride, int64_t x_token_stride,
+                                                 const int32_t *first, const int32_t *count, int B, int T,
+                                                 int pos_stride, const csa_norm_rope *how, const csa_index_append *idx,
+                                                 int32_t *status, cudaStream_t stream) {
+    using namespace csa;
+    AppendParams P;
+    const csa_status_t a = make_span(cache, fmt, ring, first, count, B, T, status, &P.span);
+    if (a != CSA_OK) return a;
+    if (x_dtype != CSA_BF16 && x_dtype != CSA_FP16 && x_dtype != CSA_FP32) return CSA_ERR_INVALID_ARG;
+    const int64_t per16 = x_dtype == CSA_FP32 ? 4 : 8;
+    if (!x || misaligned(x) || x_seq_stride < 0 || x_token_stride < 0 || x_seq_stride % per16 ||
+        x_token_stride % per16 || pos_stride < 1 || pos_stride > 65536)
+        return CSA_ERR_INVALID_ARG;
+    if (!make_row_ops(how, kDim, &P.ops) || (P.ops.rope_dim != 0 && P.ops.rope_dim != kRope)) return CSA_ERR_INVALID_ARG;
+    P.key = nullptr;
+    P.key_seq_stride = P.key_token_stride = 0;
+    P.k_idx = nullptr;
+    P.k_idx_scale = nullptr;
+    P.idx_cap = 0;
+    if (idx) {
+        if (ring || !idx->key || !idx->k_idx || !idx->k_idx_scale || misaligned(idx->key) || misaligned(idx->k_idx) ||
+            misaligned(idx->k_idx_scale) || idx->Ncap < 1 || idx->seq_stride < 0 || idx->token_stride < 0 ||
+            idx->seq_stride % per16 || idx->token_stride % per16)
+            return CSA_ERR_INVALID_ARG;
+        P.key = idx->key;
+        P.key_seq_stride = idx->seq_stride;
+        P.key_token_stride = idx->token_stride;
+        P.k_idx = idx->k_idx;
+        P.k_idx_scale = idx->k_idx_scale;
+        P.idx_cap = idx->Ncap;
+    }
+    P.x = x;
+    P.seq_stride = x_seq_stride;
+    P.token_stride = x_token_stride;
+    P.pos_stride = pos_stride;
+    P.base = static_cast<uint8_t *>(const_cast<void *>(cache.base));
+    P.err = status;
+    PdlLaunch l(dim3((B * T + kWarps - 1) / kWarps), dim3(kThreads), stream);
+    count_launch();
+    const cudaError_t e = x_dtype == CSA_BF16   ? launch_append<CSA_BF16>(P, fmt, l)
+                          : x_dtype == CSA_FP16 ? launch_append<CSA_FP16>(P, fmt, l)
+                                                : launch_append<CSA_FP32>(P, fmt, l);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+extern "C" CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_t fmt, int ring, const int32_t *first,
+                                               const int32_t *count, int B, int T, void *out, int32_t *status,
+                                               cudaStream_t stream) {
+    using namespace csa;
+    ReadParams P;
+    const csa_status_t a = make_span(cache, fmt, ring, first, count, B, T, status, &P.span);
+    if (a != CSA_OK) return a;
+    if (!out || misaligned(out)) return CSA_ERR_INVALID_ARG;
+    P.out = static_cast<uint4 *>(out);
+    P.err = status;
+    PdlLaunch l(dim3((B * T + kWarps - 1) / kWarps), dim3(kThreads), stream);
+    count_launch();
+    const cudaError_t e = fmt == CSA_FORMAT_FP4 ? cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP4>, P)
+                                                : cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP8>, P);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}

@@ -105,6 +105,24 @@ typedef struct {
     int32_t seq_capacity;       /* logical entries per sequence (Ncap) */
 } csa_cache_desc;
 
+/* Element types of tensors that a call reads in more than one type. */
+typedef enum { CSA_BF16 = 0, CSA_FP16 = 1, CSA_FP32 = 2 } csa_dtype_t;
+
+/* Formats of latent records. CSA_FORMAT_FP8 is the record above; a 4-bit
+ * record, CSA_FP4_RECORD_BYTES, is
+ *   bytes [0,224)   nope dims, E2M1, dim 2i in the low nibble of byte i
+ *   bytes [224,352) rope dims, BF16
+ *   bytes [352,380) 28 E4M3 block scales, scale i covers nope dims [16i, 16i+16)
+ *   byte  380       power-of-two multiplier of the record, 2^(byte - 127)
+ *                   (255: infinite, see csa_cache_append)
+ *   bytes [381,384) zero
+ * and nope dim d stands for e2m1(code d) * e4m3(scale d/16) * 2^(byte-127).
+ * The product of an E2M1 and an E4M3 value has at most 6 significant bits and
+ * the power of two changes none of them, so every 4-bit latent is a BF16
+ * value exactly: the tensor cores read it without a further rounding. */
+typedef enum { CSA_FORMAT_FP8 = 0, CSA_FORMAT_FP4 = 1 } csa_format_t;
+#define CSA_FP4_RECORD_BYTES 384
+
 typedef enum {
     CSA_OP_INDEXER = 0,
     CSA_OP_TOPK = 1,
@@ -310,6 +328,120 @@ CSA_API csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx
                                         float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                         const csa_attention_epilogue *epilogue, void *workspace,
                                         size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/* Normalisation and rotation of one head (csa_head_norm_rope,
+ * csa_head_norm_rope_e4m3, csa_cache_append). With x the D values of a head:
+ *   norm       nonzero: y_d = x_d * (sum_d x_d^2 / D + eps)^(-1/2) * weight[d]
+ *              zero: y = x (weight must then be NULL)
+ *   eps        >= 0, finite; read only with norm
+ *   weight     device fp32 [D], 16-byte aligned, or NULL for all ones
+ *   rope_dim   the last rope_dim values are turned as pairs i = (D - rope_dim +
+ *              2i, D - rope_dim + 2i + 1) by a = p * rope_theta^(-2i/rope_dim)
+ *              radians, p the token's position:
+ *                x' = x cos a - y sin a,   y' = x sin a + y cos a
+ *              (the rotation that csa_attention_epilogue turns back);
+ *              0: no rotation
+ *   rope_theta > 1, finite; read only with rope_dim > 0
+ * Sums and the rotation are fp32, the angle is reduced to one turn in 64-bit
+ * fixed point (positions far beyond 2^24 keep it), and the result is rounded
+ * once, to the output's type. */
+typedef struct {
+    int32_t norm;
+    float eps;
+    const float *weight;
+    int32_t rope_dim;
+    float rope_theta;
+} csa_norm_rope;
+
+/* RMS norm of every head and the position rotation in one pass over the
+ * heads: the attention's queries (H = 128, D = 512), or its latents before
+ * they are cached (H = 1).
+ *   x     element (b, t, h, d) at x[b*x_seq_stride + t*x_token_stride +
+ *         h*x_head_stride + d] of type x_dtype (strides in elements, >= 0;
+ *         base and strides multiples of 16 bytes): a slice of a wider
+ *         projection needs no copy
+ *   pos   [B,T] int32; a token with pos < 0 is padding: it is not read and its
+ *         rows of the output are left as they were
+ *   out   [B,T,H,D] BF16, dense. It may be x itself when x is dense BF16; any
+ *         other overlap with x is not allowed.
+ * Requires B, T, H >= 1, B*T <= 2^24, B*T*H < 2^31, D a multiple of 8 up to
+ * 512 and rope_dim a multiple of 8 up to min(D, 256). The status word is
+ * accepted as by every compute call; nothing is recorded in it. */
+CSA_API csa_status_t csa_head_norm_rope(const void *x, csa_dtype_t x_dtype, int64_t x_seq_stride,
+                                        int64_t x_token_stride, int64_t x_head_stride, const int32_t *pos, int B,
+                                        int T, int H, int D, const csa_norm_rope *how, void *out, int32_t *status,
+                                        cudaStream_t stream);
+
+/* The same pass with E4M3 output, the form that csa_indexer_logits reads its
+ * queries in (H = 64, D = 128): scale[b,t,h] = amax_d |y_d| / 448 (1 when all
+ * are zero), codes[b,t,h,d] = e4m3(y_d / scale).
+ *   codes [B,T,H,D] bytes, scale [B,T,H] fp32; neither may overlap x. */
+CSA_API csa_status_t csa_head_norm_rope_e4m3(const void *x, csa_dtype_t x_dtype, int64_t x_seq_stride,
+                                             int64_t x_token_stride, int64_t x_head_stride, const int32_t *pos,
+                                             int B, int T, int H, int D, const csa_norm_rope *how, uint8_t *codes,
+                                             float *scale, int32_t *status, cudaStream_t stream);
+
+/* Indexer keys of the entries that csa_cache_append writes: 128 values each,
+ * rotated like the latent (the last 64 of them, at the same position; not
+ * normalised) and stored as csa_indexer_logits reads them.
+ *   key         element (b, t, d) at key[b*seq_stride + t*token_stride + d], of
+ *               the latents' type (same rules for strides and alignment)
+ *   k_idx       [B,Ncap,128] e4m3 codes, k_idx_scale [B,Ncap] fp32
+ *               (amax / 448, 1 when all are zero)
+ * Entries at or past Ncap are not stored (CSA_ERR_BAD_INDEX). */
+typedef struct {
+    const void *key;
+    int64_t seq_stride, token_stride;
+    uint8_t *k_idx;
+    float *k_idx_scale;
+    int32_t Ncap;
+} csa_index_append;
+
+/* Appends latents to a cache, normalised and rotated on the way: token t of
+ * sequence b (t < count[b]) becomes entry e = first[b] + t of its sequence,
+ * at position p = e * pos_stride (1 for tokens; tokens per entry for
+ * compressed entries).
+ *   cache  the records, contiguous or paged, of format fmt; base is written
+ *   ring   nonzero: the record is entry e mod seq_capacity (the sliding
+ *          window's ring, a contiguous cache with seq_stride =
+ *          seq_capacity = R), and of more than seq_capacity tokens only the last
+ *          seq_capacity are kept
+ *   x      element (b, t, d), d < 512, at x[b*x_seq_stride + t*x_token_stride + d]
+ *          of type x_dtype (strides in elements; base and strides multiples
+ *          of 16 bytes)
+ *   first  [B] int32, >= 0
+ *   count  [B] int32 in [0, T], or NULL for T tokens of every sequence
+ *   how    D = 512; rope_dim 64 or 0
+ *   idx    NULL, or the entries' indexer keys, stored by the same launch
+ *          (not with ring)
+ * Records: rope dims are rounded to BF16. FP8: multiplier = amax / 448 of each
+ * 128-dim block (1 when it is all zero), code = e4m3(y / multiplier). 4 bits:
+ * with amax over the 448 nope dims, E = the smallest whole number with amax <=
+ * 6 * 448 * 2^E (at least -111; 0 when all are zero), the block scale s =
+ * e4m3(max |y| of the block / 6 * 2^-E), code = e2m1(y / (s * 2^E)), ties to
+ * even in both, codes 0 where s is 0. These quotients are decided as if
+ * computed exactly. An infinite or NaN nope dim makes its FP8 block or its
+ * 4-bit record read back as NaN in every nope dim.
+ * An entry outside the cache is not stored (CSA_ERR_BAD_INDEX, also for
+ * first < 0 or a count outside [0, T], which is then clamped). Every other
+ * record is left as it was. Sequences of one call must not share a page that
+ * it writes. Requires B, T >= 1, B*T <= 2^24, 1 <= pos_stride <= 65536. */
+CSA_API csa_status_t csa_cache_append(csa_cache_desc cache, csa_format_t fmt, int ring, const void *x,
+                                      csa_dtype_t x_dtype, int64_t x_seq_stride, int64_t x_token_stride,
+                                      const int32_t *first, const int32_t *count, int B, int T, int pos_stride,
+                                      const csa_norm_rope *how, const csa_index_append *idx, int32_t *status,
+                                      cudaStream_t stream);
+
+/* Reads entries back as BF16 latents: out[b,t,0..512) = the values of entry
+ * first[b] + t of sequence b for t < count[b] (with ring: of entry
+ * (first[b] + t) mod seq_capacity, for the last seq_capacity of these t). FP8
+ * values are rounded to BF16 (code x multiplier), 4-bit values are exact. Rows
+ * of out that no entry belongs to, or whose entry lies outside the cache
+ * (CSA_ERR_BAD_INDEX), are left as they were. Arguments as in csa_cache_append;
+ * out [B,T,512] BF16. */
+CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_t fmt, int ring, const int32_t *first,
+                                    const int32_t *count, int B, int T, void *out, int32_t *status,
+                                    cudaStream_t stream);
 
 /* Host-I/O decode pipeline (the pages have no counterpart; it serves callers
  * whose query-side inputs arrive in, and whose results go back to, host
