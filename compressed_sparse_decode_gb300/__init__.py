@@ -36,7 +36,8 @@ EXPORTED = ["csa_workspace_bytes", "csa_indexer_logits", "csa_topk", "csa_gather
             "csa_sink_attention_decode_noalloc", "csa_pipeline_staging_bytes", "csa_pipeline_create",
             "csa_decode_step_host", "csa_pipeline_wait", "csa_pipeline_sync", "csa_pipeline_destroy",
             "csa_sink_attention_decode_ex", "hca_sink_attention_decode_ex", "csa_decode_step_ex",
-            "csa_head_norm_rope", "csa_head_norm_rope_e4m3", "csa_cache_append", "csa_cache_read"]
+            "csa_head_norm_rope", "csa_head_norm_rope_e4m3", "csa_cache_append", "csa_cache_read",
+            "csa_sink_attention_decode_fp4", "hca_sink_attention_decode_fp4", "csa_decode_step_fp4"]
 PIPELINE_MAX_DEPTH = 4
 
 
@@ -146,6 +147,9 @@ def load(path: str | None = None):
         lib.csa_cache_append.restype = st
         lib.csa_cache_read.argtypes = [csa_cache_desc, i32, i32, P, P, i32, i32, P, P, P]
         lib.csa_cache_read.restype = st
+        for name in ("csa_sink_attention_decode", "hca_sink_attention_decode", "csa_decode_step"):
+            fp4, ex = getattr(lib, name + "_fp4"), getattr(lib, name + "_ex")
+            fp4.argtypes, fp4.restype = ex.argtypes, st
         _lib = lib
         return lib
 
@@ -582,6 +586,101 @@ def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = Fal
                                  _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _status(status, first.device),
                                  _stream(stream)), "csa_cache_read")
     return out
+
+
+def csa_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache_desc, swa_ring, W: int, topk_idx,
+                                  topk_cnt, q_pos, out=None, lse=None, ws=None, stream=None, status=None,
+                                  inverse_rope: bool = False, rope_theta: float = 10000.0, fp4_out: bool = False,
+                                  out_fp4=None, out_fp4_scale=None):
+    """csa_sink_attention_decode over caches of 4-bit records (``comp`` made with
+    ``fmt=FORMAT_FP4``, ``swa_ring`` [B, R, 384]). Returns (out, lse); with
+    fp4_out, ((out_fp4, out_fp4_scale), lse)."""
+    B, T, k = topk_idx.shape
+    R = swa_ring.shape[1]
+    dev = _dev(q, "q")
+    epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if out is None and not fp4_out:
+        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(OP_ATTENTION, B, T, comp.seq_capacity, k, q.device)
+    i32, f32 = torch.int32, torch.float32
+    _check(load().csa_sink_attention_decode_fp4(
+        _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _format(comp, FORMAT_FP4, "csa_sink_attention_decode_fp4"),
+        _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
+        _arg(topk_idx, "topk_idx", i32, (B, T, k), dev), _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
+        _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, k,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)),
+        "csa_sink_attention_decode_fp4")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def hca_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache_desc, n_comp, swa_ring, W: int,
+                                  q_pos, m_hca: int = 128, out=None, lse=None, ws=None, stream=None, status=None,
+                                  inverse_rope: bool = False, rope_theta: float = 10000.0, fp4_out: bool = False,
+                                  out_fp4=None, out_fp4_scale=None):
+    """hca_sink_attention_decode over caches of 4-bit records."""
+    B, T = q_pos.shape
+    R = swa_ring.shape[1]
+    dev = _dev(q, "q")
+    epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if out is None and not fp4_out:
+        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(OP_HCA_ATTENTION, B, T, comp.seq_capacity, 0, q.device)
+    i32, f32 = torch.int32, torch.float32
+    _check(load().hca_sink_attention_decode_fp4(
+        _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _format(comp, FORMAT_FP4, "hca_sink_attention_decode_fp4"), _arg(n_comp, "n_comp", i32, (B,), dev),
+        _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
+        _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, m_hca,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)),
+        "hca_sink_attention_decode_fp4")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale: float,
+                        comp: csa_cache_desc, swa_ring, W: int, q_pos, n_comp, m: int, k: int, out=None, lse=None,
+                        topk_idx=None, topk_cnt=None, ws=None, stream=None, status=None, inverse_rope: bool = False,
+                        rope_theta: float = 10000.0, fp4_out: bool = False, out_fp4=None, out_fp4_scale=None):
+    """csa_decode_step over caches of 4-bit records (the indexer keys stay FP8)."""
+    B, T = q_pos.shape
+    Ncap = k_idx.shape[1]
+    R = swa_ring.shape[1]
+    dev = _dev(q, "q")
+    epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if out is None and not fp4_out:
+        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(OP_DECODE_STEP, B, T, Ncap, k, q.device)
+    u8, i32, f32 = (torch.uint8, torch.float8_e4m3fn), torch.int32, torch.float32
+    _check(load().csa_decode_step_fp4(
+        _ptr(q_idx, "q_idx", u8, (B, T, IDX_HEADS, IDX_DIM)),
+        _arg(q_idx_scale, "q_idx_scale", f32, (B, T, IDX_HEADS), dev), _arg(w_idx, "w_idx", f32, (B, T, IDX_HEADS), dev),
+        _ptr(k_idx, "k_idx", u8, (B, Ncap, IDX_DIM)), _arg(k_idx_scale, "k_idx_scale", f32, (B, Ncap), dev),
+        _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _format(comp, FORMAT_FP4, "csa_decode_step_fp4"),
+        _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
+        _arg(q_pos, "q_pos", i32, (B, T), dev), _arg(n_comp, "n_comp", i32, (B,), dev), B, T, Ncap, m, k,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev),
+        None if topk_idx is None else _arg(topk_idx, "topk_idx", i32, (B, T, k), dev),
+        None if topk_cnt is None else _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
+        epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)), "csa_decode_step_fp4")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def _ws(ws, dev: int):
+    """(pointer, bytes) of a workspace; (None, 0) for none."""
+    return (None, 0) if ws is None else (_arg(ws, "workspace", torch.uint8, ws.shape, dev), ws.numel())
 
 
 def _fmt_of(cache: csa_cache_desc) -> int:

@@ -24,6 +24,10 @@ cudaError_t launch_attention(const void *, const float *, float, const csa_cache
                              const int32_t *, const int32_t *, const int32_t *, int, const int32_t *, int, int, int,
                              bool, void *, float *, const csa_attention_epilogue *, void *, size_t, int *,
                              cudaStream_t);
+cudaError_t launch_attention_fp4(const void *, const float *, float, const csa_cache_desc &, const void *, int, int,
+                                 const int32_t *, const int32_t *, const int32_t *, int, const int32_t *, int, int,
+                                 int, bool, void *, float *, const csa_attention_epilogue *, void *, size_t, int *,
+                                 cudaStream_t);
 }  // namespace csa
 
 namespace csa {
@@ -243,12 +247,16 @@ const void *checked_out(const csa_attention_epilogue *epi, const void *out) {
 }
 }  // namespace
 
-csa_status_t csa_sink_attention_decode_ex(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
-                                          const void *swa_ring, int R, int W, const int32_t *topk_idx,
-                                          const int32_t *topk_cnt, const int32_t *q_pos, int B, int T, int k,
-                                          void *out, float *lse, const csa_attention_epilogue *epilogue,
-                                          void *workspace, size_t workspace_bytes, int32_t *status,
-                                          cudaStream_t stream) {
+namespace {
+// The attention entry points' bodies; `launch` is the launcher of the cache's
+// record format (same arguments, checks and workspace for both).
+using AttentionLaunch = decltype(&launch_attention);
+
+csa_status_t sink_attention(AttentionLaunch launch, const void *q, const float *sink, float softmax_scale,
+                            const csa_cache_desc &comp, const void *swa_ring, int R, int W, const int32_t *topk_idx,
+                            const int32_t *topk_cnt, const int32_t *q_pos, int B, int T, int k, void *out, float *lse,
+                            const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                            int32_t *status, cudaStream_t stream) {
     csa_status_t a = epilogue_status(epilogue, out);
     if (a != CSA_OK) return a;
     a = attention_arg_status(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B, T, k,
@@ -257,9 +265,49 @@ csa_status_t csa_sink_attention_decode_ex(const void *q, const float *sink, floa
     const size_t need = attention_workspace_bytes(B, T, k, W);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
         return CSA_ERR_WORKSPACE;
-    return cuda_status(launch_attention(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, nullptr, 1,
-                                        q_pos, B, T, k, false, out, lse, epilogue, workspace, workspace_bytes, status,
-                                        stream));
+    return cuda_status(launch(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, nullptr, 1, q_pos, B,
+                              T, k, false, out, lse, epilogue, workspace, workspace_bytes, status, stream));
+}
+
+csa_status_t hca_attention(AttentionLaunch launch, const void *q, const float *sink, float softmax_scale,
+                           const csa_cache_desc &comp, const int32_t *n_comp, const void *swa_ring, int R, int W,
+                           const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
+                           const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                           int32_t *status, cudaStream_t stream) {
+    const csa_status_t a = epilogue_status(epilogue, out);
+    if (a != CSA_OK) return a;
+    if (!q || !sink || !n_comp || !swa_ring || !q_pos || !lse) return CSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(swa_ring) || !valid_cache(comp, B) || !valid_status_word(status))
+        return CSA_ERR_INVALID_ARG;
+    if (!valid_dims(B, T) || W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || m_hca < 1 || !(softmax_scale > 0.f))
+        return CSA_ERR_INVALID_ARG;
+    const size_t need = attention_workspace_bytes(B, T, comp.seq_capacity, W);
+    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
+        return CSA_ERR_WORKSPACE;
+    return cuda_status(launch(q, sink, softmax_scale, comp, swa_ring, R, W, nullptr, nullptr, n_comp, m_hca, q_pos, B, T,
+                              comp.seq_capacity, true, out, lse, epilogue, workspace, workspace_bytes, status,
+                              stream));
+}
+}  // namespace
+
+csa_status_t csa_sink_attention_decode_ex(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
+                                          const void *swa_ring, int R, int W, const int32_t *topk_idx,
+                                          const int32_t *topk_cnt, const int32_t *q_pos, int B, int T, int k,
+                                          void *out, float *lse, const csa_attention_epilogue *epilogue,
+                                          void *workspace, size_t workspace_bytes, int32_t *status,
+                                          cudaStream_t stream) {
+    return sink_attention(launch_attention, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B,
+                          T, k, out, lse, epilogue, workspace, workspace_bytes, status, stream);
+}
+
+csa_status_t csa_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
+                                           const void *swa_ring, int R, int W, const int32_t *topk_idx,
+                                           const int32_t *topk_cnt, const int32_t *q_pos, int B, int T, int k,
+                                           void *out, float *lse, const csa_attention_epilogue *epilogue,
+                                           void *workspace, size_t workspace_bytes, int32_t *status,
+                                           cudaStream_t stream) {
+    return sink_attention(launch_attention_fp4, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt,
+                          q_pos, B, T, k, out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
 csa_status_t csa_sink_attention_decode(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
@@ -276,19 +324,17 @@ csa_status_t hca_sink_attention_decode_ex(const void *q, const float *sink, floa
                                           const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
                                           const csa_attention_epilogue *epilogue, void *workspace,
                                           size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
-    const csa_status_t a = epilogue_status(epilogue, out);
-    if (a != CSA_OK) return a;
-    if (!q || !sink || !n_comp || !swa_ring || !q_pos || !lse) return CSA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(swa_ring) || !valid_cache(comp, B) || !valid_status_word(status))
-        return CSA_ERR_INVALID_ARG;
-    if (!valid_dims(B, T) || W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || m_hca < 1 || !(softmax_scale > 0.f))
-        return CSA_ERR_INVALID_ARG;
-    const size_t need = attention_workspace_bytes(B, T, comp.seq_capacity, W);
-    if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
-        return CSA_ERR_WORKSPACE;
-    return cuda_status(launch_attention(q, sink, softmax_scale, comp, swa_ring, R, W, nullptr, nullptr, n_comp, m_hca,
-                                        q_pos, B, T, comp.seq_capacity, true, out, lse, epilogue, workspace,
-                                        workspace_bytes, status, stream));
+    return hca_attention(launch_attention, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T, m_hca,
+                         out, lse, epilogue, workspace, workspace_bytes, status, stream);
+}
+
+csa_status_t hca_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
+                                           const int32_t *n_comp, const void *swa_ring, int R, int W,
+                                           const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
+                                           const csa_attention_epilogue *epilogue, void *workspace,
+                                           size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
+    return hca_attention(launch_attention_fp4, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T,
+                         m_hca, out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
 csa_status_t hca_sink_attention_decode(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
@@ -300,13 +346,14 @@ csa_status_t hca_sink_attention_decode(const void *q, const float *sink, float s
                                         lse, nullptr, workspace, workspace_bytes, status, stream);
 }
 
-csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
-                                const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
-                                float softmax_scale, csa_cache_desc comp, const void *swa_ring, int R, int W,
-                                const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
-                                void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
-                                const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
-                                int32_t *status, cudaStream_t stream) {
+namespace {
+csa_status_t decode_step(AttentionLaunch launch, const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                         const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
+                         float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R, int W,
+                         const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
+                         void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
+                         const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                         int32_t *status, cudaStream_t stream) {
     // every argument of the three calls is checked before the first launch
     csa_status_t a = epilogue_status(epilogue, out);
     if (a != CSA_OK) return a;
@@ -330,8 +377,33 @@ csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, 
     if (s != CSA_OK) return s;
     s = csa_topk(logits, q_pos, n_comp, B, T, Ncap, m, k, idx, cnt, tk_ws, tk_bytes, status, stream);
     if (s != CSA_OK) return s;
-    return csa_sink_attention_decode_ex(q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out,
-                                        lse, epilogue, at_bytes ? ws : nullptr, at_bytes, status, stream);
+    return sink_attention(launch, q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out, lse,
+                          epilogue, at_bytes ? ws : nullptr, at_bytes, status, stream);
+}
+}  // namespace
+
+csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                                const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
+                                float softmax_scale, csa_cache_desc comp, const void *swa_ring, int R, int W,
+                                const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
+                                void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
+                                const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                                int32_t *status, cudaStream_t stream) {
+    return decode_step(launch_attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+                       swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
+                       workspace, workspace_bytes, status, stream);
+}
+
+csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                                 const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
+                                 float softmax_scale, csa_cache_desc comp, const void *swa_ring, int R, int W,
+                                 const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
+                                 void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
+                                 const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                                 int32_t *status, cudaStream_t stream) {
+    return decode_step(launch_attention_fp4, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+                       swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
+                       workspace, workspace_bytes, status, stream);
 }
 
 csa_status_t csa_decode_step(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,

@@ -443,6 +443,34 @@ CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_t fmt, int 
                                     const int32_t *count, int B, int T, void *out, int32_t *status,
                                     cudaStream_t stream);
 
+/* The sink-merged attention over caches of 4-bit records: formulas, arguments,
+ * output epilogue, workspace (csa_workspace_bytes of CSA_OP_ATTENTION,
+ * CSA_OP_HCA_ATTENTION and CSA_OP_DECODE_STEP) and error behaviour of
+ * csa_sink_attention_decode_ex, hca_sink_attention_decode_ex and
+ * csa_decode_step_ex, but comp and swa_ring hold records of
+ * CSA_FP4_RECORD_BYTES bytes (swa_ring [B,R,384]). The latents enter the tensor
+ * cores without a rounding; the softmax weights are rounded to BF16. */
+CSA_API csa_status_t csa_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale,
+                                                   csa_cache_desc comp, const void *swa_ring, int R, int W,
+                                                   const int32_t *topk_idx, const int32_t *topk_cnt,
+                                                   const int32_t *q_pos, int B, int T, int k, void *out, float *lse,
+                                                   const csa_attention_epilogue *epilogue, void *workspace,
+                                                   size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+CSA_API csa_status_t hca_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale,
+                                                   csa_cache_desc comp, const int32_t *n_comp, const void *swa_ring,
+                                                   int R, int W, const int32_t *q_pos, int B, int T, int m_hca,
+                                                   void *out, float *lse, const csa_attention_epilogue *epilogue,
+                                                   void *workspace, size_t workspace_bytes, int32_t *status,
+                                                   cudaStream_t stream);
+CSA_API csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                                         const uint8_t *k_idx, const float *k_idx_scale, const void *q,
+                                         const float *sink, float softmax_scale, csa_cache_desc comp,
+                                         const void *swa_ring, int R, int W, const int32_t *q_pos,
+                                         const int32_t *n_comp, int B, int T, int Ncap, int m, int k, void *out,
+                                         float *lse, int32_t *topk_idx, int32_t *topk_cnt,
+                                         const csa_attention_epilogue *epilogue, void *workspace,
+                                         size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
 /* Host-I/O decode pipeline (the pages have no counterpart; it serves callers
  * whose query-side inputs arrive in, and whose results go back to, host
  * memory). csa_decode_step_host runs csa_decode_step on per-step copies of

@@ -93,7 +93,8 @@ def fp8_values(rec: np.ndarray) -> np.ndarray:
 
 def bf16(b: np.ndarray) -> np.ndarray:
     """[n, 128] bytes -> [n, 64] float64."""
-    return torch.from_numpy(np.ascontiguousarray(b)).view(torch.bfloat16).double().numpy()
+    bits = b[:, 0::2].astype(np.uint32) | (b[:, 1::2].astype(np.uint32) << 8)
+    return (bits << 16).view(np.float32).astype(np.float64)
 
 
 def random_fp4_records(n: int, seed: int, spread: float = 1.0) -> torch.Tensor:

@@ -139,3 +139,31 @@ def test_plain_quantiser_picks_nearest_values():
     unit = np.repeat(R.E4M3[scales] * 2.0 ** E, 16)
     assert np.all(np.abs(R.fp4_values(rec)[0, :448] - y[:448]) <= unit)
     assert R.fp4_record(np.zeros(512))[2] == 0
+
+
+def test_fp4_attention_refuses_like_the_fp8_calls(lib):
+    """Same host checks and codes as the FP8 entry points, argument by argument."""
+    good = desc(seq_stride=10, seq_capacity=10, n_records=10)
+    over = desc(seq_stride=5, seq_capacity=10)
+    E = csd.csa_attention_epilogue
+    for c in [dict(q=None), dict(comp=csd.csa_cache_desc()), dict(comp=over, B=2), dict(W=600, R=600), dict(R=64),
+              dict(scale=0.0), dict(k=4096), dict(T=129), dict(out=P(0x1008)), dict(status=P(0x1001)),
+              dict(epi=E(1, 1.0, None, None)), dict(epi=E(0, 0.0, 0x2000, None)), dict(out=None), {}]:
+        a = dict(q=FAKE, comp=good, R=128, W=128, B=1, T=1, k=4, out=FAKE, scale=0.1, status=None, epi=None)
+        a.update(c)
+        epi = None if a["epi"] is None else C.byref(a["epi"])
+        head = (a["q"], FAKE, C.c_float(a["scale"]), a["comp"])
+        tail = (a["out"], FAKE, epi, None, 0, a["status"], None)
+        csa = (*head, FAKE, a["R"], a["W"], FAKE, FAKE, FAKE, a["B"], a["T"], a["k"], *tail)
+        hca = (*head, FAKE, FAKE, a["R"], a["W"], FAKE, a["B"], a["T"], 128, *tail)
+        # (with everything right and no workspace, a split row is refused for its workspace)
+        want = lib.csa_sink_attention_decode_ex(*csa)
+        assert lib.csa_sink_attention_decode_fp4(*csa) == want != csd.OK, c
+        assert lib.hca_sink_attention_decode_fp4(*hca) == lib.hca_sink_attention_decode_ex(*hca) != csd.OK, c
+    step = [FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, C.c_float(0.1), good, FAKE, 128, 128, FAKE, FAKE, 1, 1, 8, 4, 4,
+            FAKE, FAKE, None, None, None, None, 0, None, None]
+    assert lib.csa_decode_step_fp4(*step) == csd.ERR_WORKSPACE
+    for i, bad, want in [(0, None, 1), (6, None, 1), (10, 64, 1), (19, P(0x1004), 1), (18, 9, 2)]:
+        b = list(step)
+        b[i] = bad
+        assert lib.csa_decode_step_fp4(*b) == want, i
