@@ -1,12 +1,36 @@
 // attention_fp4.cu -- sink-merged attention over caches of 4-bit records
-// (csa_sink_attention_decode_fp4, hca_sink_attention_decode_fp4).
+// (csa_sink_attention_decode_fp4, hca_sink_attention_decode_fp4) on the tensor
+// cores.
 //
 // For head h over candidates j (x_j the dequantised latent):
 //   z_j = scale * q_h . x_j,  o_h = sum_j e^{z_j-M} x_j / (e^{sink_h-M} + sum_j e^{z_j-M}),
 //   lse_h = M + ln(den),  M = max(sink_h, max_j z_j).
 //
-// One CTA a (query token, 16 heads); candidates in chunks of 32, dequantised to
-// fp32 in shared memory, a running maximum and sum for each head.
+// Work unit = (query token, candidate split), on a cluster of two CTAs. The
+// 128 x 512 fp32 output fills all of one SM's tensor memory, so CTA r keeps
+// output dims [256 r, 256 r + 256) of every head (256 columns). The scores are
+// split by candidate: of each block of 128 candidates CTA r computes QK and the
+// softmax weights of the 64 it owns, over all 512 dims, and sends the weights
+// (128 heads x 64, BF16, 16 KB) to the other CTA's shared memory; each CTA then
+// adds both halves' weights times its own dims of both halves' latents. So QK
+// and the exponentials run once a pair, not once a CTA, and three quarters of
+// the latents' dims are unpacked a CTA instead of all. Per block of 128 and CTA:
+//   QK   S = Q X^T        M = 128 heads, N = 64 own candidates, K = 512
+//   PV   O += P X[:, own] M = 128, N = 256 own dims, K = 64, for own and for
+//                         the other CTA's candidates
+// Both CTAs scale the weights by the same reference maximum: each sends the
+// largest of its 64 scores of every head (512 B) to the other, and both apply
+// the same rule to the pair of maxima (the reference moves only when they
+// exceed it by more than 2^8, log2 domain), so neither has to look at the
+// other's decision. The weights are computed with the old reference while the
+// maxima travel.
+//
+// Latents are unpacked by eight warps from 4-bit records in global memory
+// (through registers, one block ahead) to BF16 in shared memory, exactly (see
+// csa_format_t), in pieces of 64 candidates x 256 dims (32 KB): piece 3i = the
+// other CTA's dims of the own candidates of block i (read by QK only), 3i + 1 =
+// the own dims of the own candidates (QK and PV), 3i + 2 = the own dims of the
+// other CTA's candidates (PV). The pieces go round a ring of kSlots buffers.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -15,173 +39,880 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHeadGroup = 16;
-constexpr int kChunk = 32;
-constexpr int kXStride = kDim + 4;
+constexpr int kChunk = 64;                 // candidates of a block that a CTA owns
+constexpr int kBlock = 2 * kChunk;         // candidates a block
+constexpr int kHalf = 256;                 // output dims per CTA
+constexpr int kThreads = 416;              // 13 warps, see warp_role
+constexpr int kConvWarps = 8;
+constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
+constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
+constexpr int kSlots = 5;
+constexpr int kQTmemDims = 384;            // Q dims held in TMEM; the rest in shared memory
+constexpr int kQAtom = kHeads * 128;       // 64 dims of Q: 128 rows x 128 B
+constexpr int kMaskRing = 4;
+constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.f;               // the reference moves only by more than 2^8
+
+constexpr uint32_t kColQ = 0;    // 192 columns: Q dims 0..383, BF16 pairs
+constexpr uint32_t kColS = 192;  // 64 columns: scores
+constexpr uint32_t kColO = 256;  // 256 columns: O half, fp32
+constexpr uint32_t kTmemCols = 512;
+
+struct AttSmem {
+    alignas(1024) uint8_t x[kSlots][kPieceBytes];
+    alignas(1024) uint8_t qs[2 * kQAtom];      // Q dims 384..511
+    alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
+    alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
+    float pmax[2][kHeads];                     // written by the other CTA
+    uint64_t vmask[kMaskRing];                 // which own candidates of a block exist
+    uint64_t x_full[kSlots], x_empty[kSlots], mask_full[kMaskRing];
+    uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(AttSmem) + 1024 <= 232448, "shared memory plan exceeds the per-CTA limit");
 
 struct Params {
     const __nv_bfloat16 *q;
     const float *sink;
-    float scale;
+    float scale_log2;  // softmax scale * log2(e)
     CacheView comp;
     const uint8_t *ring;
     int R, W;
     const int32_t *topk_idx, *topk_cnt, *n_comp, *q_pos;
-    int m_hca, hca, T, k;
+    int m_hca, hca, T, k, n_split;
     __nv_bfloat16 *out;
     float *lse;
-    uint8_t *out_fp4;
+    __nv_bfloat16 *part_o;  // [rows, n_split, 128, 512] BF16 (n_split > 1)
+    float2 *part_ml;        // [rows, n_split, 128] (max, sum) in log2 units
+    uint8_t *out_fp4;       // null: BF16 output
     float *out_fp4_scale;
     int inv_rope;
     uint64_t turn[kRope / 2];
     int *err;
+    uint64_t wait_ns;  // limit of each bounded wait (drains keep kDrainWaitNs)
 };
 
-struct Smem {
-    float x[kChunk][kXStride];
-    float q[kHeadGroup][kDim];
-    float p[kHeadGroup][kChunk];
-    float m[kHeadGroup], l[kHeadGroup], alpha[kHeadGroup];
-    float amax[kHeadGroup][kThreads / 32];
-    int valid[kChunk];
+// The candidates of a work unit: [cb, ce) of the row's selected entries
+// followed by its window.
+struct Unit {
+    int r, b, split, p, n_sel, j0, cb, ce, n_blocks;
 };
 
-__global__ void __launch_bounds__(kThreads)
-attention_fp4_kernel(const __grid_constant__ Params P) {
-    extern __shared__ uint8_t raw[];
-    Smem &s = *reinterpret_cast<Smem *>(raw);
-    const int tid = threadIdx.x, r = blockIdx.y, b = r / P.T, h0 = blockIdx.x * kHeadGroup;
-    const int p = P.q_pos[r];
-    int n_sel;
+__device__ __forceinline__ Unit make_unit(const Params &P) {
+    Unit u;
+    const int pair = blockIdx.x >> 1;
+    u.r = pair / P.n_split;
+    u.split = pair % P.n_split;
+    u.b = u.r / P.T;
+    u.p = __ldg(P.q_pos + u.r);
     if (P.hca) {
-        n_sel = visible_entries(p, P.m_hca, P.n_comp[b], P.comp.seq_capacity);
+        u.n_sel = visible_entries(u.p, P.m_hca, __ldg(P.n_comp + u.b), P.comp.seq_capacity);
     } else {
-        const int c = P.topk_cnt[r];
-        n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
+        const int c = __ldg(P.topk_cnt + u.r);
+        u.n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
     }
-    const int j0 = max(0, p - P.W + 1);
-    const int n = n_sel + (p >= 0 ? p - j0 + 1 : 0);
-    for (int i = tid; i < kHeadGroup * kDim; i += kThreads)
-        s.q[i / kDim][i % kDim] = __bfloat162float(P.q[((size_t)r * kHeads + h0) * kDim + i]) * P.scale;
-    if (tid < kHeadGroup) {
-        s.m[tid] = P.sink[h0 + tid];
-        s.l[tid] = s.m[tid] == -INFINITY ? 0.f : 1.f;
-    }
-    float2 acc[kHeadGroup];
+    u.j0 = max(0, u.p - P.W + 1);
+    const int n = u.n_sel + (u.p >= 0 ? u.p - u.j0 + 1 : 0);
+    const int per = ((n + P.n_split - 1) / P.n_split + kBlock - 1) / kBlock * kBlock;
+    u.cb = min(n, u.split * per);
+    u.ce = min(n, u.cb + per);
+    u.n_blocks = (u.ce - u.cb + kBlock - 1) / kBlock;
+    return u;
+}
+
+// 16-byte chunk cc of row `row` of a swizzled block of 128-byte rows.
+__device__ __forceinline__ uint4 *sw128(uint8_t *block, int row, int cc) {
+    return reinterpret_cast<uint4 *>(block + row * 128 + ((cc ^ (row & 7)) << 4));
+}
+
+// ---------------------------------------------------------------- PTX of the pair
+
+// One lane of a converged warp, the same for every call.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+
+// tcgen05.mma kind::f16 with the issuing lane chosen by a predicate instead of
+// a branch, so that the descriptors stay warp-uniform values.
+__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(issue), "r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(issue), "r"(d), "r"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs of the pair when the MMAs
+// issued so far by this thread are done.
+__device__ __forceinline__ void commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            ptx::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void remote_store(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void remote_store16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void remote_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// ptx::mbar_wait for a barrier that the other CTA arrives on.
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    if (!ptx::mbar_wait(bar, parity, abort, limit_ns)) return false;
+    return try_wait_cluster(bar, parity);  // (complete: returns at once) orders the other CTA's writes
+}
+
+// ---------------------------------------------------------------- unpacking
+
+// A thread's part of one piece of a record: four units of 16 dims, unit 4 i + hq
+// of the half (i < 4). The last unit of the upper half is 16 rope dims.
+struct Part {
+    uint2 code[3];
+    uint4 last[2];   // lower half: the fourth unit's codes in last[0].x, .y; upper half: rope dims
+    uint4 scale;     // byte hq of word i: the scale of unit i (upper half: word 3 = the power)
+    uint32_t power;
+};
+
+__device__ __forceinline__ uint2 load_code(const uint8_t *p) {
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 load16(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void load_part(Part &a, const uint8_t *rec, int hf, int hq) {
+    if (!rec) return;
+    const uint8_t *c = rec + hf * 128 + 8 * hq;
 #pragma unroll
-    for (int h = 0; h < kHeadGroup; ++h) acc[h] = make_float2(0.f, 0.f);
-    for (int c0 = 0; c0 < n; c0 += kChunk) {
-        __syncthreads();
-        {  // eight threads a candidate
-            const int c = tid >> 3, part = tid & 7, i = c0 + c;
-            const uint8_t *rec = nullptr;
-            if (i < n_sel) {
-                const int e = P.hca ? i : P.topk_idx[(size_t)r * P.k + i];
-                const int64_t ri = record_index(P.comp, b, e);
-                if (ri >= 0) rec = P.comp.base + ri * kFp4Bytes;
-                else if (part == 0 && blockIdx.x == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
-            } else if (i < n) {
-                rec = P.ring + ((int64_t)b * P.R + (j0 + i - n_sel) % P.R) * kFp4Bytes;
+    for (int i = 0; i < 3; ++i) a.code[i] = load_code(c + 32 * i);
+    a.scale = load16(rec + kFp4ScaleOffset + 16 * hf);
+    if (hf == 0) {
+        const uint2 v = load_code(c + 96);
+        a.last[0].x = v.x;
+        a.last[0].y = v.y;
+        a.power = *reinterpret_cast<const uint32_t *>(rec + kFp4PowerOffset);
+    } else {
+        a.last[0] = load16(rec + kFp4RopeOffset + 32 * hq);
+        a.last[1] = load16(rec + kFp4RopeOffset + 32 * hq + 16);
+        a.power = a.scale.w;
+    }
+}
+
+// 8 E2M1 codes times s -> 8 BF16 values (exact).
+__device__ __forceinline__ uint4 unpack8(uint32_t w, float s) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * i)), __NV_E2M1);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        o[i] = pack_bf16(v.x * s, v.y * s);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Unpacks a part into its row of a piece (rolled: the code of all warp roles
+// shares the schedulers' instruction caches).
+__device__ __forceinline__ void unpack_part(Part a, bool valid, int hf, int hq, int row, uint8_t *xs) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const float power = fp4_power(a.power & 0xFFu);
+    uint32_t sc[4] = {a.scale.x, a.scale.y, a.scale.z, a.scale.w};
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        uint4 lo = zero, hi = zero;
+        if (valid) {
+            if (i == 3 && hf == 1) {
+                lo = a.last[0];
+                hi = a.last[1];
+            } else {
+                const float s = e4m3x2_to_float2((uint16_t)((sc[0] >> (8 * hq)) & 0xFFu)).x * power;
+                lo = unpack8(a.code[0].x, s);
+                hi = unpack8(a.code[0].y, s);
             }
-            if (part == 0) s.valid[c] = rec != nullptr;
-            for (int d = part * 64; d < part * 64 + 64; ++d) {
-                float v = 0.f;
-                if (rec) {
-                    if (d >= kNope) {
-                        v = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(rec + kFp4RopeOffset)[d - kNope]);
-                    } else {
-                        const __half2_raw two = __nv_cvt_fp4x2_to_halfraw2(rec[d >> 1], __NV_E2M1);
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&two));
-                        const float sb = e4m3x2_to_float2(rec[kFp4ScaleOffset + d / kFp4Block]).x;
-                        v = ((d & 1) ? f.y : f.x) * sb * fp4_power(rec[kFp4PowerOffset]);
+        }
+        *sw128(xs + i * kAtom, row, 2 * hq) = lo;
+        *sw128(xs + i * kAtom, row, 2 * hq + 1) = hi;
+        a.code[0] = a.code[1];
+        a.code[1] = a.code[2];
+        a.code[2] = make_uint2(a.last[0].x, a.last[0].y);
+        sc[0] = sc[1];
+        sc[1] = sc[2];
+        sc[2] = sc[3];
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// Warps: 0..7 load + unpack, 8 MMA issuer (and TMEM owner), 9..12 softmax and
+// epilogue (thread = head; a warp's TMEM lanes are 32 (warp % 4) ..).
+constexpr int kMmaWarp = 8;
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+attention_fp4_kernel(const __grid_constant__ Params P) {
+    extern __shared__ uint8_t smem_raw[];
+    AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x & 1;  // = the CTA's rank in its cluster
+    volatile int *abort = &s.abort_flag;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(&s.x_full[i], kConvWarps);
+            ptx::mbar_init(&s.x_empty[i], 1);
+        }
+        for (int i = 0; i < kMaskRing; ++i) ptx::mbar_init(&s.mask_full[i], kConvWarps);
+        ptx::mbar_init(&s.s_full, 1);
+        ptx::mbar_init(&s.s_free, 4);
+        ptx::mbar_init(&s.p_full, 4);
+        ptx::mbar_init(&s.pp_full, 4);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], 4);
+        ptx::mbar_init(&s.o_done, 2);  // both CTAs' PV of a block
+        ptx::mbar_init(&s.q_ready, 4);
+        ptx::mbar_init(&s.mma_done, 1);
+        s.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) ptx::tmem_alloc(&s.tmem_base, kTmemCols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();  // the other CTA's barriers exist before anything is sent to it
+    ptx::tc_fence_after();
+    const uint32_t tmem = s.tmem_base;
+    ptx::griddep_wait();
+    const Unit u = make_unit(P);
+
+    auto fail = [&]() {
+        report_error(P.err, CSA_ERR_TIMEOUT);
+        *abort = 1;
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, P.wait_ns)) != 0;
+    };
+    auto wait_peer = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_cluster(bar, parity, abort, P.wait_ns)) != 0;
+    };
+
+    if (warp < kConvWarps) {
+        // ------------------------------------------------------------ load + unpack
+        const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
+        // candidate `row` of the own (o = 0) or the other CTA's (o = 1) chunk of block i
+        auto cand = [&](int i, int o) { return u.cb + i * kBlock + (o ? rank ^ 1 : rank) * kChunk + row; };
+        auto entry = [&](int i, int o) {
+            const int c = cand(i, o);
+            if (P.hca || c >= u.ce || c >= u.n_sel) return c;
+            return __ldg(P.topk_idx + (size_t)u.r * P.k + c);
+        };
+        auto record = [&](int i, int o, int e) -> const uint8_t * {
+            const int c = cand(i, o);
+            if (c >= u.ce) return nullptr;
+            if (c >= u.n_sel) {
+                const int pos = u.j0 + (c - u.n_sel);
+                return P.ring + ((int64_t)u.b * P.R + pos % P.R) * kFp4Bytes;
+            }
+            const int64_t ri = record_index(P.comp, u.b, e);
+            if (ri >= 0) return P.comp.base + ri * kFp4Bytes;
+            if (rank == 0 && hq == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+            return nullptr;
+        };
+        bool ok = true;
+        Part part[3];  // the pieces to come, in order
+        const uint8_t *rec[3];
+        int e_own = 0, e_oth = 0;  // entries of the block after the loaded one
+        if (u.n_blocks > 0) {
+            const uint8_t *own = record(0, 0, entry(0, 0)), *oth = record(0, 1, entry(0, 1));
+            rec[0] = rec[1] = own;
+            rec[2] = oth;
+            load_part(part[0], own, rank ^ 1, hq);
+            load_part(part[1], own, rank, hq);
+            load_part(part[2], oth, rank, hq);
+            if (u.n_blocks > 1) {
+                e_own = entry(1, 0);
+                e_oth = entry(1, 1);
+            }
+        }
+        int slot = 0, turn = 0;  // ring position of piece t, and how often the ring has gone round
+#pragma unroll 1
+        for (int t = 0, i = 0, j = 0; t < 3 * u.n_blocks; ++t) {  // piece t = 3 i + j
+            if (j == 0) {
+                // which own candidates exist (rows 8 warp .. of this warp)
+                const uint32_t have = __ballot_sync(0xffffffffu, rec[0] != nullptr);
+                if (lane == 0) {
+                    uint32_t byte = 0;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) byte |= ((have >> (4 * q)) & 1u) << q;
+                    reinterpret_cast<uint8_t *>(&s.vmask[i % kMaskRing])[warp] = (uint8_t)byte;
+                    ptx::mbar_arrive(&s.mask_full[i % kMaskRing]);
+                }
+            }
+            const int hf = j == 0 ? rank ^ 1 : rank;
+            if (!wait(&s.x_empty[slot], (turn & 1) ^ 1)) { fail(); ok = false; break; }
+            unpack_part(part[0], rec[0] != nullptr, hf, hq, row, s.x[slot]);
+            ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.x_full[slot]);
+            // the same piece of the next block takes the end of the queue
+            part[0] = part[1];
+            part[1] = part[2];
+            const uint8_t *nxt = nullptr;
+            if (i + 1 < u.n_blocks) {
+                if (j == 0) nxt = record(i + 1, 0, e_own);
+                else if (j == 1) nxt = rec[2];  // (after two shifts: the record of the queue's last piece)
+                else nxt = record(i + 1, 1, e_oth);
+                load_part(part[2], nxt, hf, hq);
+            }
+            rec[0] = rec[1];
+            rec[1] = rec[2];
+            rec[2] = nxt;
+            if (j == 2 && i + 2 < u.n_blocks) {
+                e_own = entry(i + 2, 0);
+                e_oth = entry(i + 2, 1);
+            }
+            if (++j == 3) j = 0, ++i;
+            if (++slot == kSlots) slot = 0, ++turn;
+        }
+        (void)ok;
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t kIdescQK = ptx::idesc_f32acc(1, 1, 128, kChunk);
+        constexpr uint32_t kIdescPV = ptx::idesc_f32acc(1, 1, 128, kHalf, 1);
+        const uint32_t leader = elect_one();
+        bool ok = u.n_blocks == 0 || wait(&s.q_ready, 0);
+        if (!ok) fail();
+        const uint64_t qd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.qs));
+        // the 16 K-steps of dims 256 hf ..: Q from TMEM below kQTmemDims, from
+        // shared memory above
+        auto qk_half = [&](int hf, const uint8_t *x, bool first) {
+            const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(x));
+            if (hf == 0) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    mma_ts(leader, tmem + kColS, tmem + kColQ + k * 8,
+                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(leader, tmem + kColS, tmem + kColQ + (16 + k) * 8,
+                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
+#pragma unroll
+                for (int k = 8; k < 16; ++k)
+                    mma_ss(leader, tmem + kColS, qd + (uint64_t)((((k - 8) >> 2) * kQAtom + (k & 3) * 32) >> 4),
+                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, 1u);
+            }
+        };
+        auto pv = [&](const uint8_t *w, const uint8_t *x, bool first) {
+            const uint64_t ad = ptx::desc_kmajor_sw128(ptx::smem_u32(w));
+            const uint64_t bd = ptx::desc_mnmajor_sw128(ptx::smem_u32(x), kAtom, 1024);
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+                mma_ss(leader, tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
+                       !(first && k == 0));
+        };
+        auto full = [&](int t) { return wait(&s.x_full[t % kSlots], (t / kSlots) & 1); };
+#pragma unroll 1
+        for (int i = 0; i <= u.n_blocks && ok; ++i) {
+            if (i < u.n_blocks) {
+                // QK(i): the dims that this CTA does not output first (unpacked first)
+                if (i >= 1 && !wait(&s.s_free, (i - 1) & 1)) { fail(); ok = false; break; }
+#pragma unroll 1
+                for (int own = 0; own < 2; ++own) {
+                    const int t = 3 * i + own;
+                    if (!full(t)) { fail(); ok = false; break; }
+                    ptx::tc_fence_after();
+                    qk_half(rank ^ own ^ 1, s.x[t % kSlots], own == 0);
+                    if (leader) ptx::mma_commit(own ? &s.s_full : &s.x_empty[t % kSlots]);
+                    __syncwarp();
+                }
+                if (!ok) break;
+            }
+            if (i >= 1) {
+                // PV(i - 1): own candidates, then the other CTA's
+                const int t = 3 * (i - 1) + 1;
+                const uint32_t ph = (i - 1) & 1;
+                if (!wait(&s.p_full, ph)) { fail(); ok = false; break; }
+                ptx::tc_fence_after();
+                pv(s.p, s.x[t % kSlots], i == 1);
+                if (leader) ptx::mma_commit(&s.x_empty[t % kSlots]);
+                __syncwarp();
+                if (!full(t + 1) || !wait_peer(&s.pp_full, ph)) { fail(); ok = false; break; }
+                ptx::fence_proxy_async_smem();  // the other CTA's stores -> PV (async proxy) reads
+                ptx::tc_fence_after();
+                pv(s.pp, s.x[(t + 1) % kSlots], false);
+                if (leader) {
+                    ptx::mma_commit(&s.x_empty[(t + 1) % kSlots]);
+                    commit_both(&s.o_done);
+                }
+                __syncwarp();
+            }
+        }
+        if (leader) ptx::mma_commit(&s.mma_done);
+        __syncwarp();
+        // every MMA issued has finished with tensor and shared memory before the
+        // CTA frees them (not cut short by the abort flag)
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait_drain(&s.mma_done, 0, kDrainWaitNs)))
+            report_error(P.err, CSA_ERR_TIMEOUT);
+        if (!ok || *abort) {
+            // given up: arrivals that were sent to the other CTA's barrier land
+            // long before this (bounded) pause ends
+            const uint64_t t0 = ptx::globaltimer_ns();
+            while (ptx::globaltimer_ns() - t0 < 100000ull) {}
+        }
+    } else {
+        // ------------------------------------------------------------ softmax / epilogue
+        const int quarter = warp & 3;
+        const int h = quarter * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t peer_max = ptx::mapa(ptx::smem_u32(&s.pmax[0][h]), rank ^ 1);
+        const uint32_t peer_max_full = ptx::mapa(ptx::smem_u32(&s.max_full[0]), rank ^ 1);
+        // this block's maximum (or, at the end, the sum) to the other CTA
+        auto send = [&](int i, float v) {
+            remote_store(peer_max + (i & 1) * (kHeads * 4), v);
+            __syncwarp();
+            if (lane == 0) remote_arrive(peer_max_full + (i & 1) * 8);
+        };
+        const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp), rank ^ 1) + h * 128;
+        const uint32_t peer_pp_full = ptx::mapa(ptx::smem_u32(&s.pp_full), rank ^ 1);
+        bool ok = true;
+        if (u.n_blocks > 0) {
+            // Q: dims from kQTmemDims up -> shared memory, the dims below -> TMEM
+            // (BF16 pairs, lane = head), 64 dims a piece, two pieces in flight
+            const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + ((size_t)u.r * kHeads + h) * kDim);
+            const uint64_t policy = ptx::l2_policy_evict_first();
+#pragma unroll
+            for (int c = 0; c < (kDim - kQTmemDims) / 8; ++c)
+                ptx::cp_async_16_hint(sw128(s.qs + (c >> 3) * kQAtom, h, c & 7), qg + kQTmemDims / 8 + c, policy);
+            ptx::cp_async_commit();
+            constexpr int kQPieces = kQTmemDims / 64;
+            uint4 wa[8], wb[8];
+            auto load_piece = [&](uint4 (&w)[8], int pc) {
+#pragma unroll
+                for (int v = 0; v < 8; ++v) w[v] = ptx::ldg_v4_policy(qg + pc * 8 + v, policy);
+            };
+            auto store_piece = [&](const uint4 (&w)[8], int pc) {
+                uint32_t regs[32];
+#pragma unroll
+                for (int v = 0; v < 8; ++v) {
+                    regs[4 * v] = w[v].x;
+                    regs[4 * v + 1] = w[v].y;
+                    regs[4 * v + 2] = w[v].z;
+                    regs[4 * v + 3] = w[v].w;
+                }
+                ptx::tmem_st32(lane_base + kColQ + pc * 32, regs);
+            };
+            load_piece(wa, 0);
+            load_piece(wb, 1);
+#pragma unroll 1
+            for (int pc = 0; pc < kQPieces; pc += 2) {
+                store_piece(wa, pc);
+                if (pc + 2 < kQPieces) load_piece(wa, pc + 2);
+                store_piece(wb, pc + 1);
+                if (pc + 3 < kQPieces) load_piece(wb, pc + 3);
+            }
+            ptx::cp_async_wait<0>();
+            ptx::tmem_st_wait();
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.q_ready);
+        }
+        float m = -INFINITY, l = 0.f;  // reference and own sum, log2 domain, sink not included
+#pragma unroll 1
+        for (int i = 0; i < u.n_blocks; ++i) {
+            if (!wait(&s.mask_full[i % kMaskRing], (i / kMaskRing) & 1)) { fail(); ok = false; break; }
+            const uint64_t mask = *reinterpret_cast<volatile uint64_t *>(&s.vmask[i % kMaskRing]);
+            if (!wait(&s.s_full, i & 1)) { fail(); ok = false; break; }
+            ptx::tc_fence_after();
+            float z[kChunk];
+            {
+                uint32_t sa[32], sb[32];
+                ptx::tmem_ld32(lane_base + kColS, sa);
+                ptx::tmem_ld32(lane_base + kColS + 32, sb);
+                ptx::tmem_ld_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.s_free);
+#pragma unroll
+                for (int c = 0; c < kChunk; ++c) {
+                    const float sv = __uint_as_float(c < 32 ? sa[c] : sb[c - 32]);
+                    z[c] = ((mask >> c) & 1ull) ? sv * P.scale_log2 : -INFINITY;
+                }
+            }
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kChunk; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], z[c]);
+            const float own = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            // the pair's maxima: buffer i % 2 is free, since the other CTA sent
+            // its maximum of block i - 1 after it had read that of block i - 2
+            send(i, own);
+            if (!wait_peer(&s.max_full[i & 1], (i >> 1) & 1)) { fail(); ok = false; break; }
+            const float mx = fmaxf(own, *reinterpret_cast<volatile float *>(&s.pmax[i & 1][h]));
+            // Both CTAs' PV of block i - 1 is done: O holds the blocks before
+            // this one, the own weights have been read here and copied there.
+            if (i > 0) {
+                if (!wait_peer(&s.o_done, (i - 1) & 1)) { fail(); ok = false; break; }
+                ptx::tc_fence_after();
+            }
+            // Lazy rescale, the same decision in both CTAs. It is per head (lane)
+            // but the TMEM accesses are warp-collective, so the whole warp
+            // enters when any lane needs it; other lanes use a factor of 1.
+            const bool need = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+            if (__any_sync(0xffffffffu, need)) {
+                const float alpha = need ? ptx::ex2_approx(m - mx) : 1.f;  // 0 when m = -inf
+                if (i > 0) {
+#pragma unroll 1
+                    for (int piece = 0; piece < kHalf / 32; ++piece) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(lane_base + kColO + piece * 32, o);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        ptx::tmem_st32(lane_base + kColO + piece * 32, o);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                }
+                l *= alpha;
+                if (need) m = mx;
+            }
+            const float mref = (m == -INFINITY) ? 0.f : m;  // every z is -inf while m is
+            float ps4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c8 = 0; c8 < kChunk / 8; ++c8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p0 = ptx::ex2_approx(z[8 * c8 + 2 * e] - mref);
+                    const float p1 = ptx::ex2_approx(z[8 * c8 + 2 * e + 1] - mref);
+                    ps4[e] += p0 + p1;
+                    w[e] = pack_bf16(p0, p1);
+                }
+                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+                *sw128(s.p, h, c8) = v;
+                remote_store16(peer_pp + ((c8 ^ (h & 7)) << 4), v);
+            }
+            l += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
+            ptx::fence_proxy_async_smem();  // own weights -> PV (async proxy) reads
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(&s.p_full);
+                remote_arrive(peer_pp_full);
+            }
+        }
+        // the pair's sums travel like one more block's maxima
+        if (ok && u.n_blocks > 0) {
+            const int i = u.n_blocks;
+            send(i, l);
+            if (!wait_peer(&s.max_full[i & 1], (i >> 1) & 1) || !wait_peer(&s.o_done, (i - 1) & 1)) {
+                fail();
+                ok = false;
+            } else {
+                l += *reinterpret_cast<volatile float *>(&s.pmax[i & 1][h]);
+            }
+            ptx::tc_fence_after();
+        }
+        // ---------------- epilogue: O half (and LSE) out
+        if (ok) {
+            const int r = u.r;
+            float factor, lse_out = 0.f;
+            const float2 ml = make_float2(m, l);
+            const bool final_out = P.n_split == 1;
+            if (final_out) {
+                const float sk = __ldg(P.sink + h) * kLog2e;
+                const float M = fmaxf(sk, m);
+                const float es = (sk == -INFINITY) ? 0.f : exp2f(sk - M);
+                const float eo = (m == -INFINITY) ? 0.f : exp2f(m - M);
+                const float den = es + l * eo;
+                factor = den > 0.f ? eo / den : 0.f;
+                lse_out = l > 0.f ? (M + log2f(den)) * kLn2 : __ldg(P.sink + h);  // no candidates: the sink itself
+            } else {
+                factor = l > 0.f ? 1.f / l : 0.f;
+            }
+            const bool rope_here = final_out && P.inv_rope && rank == 1;
+            float2 cs = make_float2(1.f, 0.f);  // lane i: cos, sin of rope pair i
+            if (rope_here) cs = turn_cos_sin(u.p, P.turn[lane]);
+            // piece (32 dims) of this head's O half, normalised and turned back
+            auto piece_values = [&](int piece, float (&v)[32]) {
+                if (u.n_blocks > 0) {
+                    uint32_t o[32];
+                    ptx::tmem_ld32(lane_base + kColO + piece * 32, o);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * factor;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (rope_here && piece >= (kNope - kHalf) / 32) {  // latent dims 448..511
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int pair = (piece - (kNope - kHalf) / 32) * 16 + e;
+                        const float c = __shfl_sync(0xffffffffu, cs.x, pair);
+                        const float sn = __shfl_sync(0xffffffffu, cs.y, pair);
+                        const float x = v[2 * e], y = v[2 * e + 1];
+                        v[2 * e] = fmaf(x, c, y * sn);
+                        v[2 * e + 1] = fmaf(-x, sn, y * c);
                     }
                 }
-                s.x[c][d] = v;
+            };
+            // Rows are staged in shared memory (the pieces' buffers are free once
+            // every PV is done), then each warp writes its 32 head rows whole.
+            // Chunk c (16 B) of row h sits at position c ^ (h & 7).
+            uint8_t *ostage = &s.x[0][0];
+            if (!(final_out && P.out_fp4)) {
+                uint8_t *srow = ostage + h * (kHalf * 2);
+#pragma unroll 1
+                for (int piece = 0; piece < kHalf / 32; ++piece) {
+                    float v[32];
+                    piece_values(piece, v);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const int c = piece * 4 + q4;
+                        *reinterpret_cast<uint4 *>(srow + ((c ^ (h & 7)) << 4)) =
+                            make_uint4(pack_bf16(v[8 * q4 + 0], v[8 * q4 + 1]), pack_bf16(v[8 * q4 + 2], v[8 * q4 + 3]),
+                                       pack_bf16(v[8 * q4 + 4], v[8 * q4 + 5]), pack_bf16(v[8 * q4 + 6], v[8 * q4 + 7]));
+                    }
+                }
+                __syncwarp();
+                const uint64_t policy = ptx::l2_policy_evict_first();
+                __nv_bfloat16 *dst0 = final_out
+                                          ? P.out + (size_t)r * kHeads * kDim + rank * kHalf
+                                          : P.part_o + ((size_t)r * P.n_split + u.split) * kHeads * kDim + rank * kHalf;
+#pragma unroll 4
+                for (int i = 0; i < 32; ++i) {
+                    const int hr = quarter * 32 + i;  // a head row of this warp
+                    const uint4 v = *reinterpret_cast<const uint4 *>(ostage + hr * (kHalf * 2) + ((lane ^ (hr & 7)) << 4));
+                    if (final_out)
+                        reinterpret_cast<uint4 *>(dst0 + (size_t)hr * kDim)[lane] = v;
+                    else  // split partials are read once, by the combine: evict-first
+                        ptx::stg_v4_policy(reinterpret_cast<uint4 *>(dst0 + (size_t)hr * kDim) + lane, v, policy);
+                }
+            } else {
+                // E2M1: two 128-dim blocks per half, each scaled by its amax / 6
+                // (a first pass over TMEM finds the amax); 128 B per head row
+                uint8_t *frow = ostage + h * (kFp4RowBytes / 2);
+#pragma unroll 1
+                for (int bl = 0; bl < 2; ++bl) {
+                    float amax = 0.f;
+#pragma unroll 1
+                    for (int pp = 0; pp < 4; ++pp) {
+                        float v[32];
+                        piece_values(4 * bl + pp, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
+                    }
+                    const float sc = amax > 0.f ? amax / 6.f : 1.f;
+                    const float inv = 1.f / sc;
+#pragma unroll 1
+                    for (int pp = 0; pp < 4; ++pp) {
+                        float v[32];
+                        piece_values(4 * bl + pp, v);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4)
+                            w[q4] = e2m1x4(v[8 * q4] * inv, v[8 * q4 + 1] * inv, v[8 * q4 + 2] * inv,
+                                           v[8 * q4 + 3] * inv) |
+                                    (e2m1x4(v[8 * q4 + 4] * inv, v[8 * q4 + 5] * inv, v[8 * q4 + 6] * inv,
+                                            v[8 * q4 + 7] * inv) << 16);
+                        const int c = 4 * bl + pp;
+                        *reinterpret_cast<uint4 *>(frow + ((c ^ (h & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    P.out_fp4_scale[((size_t)r * kHeads + h) * 4 + rank * 2 + bl] = sc;
+                }
+                __syncwarp();
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int hr = quarter * 32 + i * 4 + (lane >> 3);  // 8 lanes per 128-byte row
+                    const int c = lane & 7;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(ostage + hr * (kFp4RowBytes / 2) + ((c ^ (hr & 7)) << 4));
+                    reinterpret_cast<uint4 *>(P.out_fp4 + ((size_t)r * kHeads + hr) * kFp4RowBytes +
+                                              rank * (kFp4RowBytes / 2))[c] = v;
+                }
+            }
+            if (rank == 0) {
+                if (final_out)
+                    P.lse[(size_t)r * kHeads + h] = lse_out;
+                else
+                    P.part_ml[((size_t)r * P.n_split + u.split) * kHeads + h] = ml;
             }
         }
-        __syncthreads();
-        const int h = tid >> 4;  // 16 threads a head, two candidates each
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, kTmemCols);
+    ptx::cluster_sync();  // nothing is on its way to a CTA that has left
+}
+
+// Folds the per-split normalised partials and the sink (log2 domain):
+//   M = max(sink, m_s), den = e^{sink-M} + sum_s l_s e^{m_s-M},
+//   out = sum_s l_s e^{m_s-M} o_s / den, lse = M + ln den.
+// One warp per (row, head), 16 dims per lane; up to 8 splits' rows in flight.
+constexpr int kCombineBatch = 8;
+__global__ void __launch_bounds__(256)
+combine_fp4_kernel(const __grid_constant__ Params P) {
+    ptx::griddep_wait();
+    const int r = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float2 cs = make_float2(1.f, 0.f);  // lane i: cos, sin of rope pair i
+    if (P.inv_rope) cs = turn_cos_sin(__ldg(P.q_pos + r), P.turn[lane]);
+    const int h = blockIdx.x * 8 + warp;
+    const float sk = __ldg(P.sink + h) * kLog2e;
+    const float2 *ml_row = P.part_ml + (size_t)r * P.n_split * kHeads + h;
+    const uint4 *o_row = reinterpret_cast<const uint4 *>(P.part_o + ((size_t)r * P.n_split * kHeads + h) * kDim) + lane * 2;
+    const size_t split_stride = (size_t)kHeads * kDim / 8;  // uint4 per split
+    const uint64_t policy = ptx::l2_policy_evict_first();
+    float M = sk;
+    if (P.n_split > kCombineBatch)
+        for (int sp = 0; sp < P.n_split; ++sp) {
+            const float2 ml = ml_row[(size_t)sp * kHeads];
+            if (ml.y > 0.f) M = fmaxf(M, ml.x);
+        }
+    float den = 0.f;
+    float acc[2][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
+    for (int s0 = 0; s0 < P.n_split; s0 += kCombineBatch) {
+        float2 ml[kCombineBatch];
+        Octet<CSA_BF16> v[kCombineBatch][2];
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) {
+            const int sp = s0 + q;
+            ml[q] = make_float2(0.f, 0.f);
+            if (sp < P.n_split) {
+                ml[q] = ml_row[(size_t)sp * kHeads];
+                v[q][0].v = ptx::ldg_v4_policy(o_row + sp * split_stride, policy);
+                v[q][1].v = ptx::ldg_v4_policy(o_row + sp * split_stride + 1, policy);
+            }
+        }
+        if (P.n_split <= kCombineBatch) {
+#pragma unroll
+            for (int q = 0; q < kCombineBatch; ++q)
+                if (ml[q].y > 0.f) M = fmaxf(M, ml[q].x);
+        }
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) {
+            if (!(ml[q].y > 0.f)) continue;
+            const float w = ml[q].y * exp2f(ml[q].x - M);
+            den += w;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float f[8];
+                v[q][e].floats(f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[e][i] = fmaf(w, f[i], acc[e][i]);
+            }
+        }
+    }
+    const bool none = !(den > 0.f);  // no candidates: lse is the sink itself
+    den += (sk == -INFINITY) ? 0.f : exp2f(sk - M);
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[e][i] *= inv;
+    // lanes 28..31 hold the rope dims 448..511, 8 pairs each
+    if (P.inv_rope) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int c = (tid & 15) + 16 * e;
-            float z = 0.f;
-            for (int d = 0; d < kDim; d += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&s.q[h][d]);
-                const float4 x = *reinterpret_cast<const float4 *>(&s.x[c][d]);
-                z = fmaf(a.x, x.x, fmaf(a.y, x.y, fmaf(a.z, x.z, fmaf(a.w, x.w, z))));
-            }
-            s.p[h][c] = s.valid[c] ? z : -INFINITY;
-        }
-        __syncthreads();
-        if (tid < kHeadGroup) {
-            float m = s.m[tid];
-            for (int c = 0; c < kChunk; ++c) m = fmaxf(m, s.p[tid][c]);
-            const float ref = m == -INFINITY ? 0.f : m, al = s.m[tid] == -INFINITY ? 0.f : expf(s.m[tid] - ref);
-            float l = s.l[tid] * al;
-            for (int c = 0; c < kChunk; ++c) {
-                const float e = expf(s.p[tid][c] - ref);
-                s.p[tid][c] = e;
-                l += e;
-            }
-            s.m[tid] = m;
-            s.l[tid] = l;
-            s.alpha[tid] = al;
-        }
-        __syncthreads();
+            float2 back[4];
 #pragma unroll
-        for (int g = 0; g < kHeadGroup; ++g) {
-            float2 a = make_float2(acc[g].x * s.alpha[g], acc[g].y * s.alpha[g]);
-            for (int c = 0; c < kChunk; ++c) {
-                const float w = s.p[g][c];
-                a.x = fmaf(w, s.x[c][2 * tid], a.x);
-                a.y = fmaf(w, s.x[c][2 * tid + 1], a.y);
+            for (int i = 0; i < 4; ++i) {
+                const int pair = ((lane - kNope / 16) & 3) * 8 + 4 * e + i;
+                back[i].x = __shfl_sync(0xffffffffu, cs.x, pair);
+                back[i].y = -__shfl_sync(0xffffffffu, cs.y, pair);
             }
-            acc[g] = a;
+            if (lane >= kNope / 16) turn_octet(acc[e], back);
         }
     }
-    __syncthreads();
-    // thread t holds dims 2t, 2t + 1 of every head: a rope pair from t = 224 on
-    float2 cs = make_float2(1.f, 0.f);
-    if (P.inv_rope && tid >= kNope / 2) cs = turn_cos_sin(p, P.turn[tid - kNope / 2]);
+    const size_t row = (size_t)r * kHeads + h;
+    if (P.out_fp4) {
+        // E2M1 with one multiplier per 128 dims = 8 lanes
+        float amax = 0.f;
 #pragma unroll
-    for (int g = 0; g < kHeadGroup; ++g) {
-        const float inv = s.l[g] > 0.f ? 1.f / s.l[g] : 0.f;
-        const float x = acc[g].x * inv, y = acc[g].y * inv;
-        acc[g] = make_float2(fmaf(x, cs.x, y * cs.y), fmaf(-x, cs.y, y * cs.x));
-        const size_t row = (size_t)r * kHeads + h0 + g;
-        if (P.out_fp4) {
-            float a = fmaxf(fabsf(acc[g].x), fabsf(acc[g].y));
-            for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if ((tid & 31) == 0) s.amax[g][tid >> 5] = a;
-        } else {
-            reinterpret_cast<uint32_t *>(P.out)[row * (kDim / 2) + tid] = pack_bf16(acc[g].x, acc[g].y);
-        }
-        if (tid == 0) P.lse[row] = s.l[g] > 0.f ? s.m[g] + logf(s.l[g]) : -INFINITY;
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(acc[e][i]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float sc = amax > 0.f ? amax / 6.f : 1.f;
+        const float isc = 1.f / sc;
+        uint32_t w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            w[e] = e2m1x4(acc[e][0] * isc, acc[e][1] * isc, acc[e][2] * isc, acc[e][3] * isc) |
+                   (e2m1x4(acc[e][4] * isc, acc[e][5] * isc, acc[e][6] * isc, acc[e][7] * isc) << 16);
+        reinterpret_cast<uint2 *>(P.out_fp4 + row * kFp4RowBytes)[lane] = make_uint2(w[0], w[1]);
+        if ((lane & 7) == 0) P.out_fp4_scale[row * 4 + (lane >> 3)] = sc;
+    } else {
+        uint4 *dst = reinterpret_cast<uint4 *>(P.out + row * kDim) + lane * 2;
+        ptx::stg_v4_policy(dst, pack_bf16_octet(acc[0]), policy);
+        ptx::stg_v4_policy(dst + 1, pack_bf16_octet(acc[1]), policy);
     }
-    if (!P.out_fp4) return;
-    __syncthreads();
-    for (int g = 0; g < kHeadGroup; ++g) {
-        const size_t row = (size_t)r * kHeads + h0 + g;
-        const float a = fmaxf(s.amax[g][(tid >> 5) & ~1], s.amax[g][tid >> 5 | 1]);
-        const float sc = a > 0.f ? a / 6.f : 1.f, inv = 1.f / sc;
-        P.out_fp4[row * (kDim / 2) + tid] = (uint8_t)e2m1x4(acc[g].x * inv, acc[g].y * inv, 0.f, 0.f);
-        if ((tid & 63) == 0) P.out_fp4_scale[row * 4 + (tid >> 6)] = sc;
-    }
+    if (lane == 0) P.lse[row] = none ? __ldg(P.sink + h) : (M + log2f(den)) * kLn2;
+}
+
+// Splits per query so that about one CTA pair per two SMs is busy.
+// `max_candidates` bounds the candidates of any query (selected + window).
+int choose_splits(int rows, int max_candidates) {
+    const int blocks = (max_candidates + kBlock - 1) / kBlock;
+    int n = cached_sm_count() / 2 / (rows > 0 ? rows : 1);
+    if (n > blocks) n = blocks;
+    return n < 1 ? 1 : n;
 }
 
 }  // namespace
 
-// `k` = the top-k row length (CSA) or the per-sequence capacity (HCA).
+// `k` = the top-k row length (CSA) or the per-sequence capacity (HCA). The
+// workspace holds the splits' BF16 partials and their (max, sum); the splits
+// are at most those that attention_workspace_bytes counts (chunks of 64
+// candidates there, blocks of 128 here).
 cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, const csa_cache_desc &comp,
                                  const void *ring, int R, int W, const int32_t *topk_idx, const int32_t *topk_cnt,
                                  const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
-                                 void *out, float *lse, const csa_attention_epilogue *epi, void *, size_t, int *err,
-                                 cudaStream_t stream) {
+                                 void *out, float *lse, const csa_attention_epilogue *epi, void *ws, size_t ws_bytes,
+                                 int *err, cudaStream_t stream) {
     Params P = {};
     P.q = static_cast<const __nv_bfloat16 *>(q);
     P.sink = sink;
-    P.scale = scale;
+    P.scale_log2 = scale * kLog2e;
     P.comp = make_view(comp);
     P.ring = static_cast<const uint8_t *>(ring);
     P.R = R;
@@ -197,6 +928,7 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
     P.out = static_cast<__nv_bfloat16 *>(out);
     P.lse = lse;
     P.err = err;
+    P.wait_ns = wait_limit_ns();
     if (epi) {
         P.out_fp4 = epi->out_fp4;
         P.out_fp4_scale = epi->out_fp4_scale;
@@ -208,11 +940,27 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
             for (int i = 0; i < kRope / 2; ++i) P.turn[i] = o.turn[i];
         }
     }
-    const cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel), sizeof(Smem));
+    const int rows = B * T;
+    P.n_split = choose_splits(rows, k + W);
+    if (P.n_split > 1) {
+        const size_t po = ((size_t)rows * P.n_split * kHeads * kDim * sizeof(__nv_bfloat16) + 255) / 256 * 256;
+        if (!ws || ws_bytes < po + (size_t)rows * P.n_split * kHeads * sizeof(float2)) return cudaErrorInvalidValue;
+        P.part_o = static_cast<__nv_bfloat16 *>(ws);
+        P.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + po);
+    }
+    constexpr size_t smem = sizeof(AttSmem) + 1024;
+    cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel), (int)smem);
     if (e != cudaSuccess) return e;
+    PdlLaunch l(dim3(2 * rows * P.n_split), dim3(kThreads), stream);
+    l.cfg.dynamicSmemBytes = smem;
     count_launch();
-    attention_fp4_kernel<<<dim3(kHeads / kHeadGroup, B * T), kThreads, sizeof(Smem), stream>>>(P);
-    return cudaGetLastError();
+    e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel, P);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess || P.n_split == 1) return e;
+    PdlLaunch c(dim3(kHeads / 8, rows), dim3(256), stream);
+    count_launch();
+    e = cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel, P);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace csa
