@@ -169,12 +169,15 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
 __device__ __forceinline__ void remote_store(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ void remote_store16(uint32_t addr, uint4 v) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
 __device__ __forceinline__ void remote_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Copy into the other CTA, counted on a barrier there.
+__device__ __forceinline__ void copy_to_peer(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "r"(ptx::smem_u32(src)), "r"(bytes), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -302,7 +305,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         ptx::mbar_init(&s.s_full, 1);
         ptx::mbar_init(&s.s_free, 4);
         ptx::mbar_init(&s.p_full, 4);
-        ptx::mbar_init(&s.pp_full, 4);
+        ptx::mbar_init(&s.pp_full, 1);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], 4);
         ptx::mbar_init(&s.o_done, 2);  // both CTAs' PV of a block
         ptx::mbar_init(&s.q_ready, 4);
@@ -333,82 +336,101 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     if (warp < kConvWarps) {
         // ------------------------------------------------------------ load + unpack
         const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
-        // candidate `row` of the own (o = 0) or the other CTA's (o = 1) chunk of block i
+        // Candidate `row` of the own (o = 0) or the other CTA's (o = 1) chunk of a
+        // block goes through three stages, one block apart, so that no stage
+        // waits for the load that it started: its entry (top-k list), its page
+        // (block table), its record (three pieces' worth of loads).
         auto cand = [&](int i, int o) { return u.cb + i * kBlock + (o ? rank ^ 1 : rank) * kChunk + row; };
-        auto entry = [&](int i, int o) {
+        auto load_entry = [&](int i, int o) {
             const int c = cand(i, o);
             if (P.hca || c >= u.ce || c >= u.n_sel) return c;
             return __ldg(P.topk_idx + (size_t)u.r * P.k + c);
         };
-        auto record = [&](int i, int o, int e) -> const uint8_t * {
+        // the physical page of entry e, -1 for none (0 without a block table)
+        auto load_page = [&](int i, int o, int e) {
+            const int c = cand(i, o);
+            if (c >= u.ce || c >= u.n_sel) return 0;
+            if (e < 0 || e >= P.comp.seq_capacity) return -1;
+            if (!P.comp.block_table) return 0;
+            const int page = e / P.comp.page_records;
+            return page < P.comp.max_pages ? __ldg(P.comp.block_table + (int64_t)u.b * P.comp.max_pages + page) : -1;
+        };
+        auto record = [&](int i, int o, int e, int page) -> const uint8_t * {
             const int c = cand(i, o);
             if (c >= u.ce) return nullptr;
             if (c >= u.n_sel) {
                 const int pos = u.j0 + (c - u.n_sel);
                 return P.ring + ((int64_t)u.b * P.R + pos % P.R) * kFp4Bytes;
             }
-            const int64_t ri = record_index(P.comp, u.b, e);
-            if (ri >= 0) return P.comp.base + ri * kFp4Bytes;
+            const int64_t ri = !P.comp.block_table ? (int64_t)u.b * P.comp.seq_stride + e
+                                                   : (int64_t)page * P.comp.page_records + e % P.comp.page_records;
+            if (page >= 0 && ri < P.comp.n_records) return P.comp.base + ri * kFp4Bytes;
             if (rank == 0 && hq == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
             return nullptr;
         };
-        bool ok = true;
-        Part part[3];  // the pieces to come, in order
-        const uint8_t *rec[3];
-        int e_own = 0, e_oth = 0;  // entries of the block after the loaded one
+        Part oth, own, peer;  // the three pieces of a block (see the top of the file)
+        const uint8_t *rec_own = nullptr, *rec_peer = nullptr;
+        int entry[2] = {0, 0}, page[2] = {0, 0};
         if (u.n_blocks > 0) {
-            const uint8_t *own = record(0, 0, entry(0, 0)), *oth = record(0, 1, entry(0, 1));
-            rec[0] = rec[1] = own;
-            rec[2] = oth;
-            load_part(part[0], own, rank ^ 1, hq);
-            load_part(part[1], own, rank, hq);
-            load_part(part[2], oth, rank, hq);
-            if (u.n_blocks > 1) {
-                e_own = entry(1, 0);
-                e_oth = entry(1, 1);
-            }
-        }
-        int slot = 0, turn = 0;  // ring position of piece t, and how often the ring has gone round
-#pragma unroll 1
-        for (int t = 0, i = 0, j = 0; t < 3 * u.n_blocks; ++t) {  // piece t = 3 i + j
-            if (j == 0) {
-                // which own candidates exist (rows 8 warp .. of this warp)
-                const uint32_t have = __ballot_sync(0xffffffffu, rec[0] != nullptr);
-                if (lane == 0) {
-                    uint32_t byte = 0;
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) byte |= ((have >> (4 * q)) & 1u) << q;
-                    reinterpret_cast<uint8_t *>(&s.vmask[i % kMaskRing])[warp] = (uint8_t)byte;
-                    ptx::mbar_arrive(&s.mask_full[i % kMaskRing]);
-                }
+            for (int o = 0; o < 2; ++o) {
+                entry[o] = load_entry(0, o);
+                page[o] = load_page(0, o, entry[o]);
             }
-            const int hf = j == 0 ? rank ^ 1 : rank;
-            if (!wait(&s.x_empty[slot], (turn & 1) ^ 1)) { fail(); ok = false; break; }
-            unpack_part(part[0], rec[0] != nullptr, hf, hq, row, s.x[slot]);
+            rec_own = record(0, 0, entry[0], page[0]);
+            rec_peer = record(0, 1, entry[1], page[1]);
+            load_part(oth, rec_own, rank ^ 1, hq);
+            load_part(own, rec_own, rank, hq);
+            load_part(peer, rec_peer, rank, hq);
+        }
+        int next_entry[2];  // of the block after entry / page
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            if (u.n_blocks > 1) entry[o] = load_entry(1, o);
+            if (u.n_blocks > 2) next_entry[o] = load_entry(2, o);
+            if (u.n_blocks > 1) page[o] = load_page(1, o, entry[o]);
+        }
+        int slot = 0, turn = 0;  // ring position of the next piece, and how often the ring has gone round
+        auto put = [&](const Part &part, bool valid, int hf) {
+            if (!wait(&s.x_empty[slot], (turn & 1) ^ 1)) return false;
+            unpack_part(part, valid, hf, hq, row, s.x[slot]);
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.x_full[slot]);
-            // the same piece of the next block takes the end of the queue
-            part[0] = part[1];
-            part[1] = part[2];
-            const uint8_t *nxt = nullptr;
-            if (i + 1 < u.n_blocks) {
-                if (j == 0) nxt = record(i + 1, 0, e_own);
-                else if (j == 1) nxt = rec[2];  // (after two shifts: the record of the queue's last piece)
-                else nxt = record(i + 1, 1, e_oth);
-                load_part(part[2], nxt, hf, hq);
-            }
-            rec[0] = rec[1];
-            rec[1] = rec[2];
-            rec[2] = nxt;
-            if (j == 2 && i + 2 < u.n_blocks) {
-                e_own = entry(i + 2, 0);
-                e_oth = entry(i + 2, 1);
-            }
-            if (++j == 3) j = 0, ++i;
             if (++slot == kSlots) slot = 0, ++turn;
+            return true;
+        };
+#pragma unroll 1
+        for (int i = 0; i < u.n_blocks; ++i) {
+            // which own candidates exist (rows 8 warp .. of this warp)
+            const uint32_t have = __ballot_sync(0xffffffffu, rec_own != nullptr);
+            if (lane == 0) {
+                uint32_t byte = 0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) byte |= ((have >> (4 * q)) & 1u) << q;
+                reinterpret_cast<uint8_t *>(&s.vmask[i % kMaskRing])[warp] = (uint8_t)byte;
+                ptx::mbar_arrive(&s.mask_full[i % kMaskRing]);
+            }
+            const bool v_own = rec_own != nullptr, v_peer = rec_peer != nullptr;
+            const bool more = i + 1 < u.n_blocks;
+            if (more) {
+                rec_own = record(i + 1, 0, entry[0], page[0]);
+                rec_peer = record(i + 1, 1, entry[1], page[1]);
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    entry[o] = next_entry[o];
+                    if (i + 2 < u.n_blocks) page[o] = load_page(i + 2, o, entry[o]);
+                    if (i + 3 < u.n_blocks) next_entry[o] = load_entry(i + 3, o);
+                }
+            }
+            // each part is unpacked and then loaded again, for the next block
+            if (!put(oth, v_own, rank ^ 1)) { fail(); break; }
+            if (more) load_part(oth, rec_own, rank ^ 1, hq);
+            if (!put(own, v_own, rank)) { fail(); break; }
+            if (more) load_part(own, rec_own, rank, hq);
+            if (!put(peer, v_peer, rank)) { fail(); break; }
+            if (more) load_part(peer, rec_peer, rank, hq);
         }
-        (void)ok;
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescQK = ptx::idesc_f32acc(1, 1, 128, kChunk);
@@ -469,10 +491,12 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (!wait(&s.p_full, ph)) { fail(); ok = false; break; }
                 ptx::tc_fence_after();
                 pv(s.p, s.x[t % kSlots], i == 1);
-                if (leader) ptx::mma_commit(&s.x_empty[t % kSlots]);
+                if (leader) {
+                    ptx::mma_commit(&s.x_empty[t % kSlots]);
+                    ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
+                }
                 __syncwarp();
                 if (!full(t + 1) || !wait_peer(&s.pp_full, ph)) { fail(); ok = false; break; }
-                ptx::fence_proxy_async_smem();  // the other CTA's stores -> PV (async proxy) reads
                 ptx::tc_fence_after();
                 pv(s.pp, s.x[(t + 1) % kSlots], false);
                 if (leader) {
@@ -489,8 +513,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         if (!__all_sync(0xffffffffu, ptx::mbar_wait_drain(&s.mma_done, 0, kDrainWaitNs)))
             report_error(P.err, CSA_ERR_TIMEOUT);
         if (!ok || *abort) {
-            // given up: arrivals that were sent to the other CTA's barrier land
-            // long before this (bounded) pause ends
+            // given up: arrivals and copies that were sent to the other CTA (a few
+            // KB, microseconds) land long before this bounded pause ends
             const uint64_t t0 = ptx::globaltimer_ns();
             while (ptx::globaltimer_ns() - t0 < 100000ull) {}
         }
@@ -507,7 +531,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             __syncwarp();
             if (lane == 0) remote_arrive(peer_max_full + (i & 1) * 8);
         };
-        const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp), rank ^ 1) + h * 128;
+        const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp + quarter * 32 * 128), rank ^ 1);
         const uint32_t peer_pp_full = ptx::mapa(ptx::smem_u32(&s.pp_full), rank ^ 1);
         bool ok = true;
         if (u.n_blocks > 0) {
@@ -581,6 +605,21 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             // the pair's maxima: buffer i % 2 is free, since the other CTA sent
             // its maximum of block i - 1 after it had read that of block i - 2
             send(i, own);
+            // the weights with the reference as it stands, while the maxima travel
+            uint32_t w[kChunk / 2];
+            float sum;
+            auto weights = [&]() {
+                const float mref = (m == -INFINITY) ? 0.f : m;  // every z is -inf while m is (or they come again)
+                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < kChunk / 2; ++c) {
+                    const float p0 = ptx::ex2_approx(z[2 * c] - mref), p1 = ptx::ex2_approx(z[2 * c + 1] - mref);
+                    ps[c & 3] += p0 + p1;
+                    w[c] = pack_bf16(p0, p1);
+                }
+                sum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+            };
+            weights();
             if (!wait_peer(&s.max_full[i & 1], (i >> 1) & 1)) { fail(); ok = false; break; }
             const float mx = fmaxf(own, *reinterpret_cast<volatile float *>(&s.pmax[i & 1][h]));
             // Both CTAs' PV of block i - 1 is done: O holds the blocks before
@@ -610,29 +649,17 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 }
                 l *= alpha;
                 if (need) m = mx;
+                weights();
             }
-            const float mref = (m == -INFINITY) ? 0.f : m;  // every z is -inf while m is
-            float ps4[4] = {0.f, 0.f, 0.f, 0.f};
+            l += sum;
 #pragma unroll
-            for (int c8 = 0; c8 < kChunk / 8; ++c8) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float p0 = ptx::ex2_approx(z[8 * c8 + 2 * e] - mref);
-                    const float p1 = ptx::ex2_approx(z[8 * c8 + 2 * e + 1] - mref);
-                    ps4[e] += p0 + p1;
-                    w[e] = pack_bf16(p0, p1);
-                }
-                const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-                *sw128(s.p, h, c8) = v;
-                remote_store16(peer_pp + ((c8 ^ (h & 7)) << 4), v);
-            }
-            l += (ps4[0] + ps4[1]) + (ps4[2] + ps4[3]);
-            ptx::fence_proxy_async_smem();  // own weights -> PV (async proxy) reads
+            for (int c8 = 0; c8 < kChunk / 8; ++c8)
+                *sw128(s.p, h, c8) = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
+            ptx::fence_proxy_async_smem();  // weights -> the copy's and PV's (async proxy) reads
             __syncwarp();
             if (lane == 0) {
+                copy_to_peer(peer_pp, s.p + quarter * 32 * 128, 32 * 128, peer_pp_full);
                 ptx::mbar_arrive(&s.p_full);
-                remote_arrive(peer_pp_full);
             }
         }
         // the pair's sums travel like one more block's maxima
