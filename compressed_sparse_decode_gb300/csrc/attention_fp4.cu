@@ -42,14 +42,19 @@ namespace {
 constexpr int kChunk = 64;                 // candidates of a block that a CTA owns
 constexpr int kBlock = 2 * kChunk;         // candidates a block
 constexpr int kHalf = 256;                 // output dims per CTA
-constexpr int kThreads = 416;              // 13 warps, see warp_role
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 8;              // load + unpack: warps 0..7, four threads a candidate
+constexpr int kSoftWarps = 8;              // softmax and epilogue: warps 8..15, two threads a head
+constexpr int kPtrWarp = 16;               // record pointers
+constexpr int kMmaWarp = 17;               // MMA issuer, TMEM owner
+constexpr int kThreads = 32 * 18;
+constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
-constexpr int kSlots = 5;
+constexpr int kSlots = 4;
 constexpr int kQTmemDims = 384;            // Q dims held in TMEM; the rest in shared memory
 constexpr int kQAtom = kHeads * 128;       // 64 dims of Q: 128 rows x 128 B
-constexpr int kMaskRing = 4;
+constexpr int kPtrRing = 4;                // blocks of resolved record pointers
+constexpr int kPieces = kHalf / 32 / 2;    // 32-column pieces of the output per softmax thread
 constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -65,10 +70,11 @@ struct AttSmem {
     alignas(1024) uint8_t qs[2 * kQAtom];      // Q dims 384..511
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
-    float pmax[2][kHeads];                     // written by the other CTA
-    uint64_t vmask[kMaskRing];                 // which own candidates of a block exist
-    uint64_t x_full[kSlots], x_empty[kSlots], mask_full[kMaskRing];
-    uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done;
+    float pmax[2][4][kHeads];                  // maxima: own CTA's halves, the other CTA's halves
+    const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
+    uint32_t vmask[kPtrRing][2];               // which own candidates exist
+    uint64_t x_full[kSlots], x_empty[kSlots], ptr_full[kPtrRing], ptr_empty[kPtrRing];
+    uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -209,7 +215,7 @@ struct Part {
     uint32_t power;
 };
 
-__device__ __forceinline__ uint2 load_code(const uint8_t *p) {
+__device__ __forceinline__ uint2 load8(const uint8_t *p) {
     uint2 v;
     asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
@@ -226,67 +232,60 @@ __device__ __forceinline__ void load_part(Part &a, const uint8_t *rec, int hf, i
     if (!rec) return;
     const uint8_t *c = rec + hf * 128 + 8 * hq;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) a.code[i] = load_code(c + 32 * i);
+    for (int i = 0; i < 3; ++i) a.code[i] = load8(c + 32 * i);
     a.scale = load16(rec + kFp4ScaleOffset + 16 * hf);
     if (hf == 0) {
-        const uint2 v = load_code(c + 96);
+        const uint2 v = load8(c + 96);
         a.last[0].x = v.x;
         a.last[0].y = v.y;
-        a.power = *reinterpret_cast<const uint32_t *>(rec + kFp4PowerOffset);
+        a.power = __ldg(reinterpret_cast<const uint32_t *>(rec + kFp4PowerOffset));
     } else {
         a.last[0] = load16(rec + kFp4RopeOffset + 32 * hq);
         a.last[1] = load16(rec + kFp4RopeOffset + 32 * hq + 16);
-        a.power = a.scale.w;
     }
 }
 
 // 8 E2M1 codes times s -> 8 BF16 values (exact).
-__device__ __forceinline__ uint4 unpack8(uint32_t w, float s) {
+__device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w >> (8 * i)), __NV_E2M1);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        o[i] = pack_bf16(v.x * s, v.y * s);
+        const float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2 *>(&h)), s);
+        o[i] = pack_bf16(v.x, v.y);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Unpacks a part into its row of a piece (rolled: the code of all warp roles
-// shares the schedulers' instruction caches).
-__device__ __forceinline__ void unpack_part(Part a, bool valid, int hf, int hq, int row, uint8_t *xs) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const float power = fp4_power(a.power & 0xFFu);
-    uint32_t sc[4] = {a.scale.x, a.scale.y, a.scale.z, a.scale.w};
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        uint4 lo = zero, hi = zero;
-        if (valid) {
-            if (i == 3 && hf == 1) {
-                lo = a.last[0];
-                hi = a.last[1];
-            } else {
-                const float s = e4m3x2_to_float2((uint16_t)((sc[0] >> (8 * hq)) & 0xFFu)).x * power;
-                lo = unpack8(a.code[0].x, s);
-                hi = unpack8(a.code[0].y, s);
-            }
-        }
-        *sw128(xs + i * kAtom, row, 2 * hq) = lo;
-        *sw128(xs + i * kAtom, row, 2 * hq + 1) = hi;
-        a.code[0] = a.code[1];
-        a.code[1] = a.code[2];
-        a.code[2] = make_uint2(a.last[0].x, a.last[0].y);
-        sc[0] = sc[1];
-        sc[1] = sc[2];
-        sc[2] = sc[3];
+// Unpacks a part into its row of a piece (unit i = column block i, 16-byte
+// chunks 2 hq and 2 hq + 1).
+__device__ __forceinline__ void unpack_part(const Part &a, bool valid, int hf, int hq, int row, uint8_t *xs) {
+    uint4 *lo = sw128(xs, row, 2 * hq), *hi = sw128(xs, row, 2 * hq + 1);
+    constexpr int kStep = kAtom / 16;
+    if (!valid) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lo[i * kStep] = hi[i * kStep] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const uint32_t sc[4] = {a.scale.x, a.scale.y, a.scale.z, a.scale.w};
+    const float power = fp4_power((hf ? a.scale.w : a.power) & 0xFFu);
+    auto unit = [&](uint2 code, int i) {
+        const float s = e4m3x2_to_float2((uint16_t)((sc[i] >> (8 * hq)) & 0xFFu)).x * power;
+        const float2 s2 = make_float2(s, s);
+        lo[i * kStep] = unpack8(code.x, s2);
+        hi[i * kStep] = unpack8(code.y, s2);
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i) unit(a.code[i], i);
+    if (hf == 0) {
+        unit(make_uint2(a.last[0].x, a.last[0].y), 3);
+    } else {
+        lo[3 * kStep] = a.last[0];
+        hi[3 * kStep] = a.last[1];
     }
 }
 
 // ---------------------------------------------------------------- the kernel
-
-// Warps: 0..7 load + unpack, 8 MMA issuer (and TMEM owner), 9..12 softmax and
-// epilogue (thread = head; a warp's TMEM lanes are 32 (warp % 4) ..).
-constexpr int kMmaWarp = 8;
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
@@ -301,14 +300,18 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_init(&s.x_full[i], kConvWarps);
             ptx::mbar_init(&s.x_empty[i], 1);
         }
-        for (int i = 0; i < kMaskRing; ++i) ptx::mbar_init(&s.mask_full[i], kConvWarps);
+        for (int i = 0; i < kPtrRing; ++i) {
+            ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
+            ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
+        }
         ptx::mbar_init(&s.s_full, 1);
-        ptx::mbar_init(&s.s_free, 4);
-        ptx::mbar_init(&s.p_full, 4);
+        ptx::mbar_init(&s.s_free, kSoftWarps);
+        ptx::mbar_init(&s.p_full, kSoftWarps);
         ptx::mbar_init(&s.pp_full, 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], 4);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], 2 * kSoftWarps);  // both CTAs' softmax warps
         ptx::mbar_init(&s.o_done, 2);  // both CTAs' PV of a block
-        ptx::mbar_init(&s.q_ready, 4);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&s.pair[i], 2);
+        ptx::mbar_init(&s.q_ready, kSoftWarps);
         ptx::mbar_init(&s.mma_done, 1);
         s.abort_flag = 0;
         ptx::fence_mbar_init();
@@ -333,63 +336,82 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         return __all_sync(0xffffffffu, wait_cluster(bar, parity, abort, P.wait_ns)) != 0;
     };
 
-    if (warp < kConvWarps) {
-        // ------------------------------------------------------------ load + unpack
-        const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
-        // Candidate `row` of the own (o = 0) or the other CTA's (o = 1) chunk of a
-        // block goes through three stages, one block apart, so that no stage
-        // waits for the load that it started: its entry (top-k list), its page
-        // (block table), its record (three pieces' worth of loads).
-        auto cand = [&](int i, int o) { return u.cb + i * kBlock + (o ? rank ^ 1 : rank) * kChunk + row; };
-        auto load_entry = [&](int i, int o) {
-            const int c = cand(i, o);
+    if (warp == kPtrWarp) {
+        // ------------------------------------------------------------ record pointers
+        // Lane L resolves candidates L, L + 32, .. of a block (own chunk first) in
+        // three stages, one block apart, so that no stage waits for the load it
+        // started: entry (top-k list), page (block table), record.
+        auto cand = [&](int i, int e) {
+            return u.cb + i * kBlock + (e < 2 ? rank : rank ^ 1) * kChunk + (e & 1) * 32 + lane;
+        };
+        auto load_entry = [&](int i, int e) {
+            const int c = cand(i, e);
             if (P.hca || c >= u.ce || c >= u.n_sel) return c;
             return __ldg(P.topk_idx + (size_t)u.r * P.k + c);
         };
-        // the physical page of entry e, -1 for none (0 without a block table)
-        auto load_page = [&](int i, int o, int e) {
-            const int c = cand(i, o);
+        // the physical page of an entry, -1 for none (0 without a block table)
+        auto load_page = [&](int i, int e, int entry) {
+            const int c = cand(i, e);
             if (c >= u.ce || c >= u.n_sel) return 0;
-            if (e < 0 || e >= P.comp.seq_capacity) return -1;
+            if (entry < 0 || entry >= P.comp.seq_capacity) return -1;
             if (!P.comp.block_table) return 0;
-            const int page = e / P.comp.page_records;
+            const int page = entry / P.comp.page_records;
             return page < P.comp.max_pages ? __ldg(P.comp.block_table + (int64_t)u.b * P.comp.max_pages + page) : -1;
         };
-        auto record = [&](int i, int o, int e, int page) -> const uint8_t * {
-            const int c = cand(i, o);
+        auto record = [&](int i, int e, int entry, int page) -> const uint8_t * {
+            const int c = cand(i, e);
             if (c >= u.ce) return nullptr;
             if (c >= u.n_sel) {
                 const int pos = u.j0 + (c - u.n_sel);
                 return P.ring + ((int64_t)u.b * P.R + pos % P.R) * kFp4Bytes;
             }
-            const int64_t ri = !P.comp.block_table ? (int64_t)u.b * P.comp.seq_stride + e
-                                                   : (int64_t)page * P.comp.page_records + e % P.comp.page_records;
+            const int64_t ri = P.comp.block_table ? (int64_t)page * P.comp.page_records + entry % P.comp.page_records
+                                                  : (int64_t)u.b * P.comp.seq_stride + entry;
             if (page >= 0 && ri < P.comp.n_records) return P.comp.base + ri * kFp4Bytes;
-            if (rank == 0 && hq == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+            if (rank == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
             return nullptr;
         };
+        int entry[4], page[4], next_entry[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) entry[e] = u.n_blocks > 0 ? load_entry(0, e) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) next_entry[e] = u.n_blocks > 1 ? load_entry(1, e) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) page[e] = u.n_blocks > 0 ? load_page(0, e, entry[e]) : 0;
+#pragma unroll 1
+        for (int i = 0; i < u.n_blocks; ++i) {
+            const int pr = i % kPtrRing;
+            if (!wait(&s.ptr_empty[pr], ((i / kPtrRing) & 1) ^ 1)) { fail(); break; }
+            uint32_t have[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint8_t *rec = record(i, e, entry[e], page[e]);
+                s.rec[pr][e * 32 + lane] = rec;
+                if (e < 2) have[e] = __ballot_sync(0xffffffffu, rec != nullptr);
+                entry[e] = next_entry[e];
+                if (i + 1 < u.n_blocks) page[e] = load_page(i + 1, e, entry[e]);
+                if (i + 2 < u.n_blocks) next_entry[e] = load_entry(i + 2, e);
+            }
+            if (lane == 0) {
+                s.vmask[pr][0] = have[0];
+                s.vmask[pr][1] = have[1];
+            }
+            ptx::mbar_arrive(&s.ptr_full[pr]);
+        }
+    } else if (warp < kConvWarps) {
+        // ------------------------------------------------------------ load + unpack
+        const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
         Part oth, own, peer;  // the three pieces of a block (see the top of the file)
         const uint8_t *rec_own = nullptr, *rec_peer = nullptr;
-        int entry[2] = {0, 0}, page[2] = {0, 0};
-        if (u.n_blocks > 0) {
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                entry[o] = load_entry(0, o);
-                page[o] = load_page(0, o, entry[o]);
-            }
-            rec_own = record(0, 0, entry[0], page[0]);
-            rec_peer = record(0, 1, entry[1], page[1]);
-            load_part(oth, rec_own, rank ^ 1, hq);
-            load_part(own, rec_own, rank, hq);
-            load_part(peer, rec_peer, rank, hq);
-        }
-        int next_entry[2];  // of the block after entry / page
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            if (u.n_blocks > 1) entry[o] = load_entry(1, o);
-            if (u.n_blocks > 2) next_entry[o] = load_entry(2, o);
-            if (u.n_blocks > 1) page[o] = load_page(1, o, entry[o]);
-        }
+        auto fetch = [&](int i) {  // the row's records of block i
+            const int pr = i % kPtrRing;
+            if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) return false;
+            rec_own = s.rec[pr][row];
+            rec_peer = s.rec[pr][kChunk + row];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
+            return true;
+        };
         int slot = 0, turn = 0;  // ring position of the next piece, and how often the ring has gone round
         auto put = [&](const Part &part, bool valid, int hf) {
             if (!wait(&s.x_empty[slot], (turn & 1) ^ 1)) return false;
@@ -400,29 +422,16 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             if (++slot == kSlots) slot = 0, ++turn;
             return true;
         };
+        bool ok = u.n_blocks == 0 || fetch(0);
+        if (!ok) fail();
+        load_part(oth, rec_own, rank ^ 1, hq);
+        load_part(own, rec_own, rank, hq);
+        load_part(peer, rec_peer, rank, hq);
 #pragma unroll 1
-        for (int i = 0; i < u.n_blocks; ++i) {
-            // which own candidates exist (rows 8 warp .. of this warp)
-            const uint32_t have = __ballot_sync(0xffffffffu, rec_own != nullptr);
-            if (lane == 0) {
-                uint32_t byte = 0;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) byte |= ((have >> (4 * q)) & 1u) << q;
-                reinterpret_cast<uint8_t *>(&s.vmask[i % kMaskRing])[warp] = (uint8_t)byte;
-                ptx::mbar_arrive(&s.mask_full[i % kMaskRing]);
-            }
+        for (int i = 0; i < u.n_blocks && ok; ++i) {
             const bool v_own = rec_own != nullptr, v_peer = rec_peer != nullptr;
             const bool more = i + 1 < u.n_blocks;
-            if (more) {
-                rec_own = record(i + 1, 0, entry[0], page[0]);
-                rec_peer = record(i + 1, 1, entry[1], page[1]);
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    entry[o] = next_entry[o];
-                    if (i + 2 < u.n_blocks) page[o] = load_page(i + 2, o, entry[o]);
-                    if (i + 3 < u.n_blocks) next_entry[o] = load_entry(i + 3, o);
-                }
-            }
+            if (more && !fetch(i + 1)) { fail(); break; }
             // each part is unpacked and then loaded again, for the next block
             if (!put(oth, v_own, rank ^ 1)) { fail(); break; }
             if (more) load_part(oth, rec_own, rank ^ 1, hq);
@@ -520,36 +529,43 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         }
     } else {
         // ------------------------------------------------------------ softmax / epilogue
-        const int quarter = warp & 3;
+        // Two threads a head: warps 8..11 the first half of the block's scores (and
+        // of the output columns), warps 12..15 the second; a warp's TMEM lanes
+        // are 32 (warp % 4) ..
+        const int quarter = warp & 3, half = (warp - kConvWarps) >> 2;
         const int h = quarter * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-        const uint32_t peer_max = ptx::mapa(ptx::smem_u32(&s.pmax[0][h]), rank ^ 1);
+        const uint32_t peer_max = ptx::mapa(ptx::smem_u32(&s.pmax[0][2 + half][h]), rank ^ 1);
         const uint32_t peer_max_full = ptx::mapa(ptx::smem_u32(&s.max_full[0]), rank ^ 1);
-        // this block's maximum (or, at the end, the sum) to the other CTA
-        auto send = [&](int i, float v) {
-            remote_store(peer_max + (i & 1) * (kHeads * 4), v);
-            __syncwarp();
-            if (lane == 0) remote_arrive(peer_max_full + (i & 1) * 8);
-        };
-        const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp + quarter * 32 * 128), rank ^ 1);
+        const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp), rank ^ 1);
         const uint32_t peer_pp_full = ptx::mapa(ptx::smem_u32(&s.pp_full), rank ^ 1);
+        // this thread's maximum of block i (or, at the end, its sum) to the other
+        // three threads of the head
+        auto send = [&](int i, float v) {
+            remote_store(peer_max + (i & 1) * (4 * kHeads * 4), v);
+            s.pmax[i & 1][half][h] = v;
+            __syncwarp();
+            if (lane == 0) {
+                remote_arrive(peer_max_full + (i & 1) * 8);
+                ptx::mbar_arrive(&s.max_full[i & 1]);
+            }
+        };
+        auto received = [&](int i, int from) { return *reinterpret_cast<volatile float *>(&s.pmax[i & 1][from][h]); };
         bool ok = true;
         if (u.n_blocks > 0) {
             // Q: dims from kQTmemDims up -> shared memory, the dims below -> TMEM
-            // (BF16 pairs, lane = head), 64 dims a piece, two pieces in flight
+            // (BF16 pairs, lane = head), 64 dims a piece; half the pieces a thread
             const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + ((size_t)u.r * kHeads + h) * kDim);
             const uint64_t policy = ptx::l2_policy_evict_first();
 #pragma unroll
-            for (int c = 0; c < (kDim - kQTmemDims) / 8; ++c)
-                ptx::cp_async_16_hint(sw128(s.qs + (c >> 3) * kQAtom, h, c & 7), qg + kQTmemDims / 8 + c, policy);
+            for (int c = 0; c < 8; ++c)
+                ptx::cp_async_16_hint(sw128(s.qs + half * kQAtom, h, c), qg + kQTmemDims / 8 + 8 * half + c, policy);
             ptx::cp_async_commit();
-            constexpr int kQPieces = kQTmemDims / 64;
-            uint4 wa[8], wb[8];
-            auto load_piece = [&](uint4 (&w)[8], int pc) {
+#pragma unroll 1
+            for (int pc = 3 * half; pc < 3 * half + 3; ++pc) {
+                uint4 w[8];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) w[v] = ptx::ldg_v4_policy(qg + pc * 8 + v, policy);
-            };
-            auto store_piece = [&](const uint4 (&w)[8], int pc) {
                 uint32_t regs[32];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) {
@@ -559,15 +575,6 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                     regs[4 * v + 3] = w[v].w;
                 }
                 ptx::tmem_st32(lane_base + kColQ + pc * 32, regs);
-            };
-            load_piece(wa, 0);
-            load_piece(wb, 1);
-#pragma unroll 1
-            for (int pc = 0; pc < kQPieces; pc += 2) {
-                store_piece(wa, pc);
-                if (pc + 2 < kQPieces) load_piece(wa, pc + 2);
-                store_piece(wb, pc + 1);
-                if (pc + 3 < kQPieces) load_piece(wb, pc + 3);
             }
             ptx::cp_async_wait<0>();
             ptx::tmem_st_wait();
@@ -579,49 +586,56 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         float m = -INFINITY, l = 0.f;  // reference and own sum, log2 domain, sink not included
 #pragma unroll 1
         for (int i = 0; i < u.n_blocks; ++i) {
-            if (!wait(&s.mask_full[i % kMaskRing], (i / kMaskRing) & 1)) { fail(); ok = false; break; }
-            const uint64_t mask = *reinterpret_cast<volatile uint64_t *>(&s.vmask[i % kMaskRing]);
+            const int pr = i % kPtrRing;
+            if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) { fail(); ok = false; break; }
+            const uint32_t mask = *reinterpret_cast<volatile uint32_t *>(&s.vmask[pr][half]);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
             if (!wait(&s.s_full, i & 1)) { fail(); ok = false; break; }
             ptx::tc_fence_after();
-            float z[kChunk];
+            float z[kSoftCols];  // raw scores, -inf where there is no candidate
             {
-                uint32_t sa[32], sb[32];
-                ptx::tmem_ld32(lane_base + kColS, sa);
-                ptx::tmem_ld32(lane_base + kColS + 32, sb);
+                uint32_t sv[kSoftCols];
+                ptx::tmem_ld32(lane_base + kColS + half * kSoftCols, sv);
                 ptx::tmem_ld_wait();
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&s.s_free);
 #pragma unroll
-                for (int c = 0; c < kChunk; ++c) {
-                    const float sv = __uint_as_float(c < 32 ? sa[c] : sb[c - 32]);
-                    z[c] = ((mask >> c) & 1ull) ? sv * P.scale_log2 : -INFINITY;
-                }
+                for (int c = 0; c < kSoftCols; ++c) z[c] = __uint_as_float(sv[c]);
+            }
+            if (mask != 0xffffffffu) {
+#pragma unroll
+                for (int c = 0; c < kSoftCols; ++c)
+                    if (!((mask >> c) & 1u)) z[c] = -INFINITY;
             }
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kChunk; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], z[c]);
-            const float own = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            // the pair's maxima: buffer i % 2 is free, since the other CTA sent
-            // its maximum of block i - 1 after it had read that of block i - 2
+            for (int c = 0; c < kSoftCols; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], z[c]);
+            const float own = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * P.scale_log2;  // (scale > 0)
+            // buffer i % 2 is free: every thread of the head sent its maximum of
+            // block i - 1 after it had read those of block i - 2
             send(i, own);
             // the weights with the reference as it stands, while the maxima travel
-            uint32_t w[kChunk / 2];
+            uint32_t w[kSoftCols / 2];
             float sum;
             auto weights = [&]() {
                 const float mref = (m == -INFINITY) ? 0.f : m;  // every z is -inf while m is (or they come again)
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 sc = make_float2(P.scale_log2, P.scale_log2), mm = make_float2(-mref, -mref);
+                float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < kChunk / 2; ++c) {
-                    const float p0 = ptx::ex2_approx(z[2 * c] - mref), p1 = ptx::ex2_approx(z[2 * c + 1] - mref);
-                    ps[c & 3] += p0 + p1;
-                    w[c] = pack_bf16(p0, p1);
+                for (int c = 0; c < kSoftCols / 2; ++c) {
+                    float2 e = __ffma2_rn(make_float2(z[2 * c], z[2 * c + 1]), sc, mm);
+                    e.x = ptx::ex2_approx(e.x);
+                    e.y = ptx::ex2_approx(e.y);
+                    ps[c & 1] = __fadd2_rn(ps[c & 1], e);
+                    w[c] = pack_bf16(e.x, e.y);
                 }
-                sum = (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                sum = (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
             };
             weights();
             if (!wait_peer(&s.max_full[i & 1], (i >> 1) & 1)) { fail(); ok = false; break; }
-            const float mx = fmaxf(own, *reinterpret_cast<volatile float *>(&s.pmax[i & 1][h]));
+            const float mx = fmaxf(fmaxf(received(i, 0), received(i, 1)), fmaxf(received(i, 2), received(i, 3)));
             // Both CTAs' PV of block i - 1 is done: O holds the blocks before
             // this one, the own weights have been read here and copied there.
             if (i > 0) {
@@ -636,7 +650,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 const float alpha = need ? ptx::ex2_approx(m - mx) : 1.f;  // 0 when m = -inf
                 if (i > 0) {
 #pragma unroll 1
-                    for (int piece = 0; piece < kHalf / 32; ++piece) {
+                    for (int piece = half * kPieces; piece < half * kPieces + kPieces; ++piece) {
                         uint32_t o[32];
                         ptx::tmem_ld32(lane_base + kColO + piece * 32, o);
                         ptx::tmem_ld_wait();
@@ -653,16 +667,32 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             }
             l += sum;
 #pragma unroll
-            for (int c8 = 0; c8 < kChunk / 8; ++c8)
-                *sw128(s.p, h, c8) = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
+            for (int c8 = 0; c8 < kSoftCols / 8; ++c8)
+                *sw128(s.p, h, half * (kSoftCols / 8) + c8) = make_uint4(w[4 * c8], w[4 * c8 + 1], w[4 * c8 + 2], w[4 * c8 + 3]);
             ptx::fence_proxy_async_smem();  // weights -> the copy's and PV's (async proxy) reads
+            // two warps (the halves) fill the rows of a quarter; the first of them
+            // copies it (4 KB) when both have
             __syncwarp();
             if (lane == 0) {
-                copy_to_peer(peer_pp, s.p + quarter * 32 * 128, 32 * 128, peer_pp_full);
                 ptx::mbar_arrive(&s.p_full);
+                ptx::mbar_arrive(&s.pair[quarter]);
+            }
+            if (half == 0) {
+                if (!wait(&s.pair[quarter], i & 1)) { fail(); ok = false; break; }
+                if (lane == 0)
+                    copy_to_peer(peer_pp + quarter * 32 * 128, s.p + quarter * 32 * 128, 32 * 128, peer_pp_full);
             }
         }
-        // the pair's sums travel like one more block's maxima
+        // both halves' warps of a quarter have staged their output columns (the
+        // phase before this one is complete: the sums came after it)
+        auto rows_staged = [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.pair[quarter]);
+            if (wait(&s.pair[quarter], u.n_blocks & 1)) return true;
+            fail();
+            return false;
+        };
+        // the sums travel like one more block's maxima; added in one order by all
         if (ok && u.n_blocks > 0) {
             const int i = u.n_blocks;
             send(i, l);
@@ -670,7 +700,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 fail();
                 ok = false;
             } else {
-                l += *reinterpret_cast<volatile float *>(&s.pmax[i & 1][h]);
+                const float here = received(i, 0) + received(i, 1), there = received(i, 2) + received(i, 3);
+                l = here + there;
             }
             ptx::tc_fence_after();
         }
@@ -725,7 +756,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             if (!(final_out && P.out_fp4)) {
                 uint8_t *srow = ostage + h * (kHalf * 2);
 #pragma unroll 1
-                for (int piece = 0; piece < kHalf / 32; ++piece) {
+                for (int piece = half * kPieces; piece < half * kPieces + kPieces; ++piece) {
                     float v[32];
                     piece_values(piece, v);
 #pragma unroll
@@ -736,14 +767,14 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                                        pack_bf16(v[8 * q4 + 4], v[8 * q4 + 5]), pack_bf16(v[8 * q4 + 6], v[8 * q4 + 7]));
                     }
                 }
-                __syncwarp();
+                const bool staged = rows_staged();
                 const uint64_t policy = ptx::l2_policy_evict_first();
                 __nv_bfloat16 *dst0 = final_out
                                           ? P.out + (size_t)r * kHeads * kDim + rank * kHalf
                                           : P.part_o + ((size_t)r * P.n_split + u.split) * kHeads * kDim + rank * kHalf;
 #pragma unroll 4
-                for (int i = 0; i < 32; ++i) {
-                    const int hr = quarter * 32 + i;  // a head row of this warp
+                for (int i = 0; i < 16 && staged; ++i) {
+                    const int hr = quarter * 32 + 16 * half + i;  // a head row of this warp pair
                     const uint4 v = *reinterpret_cast<const uint4 *>(ostage + hr * (kHalf * 2) + ((lane ^ (hr & 7)) << 4));
                     if (final_out)
                         reinterpret_cast<uint4 *>(dst0 + (size_t)hr * kDim)[lane] = v;
@@ -754,8 +785,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 // E2M1: two 128-dim blocks per half, each scaled by its amax / 6
                 // (a first pass over TMEM finds the amax); 128 B per head row
                 uint8_t *frow = ostage + h * (kFp4RowBytes / 2);
-#pragma unroll 1
-                for (int bl = 0; bl < 2; ++bl) {
+                {
+                    const int bl = half;
                     float amax = 0.f;
 #pragma unroll 1
                     for (int pp = 0; pp < 4; ++pp) {
@@ -782,17 +813,17 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                     }
                     P.out_fp4_scale[((size_t)r * kHeads + h) * 4 + rank * 2 + bl] = sc;
                 }
-                __syncwarp();
+                const bool staged = rows_staged();
 #pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int hr = quarter * 32 + i * 4 + (lane >> 3);  // 8 lanes per 128-byte row
+                for (int i = 0; i < 4 && staged; ++i) {
+                    const int hr = quarter * 32 + 16 * half + i * 4 + (lane >> 3);  // 8 lanes per 128-byte row
                     const int c = lane & 7;
                     const uint4 v = *reinterpret_cast<const uint4 *>(ostage + hr * (kFp4RowBytes / 2) + ((c ^ (hr & 7)) << 4));
                     reinterpret_cast<uint4 *>(P.out_fp4 + ((size_t)r * kHeads + hr) * kFp4RowBytes +
                                               rank * (kFp4RowBytes / 2))[c] = v;
                 }
             }
-            if (rank == 0) {
+            if (rank == 0 && half == 0) {
                 if (final_out)
                     P.lse[(size_t)r * kHeads + h] = lse_out;
                 else
