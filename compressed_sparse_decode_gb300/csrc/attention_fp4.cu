@@ -387,6 +387,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             for (int e = 0; e < 4; ++e) {
                 const uint8_t *rec = record(i, e, entry[e], page[e]);
                 s.rec[pr][e * 32 + lane] = rec;
+                // into L2 while the block is up to kPtrRing blocks away (each CTA
+                // its own candidates: the pair reads both)
+                if (e < 2 && rec) ptx::prefetch_l2_bulk(rec, kFp4Bytes);
                 if (e < 2) have[e] = __ballot_sync(0xffffffffu, rec != nullptr);
                 entry[e] = next_entry[e];
                 if (i + 1 < u.n_blocks) page[e] = load_page(i + 1, e, entry[e]);
