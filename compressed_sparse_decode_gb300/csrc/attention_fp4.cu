@@ -27,10 +27,12 @@
 //
 // Latents are unpacked by eight warps from 4-bit records in global memory
 // (through registers, one block ahead) to BF16 in shared memory, exactly (see
-// csa_format_t), in pieces of 64 candidates x 256 dims (32 KB): piece 3i = the
-// other CTA's dims of the own candidates of block i (read by QK only), 3i + 1 =
-// the own dims of the own candidates (QK and PV), 3i + 2 = the own dims of the
-// other CTA's candidates (PV). The pieces go round a ring of kSlots buffers.
+// csa_format_t), in pieces of 64 candidates x 256 dims (32 KB): "oth", the
+// other CTA's dims of the own candidates (read by QK only), "own", the own dims
+// of the own candidates (QK and PV), and "peer", the own dims of the other
+// CTA's candidates (PV only). They are unpacked in the order oth(i + 1),
+// own(i + 1), peer(i), so that the scores of a block come before the weights of
+// the block before it are spent; own has two buffers.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -50,6 +52,7 @@ constexpr int kThreads = 32 * 18;
 constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
+constexpr int kOth = 0, kOwn = 1, kPeer = 3;  // buffers of the three kinds of pieces (own: 1 + block % 2)
 constexpr int kSlots = 4;
 constexpr int kQTmemDims = 384;            // Q dims held in TMEM; the rest in shared memory
 constexpr int kQAtom = kHeads * 128;       // 64 dims of Q: 128 rows x 128 B
@@ -415,14 +418,14 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
             return true;
         };
-        int slot = 0, turn = 0;  // ring position of the next piece, and how often the ring has gone round
-        auto put = [&](const Part &part, bool valid, int hf) {
-            if (!wait(&s.x_empty[slot], (turn & 1) ^ 1)) return false;
+        // Unpacks a piece; then its part is loaded again, for the next block.
+        auto put = [&](Part &part, bool valid, int hf, int slot, int use, bool more, const uint8_t *next) {
+            if (!wait(&s.x_empty[slot], (use & 1) ^ 1)) return false;
             unpack_part(part, valid, hf, hq, row, s.x[slot]);
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.x_full[slot]);
-            if (++slot == kSlots) slot = 0, ++turn;
+            if (more) load_part(part, next, hf, hq);
             return true;
         };
         bool ok = u.n_blocks == 0 || fetch(0);
@@ -430,18 +433,22 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         load_part(oth, rec_own, rank ^ 1, hq);
         load_part(own, rec_own, rank, hq);
         load_part(peer, rec_peer, rank, hq);
+        bool v_peer = false;  // of the block before
 #pragma unroll 1
-        for (int i = 0; i < u.n_blocks && ok; ++i) {
-            const bool v_own = rec_own != nullptr, v_peer = rec_peer != nullptr;
-            const bool more = i + 1 < u.n_blocks;
-            if (more && !fetch(i + 1)) { fail(); break; }
-            // each part is unpacked and then loaded again, for the next block
-            if (!put(oth, v_own, rank ^ 1)) { fail(); break; }
-            if (more) load_part(oth, rec_own, rank ^ 1, hq);
-            if (!put(own, v_own, rank)) { fail(); break; }
-            if (more) load_part(own, rec_own, rank, hq);
-            if (!put(peer, v_peer, rank)) { fail(); break; }
-            if (more) load_part(peer, rec_peer, rank, hq);
+        for (int i = 0; i <= u.n_blocks && ok; ++i) {
+            const bool v_own = rec_own != nullptr, v_next = rec_peer != nullptr;
+            const uint8_t *peer_rec = rec_peer;
+            if (i < u.n_blocks) {
+                const bool more = i + 1 < u.n_blocks;
+                if (more && !fetch(i + 1)) { fail(); break; }
+                if (!put(oth, v_own, rank ^ 1, kOth, i, more, rec_own) ||
+                    !put(own, v_own, rank, kOwn + (i & 1), i >> 1, more, rec_own)) {
+                    fail();
+                    break;
+                }
+            }
+            if (i >= 1 && !put(peer, v_peer, rank, kPeer, i - 1, i < u.n_blocks, peer_rec)) { fail(); break; }
+            v_peer = v_next;
         }
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
@@ -479,7 +486,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 mma_ss(leader, tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
                        !(first && k == 0));
         };
-        auto full = [&](int t) { return wait(&s.x_full[t % kSlots], (t / kSlots) & 1); };
+        auto full = [&](int slot, int use) { return wait(&s.x_full[slot], use & 1); };
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
             if (i < u.n_blocks) {
@@ -487,32 +494,32 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (i >= 1 && !wait(&s.s_free, (i - 1) & 1)) { fail(); ok = false; break; }
 #pragma unroll 1
                 for (int own = 0; own < 2; ++own) {
-                    const int t = 3 * i + own;
-                    if (!full(t)) { fail(); ok = false; break; }
+                    const int slot = own ? kOwn + (i & 1) : kOth;
+                    if (!full(slot, own ? i >> 1 : i)) { fail(); ok = false; break; }
                     ptx::tc_fence_after();
-                    qk_half(rank ^ own ^ 1, s.x[t % kSlots], own == 0);
-                    if (leader) ptx::mma_commit(own ? &s.s_full : &s.x_empty[t % kSlots]);
+                    qk_half(rank ^ own ^ 1, s.x[slot], own == 0);
+                    if (leader) ptx::mma_commit(own ? &s.s_full : &s.x_empty[slot]);
                     __syncwarp();
                 }
                 if (!ok) break;
             }
             if (i >= 1) {
                 // PV(i - 1): own candidates, then the other CTA's
-                const int t = 3 * (i - 1) + 1;
+                const int slot = kOwn + ((i - 1) & 1);
                 const uint32_t ph = (i - 1) & 1;
                 if (!wait(&s.p_full, ph)) { fail(); ok = false; break; }
                 ptx::tc_fence_after();
-                pv(s.p, s.x[t % kSlots], i == 1);
+                pv(s.p, s.x[slot], i == 1);
                 if (leader) {
-                    ptx::mma_commit(&s.x_empty[t % kSlots]);
+                    ptx::mma_commit(&s.x_empty[slot]);
                     ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
                 }
                 __syncwarp();
-                if (!full(t + 1) || !wait_peer(&s.pp_full, ph)) { fail(); ok = false; break; }
+                if (!full(kPeer, i - 1) || !wait_peer(&s.pp_full, ph)) { fail(); ok = false; break; }
                 ptx::tc_fence_after();
-                pv(s.pp, s.x[(t + 1) % kSlots], false);
+                pv(s.pp, s.x[kPeer], false);
                 if (leader) {
-                    ptx::mma_commit(&s.x_empty[(t + 1) % kSlots]);
+                    ptx::mma_commit(&s.x_empty[kPeer]);
                     commit_both(&s.o_done);
                 }
                 __syncwarp();
