@@ -25,14 +25,18 @@
 // other's decision. The weights are computed with the old reference while the
 // maxima travel.
 //
-// Latents are unpacked by eight warps from 4-bit records in global memory
-// (through registers, one block ahead) to BF16 in shared memory, exactly (see
-// csa_format_t), in pieces of 64 candidates x 256 dims (32 KB): "oth", the
+// Latents come as three kinds of pieces of 64 candidates x 256 dims: "oth", the
 // other CTA's dims of the own candidates (read by QK only), "own", the own dims
 // of the own candidates (QK and PV), and "peer", the own dims of the other
-// CTA's candidates (PV only). They are unpacked in the order oth(i + 1),
-// own(i + 1), peer(i), so that the scores of a block come before the weights of
-// the block before it are spent; own has two buffers.
+// CTA's candidates (PV only). A pointer warp resolves the records; eight warps copy the
+// pieces' bytes into staging (cp.async, pieces ahead; a cp.async.bulk a record
+// took 80 cycles each, 2.5 times this kernel's time) and unpack them, exactly (see csa_format_t), to BF16 in the MMA's layout, one
+// 32 KB buffer a kind. Order of a block: oth(i + 1), peer(i), own(i + 1), and
+// QK(i + 1) over oth, PV(i), QK(i + 1) over own: the chain own -> QK -> softmax ->
+// PV -> own of the next block sets the pace, the rest runs beside it.
+// Every role's loop is kept short and every helper at one place: the instruction
+// caches are shared by all warps and by neighbouring SMs (a second copy of the
+// unpacking, one per rank, cost 9 %).
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -52,8 +56,12 @@ constexpr int kThreads = 32 * 18;
 constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
-constexpr int kOth = 0, kOwn = 1, kPeer = 3;  // buffers of the three kinds of pieces (own: 1 + block % 2)
-constexpr int kSlots = 4;
+constexpr int kOth = 0, kOwn = 1, kPeer = 2, kKinds = 3;
+// Staged bytes of a row of a piece. Lower half: codes 0..127, then bytes 352..383
+// (scales and power); upper half: bytes 128..383 (codes, rope dims, scales,
+// power). The strides put a warp's 8-byte reads of four rows in 32 different banks.
+constexpr int kLoCodes = 128, kLoStride = 160, kHiStride = 288;
+constexpr int kStageBytes = kChunk * (kLoStride + 2 * kHiStride);  // the larger rank's three pieces
 constexpr int kQTmemDims = 384;            // Q dims held in TMEM; the rest in shared memory
 constexpr int kQAtom = kHeads * 128;       // 64 dims of Q: 128 rows x 128 B
 constexpr int kPtrRing = 4;                // blocks of resolved record pointers
@@ -69,14 +77,15 @@ constexpr uint32_t kColO = 256;  // 256 columns: O half, fp32
 constexpr uint32_t kTmemCols = 512;
 
 struct AttSmem {
-    alignas(1024) uint8_t x[kSlots][kPieceBytes];
+    alignas(1024) uint8_t x[kKinds][kPieceBytes];
     alignas(1024) uint8_t qs[2 * kQAtom];      // Q dims 384..511
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
     float pmax[2][4][kHeads];                  // maxima: own CTA's halves, the other CTA's halves
+    alignas(16) uint8_t stage[kStageBytes];
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
-    uint64_t x_full[kSlots], x_empty[kSlots], ptr_full[kPtrRing], ptr_empty[kPtrRing];
+    uint64_t x_full[kKinds], x_empty[kKinds], ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint32_t tmem_base;
     int abort_flag;
@@ -201,52 +210,14 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// ptx::mbar_wait for a barrier that the other CTA arrives on.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
-    if (!ptx::mbar_wait(bar, parity, abort, limit_ns)) return false;
-    return try_wait_cluster(bar, parity);  // (complete: returns at once) orders the other CTA's writes
+// Bounded wait of a whole warp: true when the phase is complete for every lane,
+// and what the other CTA stored before it arrived is visible. One (suspending)
+// try is in line, the rest out of it: see above on code size.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, limit_ns) && try_wait_cluster(bar, parity)) != 0;
 }
 
 // ---------------------------------------------------------------- unpacking
-
-// A thread's part of one piece of a record: four units of 16 dims, unit 4 i + hq
-// of the half (i < 4). The last unit of the upper half is 16 rope dims.
-struct Part {
-    uint2 code[3];
-    uint4 last[2];   // lower half: the fourth unit's codes in last[0].x, .y; upper half: rope dims
-    uint4 scale;     // byte hq of word i: the scale of unit i (upper half: word 3 = the power)
-    uint32_t power;
-};
-
-__device__ __forceinline__ uint2 load8(const uint8_t *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint4 load16(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
-__device__ __forceinline__ void load_part(Part &a, const uint8_t *rec, int hf, int hq) {
-    if (!rec) return;
-    const uint8_t *c = rec + hf * 128 + 8 * hq;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) a.code[i] = load8(c + 32 * i);
-    a.scale = load16(rec + kFp4ScaleOffset + 16 * hf);
-    if (hf == 0) {
-        const uint2 v = load8(c + 96);
-        a.last[0].x = v.x;
-        a.last[0].y = v.y;
-        a.power = __ldg(reinterpret_cast<const uint32_t *>(rec + kFp4PowerOffset));
-    } else {
-        a.last[0] = load16(rec + kFp4RopeOffset + 32 * hq);
-        a.last[1] = load16(rec + kFp4RopeOffset + 32 * hq + 16);
-    }
-}
 
 // 8 E2M1 codes times s -> 8 BF16 values (exact).
 __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
@@ -260,31 +231,34 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Unpacks a part into its row of a piece (unit i = column block i, 16-byte
-// chunks 2 hq and 2 hq + 1).
-__device__ __forceinline__ void unpack_part(const Part &a, bool valid, int hf, int hq, int row, uint8_t *xs) {
-    uint4 *lo = sw128(xs, row, 2 * hq), *hi = sw128(xs, row, 2 * hq + 1);
+// Unpacks a thread's quarter of a staged row: units i < 4 of 16 dims, codes at
+// code + 32 i, scale byte at scale + 4 i, to column block i, 16-byte chunks 2 hq
+// and 2 hq + 1. `rope`: the last unit is 16 rope dims, copied as they are.
+__device__ __forceinline__ void unpack_row(const uint8_t *code, const uint8_t *scale, const uint8_t *power,
+                                           const uint8_t *rope, bool valid, uint4 *lo, uint4 *hi) {
     constexpr int kStep = kAtom / 16;
-    if (!valid) {
+    const float pw = valid ? fp4_power(*power) : 0.f;
+#pragma unroll 1
+    for (int i = 0; i < 4; i += 2) {
+        uint2 c[2];
+        uint32_t sb[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lo[i * kStep] = hi[i * kStep] = make_uint4(0, 0, 0, 0);
-        return;
-    }
-    const uint32_t sc[4] = {a.scale.x, a.scale.y, a.scale.z, a.scale.w};
-    const float power = fp4_power((hf ? a.scale.w : a.power) & 0xFFu);
-    auto unit = [&](uint2 code, int i) {
-        const float s = e4m3x2_to_float2((uint16_t)((sc[i] >> (8 * hq)) & 0xFFu)).x * power;
-        const float2 s2 = make_float2(s, s);
-        lo[i * kStep] = unpack8(code.x, s2);
-        hi[i * kStep] = unpack8(code.y, s2);
-    };
+        for (int e = 0; e < 2; ++e) {
+            c[e] = *reinterpret_cast<const uint2 *>(code + 32 * (i + e));
+            sb[e] = scale[4 * (i + e)];
+        }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) unit(a.code[i], i);
-    if (hf == 0) {
-        unit(make_uint2(a.last[0].x, a.last[0].y), 3);
-    } else {
-        lo[3 * kStep] = a.last[0];
-        hi[3 * kStep] = a.last[1];
+        for (int e = 0; e < 2; ++e) {
+            const float s = e4m3x2_to_float2((uint16_t)sb[e]).x * pw;
+            uint4 l = unpack8(c[e].x, make_float2(s, s)), h = unpack8(c[e].y, make_float2(s, s));
+            if (e == 1 && i == 2 && rope) {
+                l = *reinterpret_cast<const uint4 *>(rope);
+                h = *reinterpret_cast<const uint4 *>(rope + 16);
+            }
+            if (!valid) l = h = make_uint4(0, 0, 0, 0);  // (whatever the staging held)
+            lo[(i + e) * kStep] = l;
+            hi[(i + e) * kStep] = h;
+        }
     }
 }
 
@@ -299,9 +273,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     volatile int *abort = &s.abort_flag;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            ptx::mbar_init(&s.x_full[i], kConvWarps);
-            ptx::mbar_init(&s.x_empty[i], 1);
+        for (int k = 0; k < kKinds; ++k) {
+            ptx::mbar_init(&s.x_full[k], kConvWarps);
+            ptx::mbar_init(&s.x_empty[k], 1);
         }
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
@@ -332,11 +306,18 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         report_error(P.err, CSA_ERR_TIMEOUT);
         *abort = 1;
     };
+    const bool poll = P.wait_ns < ptx::kPollOnlyBelowNs;  // (a diagnostic limit: no suspension outlasts it)
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, P.wait_ns)) != 0;
+        const bool now = poll ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity);
+        return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
     };
     auto wait_peer = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_cluster(bar, parity, abort, P.wait_ns)) != 0;
+        const bool now = !poll && try_wait_cluster(bar, parity);
+        return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
+    };
+    auto stage_of = [&](int k) {
+        const int oth = rank ? kLoStride : kHiStride, own = rank ? kHiStride : kLoStride;
+        return s.stage + kChunk * (k == kOth ? 0 : k == kOwn ? oth : oth + own);
     };
 
     if (warp == kPtrWarp) {
@@ -405,58 +386,78 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_arrive(&s.ptr_full[pr]);
         }
     } else if (warp < kConvWarps) {
-        // ------------------------------------------------------------ load + unpack
+        // ------------------------------------------------------------ copy + unpack
         const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
-        Part oth, own, peer;  // the three pieces of a block (see the top of the file)
-        const uint8_t *rec_own = nullptr, *rec_peer = nullptr;
-        auto fetch = [&](int i) {  // the row's records of block i
-            const int pr = i % kPtrRing;
-            if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) return false;
-            rec_own = s.rec[pr][row];
-            rec_peer = s.rec[pr][kChunk + row];
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
-            return true;
-        };
-        // Unpacks a piece; then its part is loaded again, for the next block.
-        auto put = [&](Part &part, bool valid, int hf, int slot, int use, bool more, const uint8_t *next) {
-            if (!wait(&s.x_empty[slot], (use & 1) ^ 1)) return false;
-            unpack_part(part, valid, hf, hq, row, s.x[slot]);
-            ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.x_full[slot]);
-            if (more) load_part(part, next, hf, hq);
-            return true;
-        };
-        bool ok = u.n_blocks == 0 || fetch(0);
-        if (!ok) fail();
-        load_part(oth, rec_own, rank ^ 1, hq);
-        load_part(own, rec_own, rank, hq);
-        load_part(peer, rec_peer, rank, hq);
-        bool v_peer = false;  // of the block before
-#pragma unroll 1
-        for (int i = 0; i <= u.n_blocks && ok; ++i) {
-            const bool v_own = rec_own != nullptr, v_next = rec_peer != nullptr;
-            const uint8_t *peer_rec = rec_peer;
+        // Pieces in the order oth(0) own(0) | oth(i) peer(i - 1) own(i) | .. | peer(n - 1).
+        // A row's four threads copy its bytes (16-byte pieces hq, hq + 4, ..) and
+        // unpack them; after a piece is unpacked the same kind of the next block
+        // is copied, so two pieces' copies are in flight behind the one waited for.
+        const uint64_t policy = ptx::l2_policy_evict_first();  // a pair reads a record within a block, nobody later
+        uint32_t valid = 0;  // bit k: the staged row of kind k is a record
+        auto upper_half = [&](int k) { return (k == kOth) != (rank == 1); };
+        auto staged = [&](int k) { return stage_of(k) + row * (upper_half(k) ? kHiStride : kLoStride); };
+        auto load = [&](int i, int k) {
             if (i < u.n_blocks) {
-                const bool more = i + 1 < u.n_blocks;
-                if (more && !fetch(i + 1)) { fail(); break; }
-                if (!put(oth, v_own, rank ^ 1, kOth, i, more, rec_own) ||
-                    !put(own, v_own, rank, kOwn + (i & 1), i >> 1, more, rec_own)) {
-                    fail();
-                    break;
+                const int pr = i % kPtrRing;
+                if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) return false;
+                const uint8_t *rec = s.rec[pr][k == kPeer ? kChunk + row : row];
+                if (k == kPeer) {  // the block's last look at its pointers
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
+                }
+                valid = rec ? valid | 1u << k : valid & ~(1u << k);
+                if (rec) {
+                    uint8_t *dst = staged(k) + 16 * hq;
+                    const bool upper = upper_half(k);
+                    const uint8_t *src = rec + (upper ? kLoCodes : 0) + 16 * hq;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (!upper && c == 2) src += kFp4ScaleOffset - kLoCodes;
+                        if (upper || c < 2 || (c == 2 && hq < 2)) ptx::cp_async_16_hint(dst + 64 * c, src + 64 * c, policy);
+                    }
                 }
             }
-            if (i >= 1 && !put(peer, v_peer, rank, kPeer, i - 1, i < u.n_blocks, peer_rec)) { fail(); break; }
-            v_peer = v_next;
+            ptx::cp_async_commit();
+            return true;
+        };
+        bool ok = true;
+#pragma unroll 1
+        for (int k = 0; k < kKinds && ok; ++k) ok = load(0, k);
+#pragma unroll 1
+        for (int step = 0, i = 0, k = kOth; step < 3 * u.n_blocks && ok; ++step) {
+            // groups issued after this piece's: two, but one at step 2 (oth(1))
+            if (step == 2) ptx::cp_async_wait<1>();
+            else ptx::cp_async_wait<2>();
+            __syncwarp();
+            if (!wait(&s.x_empty[k], (i & 1) ^ 1)) { ok = false; break; }
+            const bool upper = upper_half(k);
+            const uint8_t *base = staged(k);
+            unpack_row(base + 8 * hq, base + (upper ? kFp4ScaleOffset + 16 - kLoCodes : kLoCodes) + hq,
+                       base + (upper ? kFp4PowerOffset - kLoCodes : kLoCodes + kFp4PowerOffset - kFp4ScaleOffset),
+                       upper ? base + kFp4RopeOffset - kLoCodes + 32 * hq : nullptr, (valid >> k) & 1u,
+                       sw128(s.x[k], row, 2 * hq), sw128(s.x[k], row, 2 * hq + 1));
+            ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
+            __syncwarp();                   // (and the row's threads are done with the staging)
+            if (lane == 0) ptx::mbar_arrive(&s.x_full[k]);
+            if (!load(i + 1, k)) { ok = false; break; }
+            if (k == kOth) {
+                if (i == 0) k = kOwn;
+                else k = kPeer, --i;
+            } else if (k == kPeer) {
+                k = kOwn, ++i;
+            } else {
+                if (i + 1 < u.n_blocks) k = kOth, ++i;
+                else k = kPeer;
+            }
         }
+        if (!ok) fail();
+        ptx::cp_async_wait<0>();  // no copy lands after this warp has moved on
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescQK = ptx::idesc_f32acc(1, 1, 128, kChunk);
         constexpr uint32_t kIdescPV = ptx::idesc_f32acc(1, 1, 128, kHalf, 1);
         const uint32_t leader = elect_one();
         bool ok = u.n_blocks == 0 || wait(&s.q_ready, 0);
-        if (!ok) fail();
         const uint64_t qd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.qs));
         // the 16 K-steps of dims 256 hf ..: Q from TMEM below kQTmemDims, from
         // shared memory above
@@ -486,45 +487,36 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 mma_ss(leader, tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
                        !(first && k == 0));
         };
-        auto full = [&](int slot, int use) { return wait(&s.x_full[slot], use & 1); };
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
-            if (i < u.n_blocks) {
-                // QK(i): the dims that this CTA does not output first (unpacked first)
-                if (i >= 1 && !wait(&s.s_free, (i - 1) & 1)) { fail(); ok = false; break; }
+            const uint32_t ph = i & 1, before = ph ^ 1;
+            // QK(i) over oth | PV(i - 1) of the own, of the other CTA's candidates | QK(i) over own
 #pragma unroll 1
-                for (int own = 0; own < 2; ++own) {
-                    const int slot = own ? kOwn + (i & 1) : kOth;
-                    if (!full(slot, own ? i >> 1 : i)) { fail(); ok = false; break; }
-                    ptx::tc_fence_after();
-                    qk_half(rank ^ own ^ 1, s.x[slot], own == 0);
-                    if (leader) ptx::mma_commit(own ? &s.s_full : &s.x_empty[slot]);
-                    __syncwarp();
-                }
+            for (int part = 0; part < 4 && ok; ++part) {
+                const bool qk = part == 0 || part == 3;
+                if (qk ? i == u.n_blocks : i == 0) continue;
+                const int k = part == 0 ? kOth : part == 2 ? kPeer : kOwn;
+                if (part == 0) ok = wait(&s.x_full[k], ph) && (i == 0 || wait(&s.s_free, before));
+                else if (part == 1) ok = wait(&s.p_full, before);
+                else if (part == 2) ok = wait(&s.x_full[k], before) && wait_peer(&s.pp_full, before);
+                else ok = wait(&s.x_full[k], ph);
                 if (!ok) break;
-            }
-            if (i >= 1) {
-                // PV(i - 1): own candidates, then the other CTA's
-                const int slot = kOwn + ((i - 1) & 1);
-                const uint32_t ph = (i - 1) & 1;
-                if (!wait(&s.p_full, ph)) { fail(); ok = false; break; }
                 ptx::tc_fence_after();
-                pv(s.p, s.x[slot], i == 1);
-                if (leader) {
-                    ptx::mma_commit(&s.x_empty[slot]);
-                    ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
-                }
-                __syncwarp();
-                if (!full(kPeer, i - 1) || !wait_peer(&s.pp_full, ph)) { fail(); ok = false; break; }
-                ptx::tc_fence_after();
-                pv(s.pp, s.x[kPeer], false);
-                if (leader) {
-                    ptx::mma_commit(&s.x_empty[kPeer]);
-                    commit_both(&s.o_done);
+                if (qk) {
+                    qk_half(part == 0 ? rank ^ 1 : rank, s.x[k], part == 0);
+                    if (leader) ptx::mma_commit(part == 0 ? &s.x_empty[k] : &s.s_full);
+                } else {
+                    pv(part == 1 ? s.p : s.pp, s.x[k], i == 1 && part == 1);
+                    if (leader) {
+                        ptx::mma_commit(&s.x_empty[k]);
+                        if (part == 1) ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
+                        else commit_both(&s.o_done);
+                    }
                 }
                 __syncwarp();
             }
         }
+        if (!ok) fail();
         if (leader) ptx::mma_commit(&s.mma_done);
         __syncwarp();
         // every MMA issued has finished with tensor and shared memory before the
