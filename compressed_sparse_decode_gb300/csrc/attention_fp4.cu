@@ -28,9 +28,9 @@
 // Latents come as three kinds of pieces of 64 candidates x 256 dims: "oth", the
 // other CTA's dims of the own candidates (read by QK only), "own", the own dims
 // of the own candidates (QK and PV), and "peer", the own dims of the other
-// CTA's candidates (PV only). A pointer warp resolves the records; eight warps copy the
-// pieces' bytes into staging (cp.async, pieces ahead; a cp.async.bulk a record
-// took 80 cycles each, 2.5 times this kernel's time) and unpack them, exactly (see csa_format_t), to BF16 in the MMA's layout, one
+// CTA's candidates (PV only). A pointer warp resolves the records, two warps copy
+// the pieces' bytes into staging (cp.async; a cp.async.bulk a record took 80
+// cycles each, 2.5 times this kernel's time), eight warps unpack them, exactly (see csa_format_t), to BF16 in the MMA's layout, one
 // 32 KB buffer a kind. Order of a block: oth(i + 1), peer(i), own(i + 1), and
 // QK(i + 1) over oth, PV(i), QK(i + 1) over own: the chain own -> QK -> softmax ->
 // PV -> own of the next block sets the pace, the rest runs beside it.
@@ -48,11 +48,13 @@ namespace {
 constexpr int kChunk = 64;                 // candidates of a block that a CTA owns
 constexpr int kBlock = 2 * kChunk;         // candidates a block
 constexpr int kHalf = 256;                 // output dims per CTA
-constexpr int kConvWarps = 8;              // load + unpack: warps 0..7, four threads a candidate
+constexpr int kConvWarps = 8;              // unpacking: warps 0..7, four threads a candidate
 constexpr int kSoftWarps = 8;              // softmax and epilogue: warps 8..15, two threads a head
 constexpr int kPtrWarp = 16;               // record pointers
 constexpr int kMmaWarp = 17;               // MMA issuer, TMEM owner
-constexpr int kThreads = 32 * 18;
+constexpr int kCopyWarps = 2;              // copies into staging: warps 18, 19
+constexpr int kCopyWarp = 18;
+constexpr int kThreads = 32 * 20;
 constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
@@ -85,7 +87,8 @@ struct AttSmem {
     alignas(16) uint8_t stage[kStageBytes];
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
-    uint64_t x_full[kKinds], x_empty[kKinds], ptr_full[kPtrRing], ptr_empty[kPtrRing];
+    uint64_t stage_full[kKinds], stage_empty[kKinds], x_full[kKinds], x_empty[kKinds];
+    uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint32_t tmem_base;
     int abort_flag;
@@ -235,31 +238,38 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
 // code + 32 i, scale byte at scale + 4 i, to column block i, 16-byte chunks 2 hq
 // and 2 hq + 1. `rope`: the last unit is 16 rope dims, copied as they are.
 __device__ __forceinline__ void unpack_row(const uint8_t *code, const uint8_t *scale, const uint8_t *power,
-                                           const uint8_t *rope, bool valid, uint4 *lo, uint4 *hi) {
+                                           const uint8_t *rope, uint4 *lo, uint4 *hi) {
     constexpr int kStep = kAtom / 16;
-    const float pw = valid ? fp4_power(*power) : 0.f;
-#pragma unroll 1
-    for (int i = 0; i < 4; i += 2) {
-        uint2 c[2];
-        uint32_t sb[2];
+    const float pw = fp4_power(*power);
+    uint2 c[4];
+    uint32_t sb[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            c[e] = *reinterpret_cast<const uint2 *>(code + 32 * (i + e));
-            sb[e] = scale[4 * (i + e)];
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float s = e4m3x2_to_float2((uint16_t)sb[e]).x * pw;
-            uint4 l = unpack8(c[e].x, make_float2(s, s)), h = unpack8(c[e].y, make_float2(s, s));
-            if (e == 1 && i == 2 && rope) {
-                l = *reinterpret_cast<const uint4 *>(rope);
-                h = *reinterpret_cast<const uint4 *>(rope + 16);
-            }
-            if (!valid) l = h = make_uint4(0, 0, 0, 0);  // (whatever the staging held)
-            lo[(i + e) * kStep] = l;
-            hi[(i + e) * kStep] = h;
-        }
+    for (int i = 0; i < 4; ++i) {
+        c[i] = *reinterpret_cast<const uint2 *>(code + 32 * i);
+        sb[i] = scale[4 * i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float s = e4m3x2_to_float2((uint16_t)sb[i]).x * pw;
+        uint4 l = unpack8(c[i].x, make_float2(s, s)), h = unpack8(c[i].y, make_float2(s, s));
+        if (i == 3 && rope) {
+            l = *reinterpret_cast<const uint4 *>(rope);
+            h = *reinterpret_cast<const uint4 *>(rope + 16);
+        }
+        lo[i * kStep] = l;
+        hi[i * kStep] = h;
+    }
+}
+
+// 16-byte copy into shared memory; `bytes` = 0 stores zeros.
+__device__ __forceinline__ void copy16(void *dst, const void *src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(ptx::smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "l"(policy)
+                 : "memory");
+}
+// Arrive (as a counted thread) when this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -274,12 +284,14 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 
     if (threadIdx.x == 0) {
         for (int k = 0; k < kKinds; ++k) {
+            ptx::mbar_init(&s.stage_full[k], 32 * kCopyWarps);
+            ptx::mbar_init(&s.stage_empty[k], kConvWarps);
             ptx::mbar_init(&s.x_full[k], kConvWarps);
             ptx::mbar_init(&s.x_empty[k], 1);
         }
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
-            ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
+            ptx::mbar_init(&s.ptr_empty[i], kCopyWarps + kSoftWarps);
         }
         ptx::mbar_init(&s.s_full, 1);
         ptx::mbar_init(&s.s_free, kSoftWarps);
@@ -315,6 +327,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         const bool now = !poll && try_wait_cluster(bar, parity);
         return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
     };
+    // which half of the dims a kind of piece holds, and where it is staged
+    auto upper_half = [&](int k) { return (k == kOth) != (rank == 1); };
     auto stage_of = [&](int k) {
         const int oth = rank ? kLoStride : kHiStride, own = rank ? kHiStride : kLoStride;
         return s.stage + kChunk * (k == kOth ? 0 : k == kOwn ? oth : oth + own);
@@ -386,60 +400,24 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_arrive(&s.ptr_full[pr]);
         }
     } else if (warp < kConvWarps) {
-        // ------------------------------------------------------------ copy + unpack
-        const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
+        // ------------------------------------------------------------ unpack
         // Pieces in the order oth(0) own(0) | oth(i) peer(i - 1) own(i) | .. | peer(n - 1).
-        // A row's four threads copy its bytes (16-byte pieces hq, hq + 4, ..) and
-        // unpack them; after a piece is unpacked the same kind of the next block
-        // is copied, so two pieces' copies are in flight behind the one waited for.
-        const uint64_t policy = ptx::l2_policy_evict_first();  // a pair reads a record within a block, nobody later
-        uint32_t valid = 0;  // bit k: the staged row of kind k is a record
-        auto upper_half = [&](int k) { return (k == kOth) != (rank == 1); };
-        auto staged = [&](int k) { return stage_of(k) + row * (upper_half(k) ? kHiStride : kLoStride); };
-        auto load = [&](int i, int k) {
-            if (i < u.n_blocks) {
-                const int pr = i % kPtrRing;
-                if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) return false;
-                const uint8_t *rec = s.rec[pr][k == kPeer ? kChunk + row : row];
-                if (k == kPeer) {  // the block's last look at its pointers
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
-                }
-                valid = rec ? valid | 1u << k : valid & ~(1u << k);
-                if (rec) {
-                    uint8_t *dst = staged(k) + 16 * hq;
-                    const bool upper = upper_half(k);
-                    const uint8_t *src = rec + (upper ? kLoCodes : 0) + 16 * hq;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        if (!upper && c == 2) src += kFp4ScaleOffset - kLoCodes;
-                        if (upper || c < 2 || (c == 2 && hq < 2)) ptx::cp_async_16_hint(dst + 64 * c, src + 64 * c, policy);
-                    }
-                }
-            }
-            ptx::cp_async_commit();
-            return true;
-        };
-        bool ok = true;
+        const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
 #pragma unroll 1
-        for (int k = 0; k < kKinds && ok; ++k) ok = load(0, k);
-#pragma unroll 1
-        for (int step = 0, i = 0, k = kOth; step < 3 * u.n_blocks && ok; ++step) {
-            // groups issued after this piece's: two, but one at step 2 (oth(1))
-            if (step == 2) ptx::cp_async_wait<1>();
-            else ptx::cp_async_wait<2>();
-            __syncwarp();
-            if (!wait(&s.x_empty[k], (i & 1) ^ 1)) { ok = false; break; }
+        for (int left = 3 * u.n_blocks, i = 0, k = kOth; left > 0; --left) {
+            if (!wait(&s.stage_full[k], i & 1) || !wait(&s.x_empty[k], (i & 1) ^ 1)) { fail(); break; }
             const bool upper = upper_half(k);
-            const uint8_t *base = staged(k);
+            const uint8_t *base = stage_of(k) + row * (upper ? kHiStride : kLoStride);
             unpack_row(base + 8 * hq, base + (upper ? kFp4ScaleOffset + 16 - kLoCodes : kLoCodes) + hq,
                        base + (upper ? kFp4PowerOffset - kLoCodes : kLoCodes + kFp4PowerOffset - kFp4ScaleOffset),
-                       upper ? base + kFp4RopeOffset - kLoCodes + 32 * hq : nullptr, (valid >> k) & 1u,
-                       sw128(s.x[k], row, 2 * hq), sw128(s.x[k], row, 2 * hq + 1));
+                       upper ? base + kFp4RopeOffset - kLoCodes + 32 * hq : nullptr, sw128(s.x[k], row, 2 * hq),
+                       sw128(s.x[k], row, 2 * hq + 1));
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
-            __syncwarp();                   // (and the row's threads are done with the staging)
-            if (lane == 0) ptx::mbar_arrive(&s.x_full[k]);
-            if (!load(i + 1, k)) { ok = false; break; }
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(&s.stage_empty[k]);
+                ptx::mbar_arrive(&s.x_full[k]);
+            }
             if (k == kOth) {
                 if (i == 0) k = kOwn;
                 else k = kPeer, --i;
@@ -450,7 +428,42 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 else k = kPeer;
             }
         }
+    } else if (warp >= kCopyWarp) {
+        // ------------------------------------------------------------ copies into staging
+        // Each of the two warps copies 32 rows of every piece, 16 bytes a lane; a row
+        // without a record is filled with zeros (codes, scales and power: zero latents).
+        const uint64_t policy = ptx::l2_policy_evict_first();  // a pair reads a record within a block, nobody later
+        bool ok = true;
+#pragma unroll 1
+        for (int i = 0; i < u.n_blocks && ok; ++i) {
+            const int pr = i % kPtrRing;
+            ok = wait(&s.ptr_full[pr], (i / kPtrRing) & 1);
+#pragma unroll 1
+            for (int k = 0; k < kKinds && ok; ++k) {
+                if (!wait(&s.stage_empty[k], (i & 1) ^ 1)) { ok = false; break; }
+                const bool upper = upper_half(k);
+                const int row0 = (warp - kCopyWarp) * 32, stride = upper ? kHiStride : kLoStride;
+                const uint8_t *const *recs = s.rec[pr] + (k == kPeer ? kChunk : 0) + row0;
+                uint8_t *dst = stage_of(k) + row0 * stride;
+                // `per` lanes a row: 256 bytes from byte 128 (upper), or the 128 of
+                // the codes and then 32 from byte 352 (lower)
+                auto rows = [&](int per, int from, int to) {
+                    const int c = 16 * (lane & (per - 1));
+#pragma unroll 4
+                    for (int r = lane / per; r < 32; r += 32 / per) {
+                        const uint8_t *rec = recs[r];
+                        copy16(dst + r * stride + to + c, (rec ? rec : P.ring) + from + c, rec ? 16u : 0u, policy);
+                    }
+                };
+                rows(upper ? 16 : 8, upper ? kLoCodes : 0, 0);
+                if (!upper) rows(2, kFp4ScaleOffset, kLoCodes);
+                arrive_after_copies(&s.stage_full[k]);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
+        }
         if (!ok) fail();
+        ptx::cp_async_commit();
         ptx::cp_async_wait<0>();  // no copy lands after this warp has moved on
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
