@@ -187,11 +187,12 @@ __device__ __forceinline__ void commit_both(uint64_t *bar) {
         : "memory");
 }
 
-__device__ __forceinline__ void remote_store(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void remote_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Store into the other CTA, counted (4 bytes) on a barrier there. (A store and a
+// releasing arrive would make the warp wait for the store's way there.)
+__device__ __forceinline__ void store_to_peer(uint32_t addr, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
 // Copy into the other CTA, counted on a barrier there.
 __device__ __forceinline__ void copy_to_peer(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -297,7 +298,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         ptx::mbar_init(&s.s_free, kSoftWarps);
         ptx::mbar_init(&s.p_full, kSoftWarps);
         ptx::mbar_init(&s.pp_full, 1);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], 2 * kSoftWarps);  // both CTAs' softmax warps
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], kSoftWarps);  // (and the other CTA's bytes)
         ptx::mbar_init(&s.o_done, 2);  // both CTAs' PV of a block
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&s.pair[i], 2);
         ptx::mbar_init(&s.q_ready, kSoftWarps);
@@ -557,13 +558,11 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         // this thread's maximum of block i (or, at the end, its sum) to the other
         // three threads of the head
         auto send = [&](int i, float v) {
-            remote_store(peer_max + (i & 1) * (4 * kHeads * 4), v);
+            store_to_peer(peer_max + (i & 1) * (4 * kHeads * 4), v, peer_max_full + (i & 1) * 8);
             s.pmax[i & 1][half][h] = v;
             __syncwarp();
-            if (lane == 0) {
-                remote_arrive(peer_max_full + (i & 1) * 8);
-                ptx::mbar_arrive(&s.max_full[i & 1]);
-            }
+            // (each warp expects the bytes of the other CTA's warp like it)
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.max_full[i & 1], 32 * 4);
         };
         auto received = [&](int i, int from) { return *reinterpret_cast<volatile float *>(&s.pmax[i & 1][from][h]); };
         bool ok = true;
