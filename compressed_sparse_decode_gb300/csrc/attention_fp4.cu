@@ -28,7 +28,7 @@
 // Latents come as three kinds of pieces of 64 candidates x 256 dims: "oth", the
 // other CTA's dims of the own candidates (read by QK only), "own", the own dims
 // of the own candidates (QK and PV), and "peer", the own dims of the other
-// CTA's candidates (PV only). A pointer warp resolves the records, two warps copy
+// CTA's candidates (PV only). A pointer warp resolves the records, four warps copy
 // the pieces' bytes into staging (cp.async; a cp.async.bulk a record took 80
 // cycles each, 2.5 times this kernel's time), eight warps unpack them, exactly (see csa_format_t), to BF16 in the MMA's layout, one
 // 32 KB buffer a kind. Order of a block: oth(i + 1), peer(i), own(i + 1), and
@@ -52,9 +52,9 @@ constexpr int kConvWarps = 8;              // unpacking: warps 0..7, four thread
 constexpr int kSoftWarps = 8;              // softmax and epilogue: warps 8..15, two threads a head
 constexpr int kPtrWarp = 16;               // record pointers
 constexpr int kMmaWarp = 17;               // MMA issuer, TMEM owner
-constexpr int kCopyWarps = 2;              // copies into staging: warps 18, 19
-constexpr int kCopyWarp = 18;
-constexpr int kThreads = 32 * 20;
+constexpr int kCopyWarp = 18, kCopyWarps = 4;  // copies into staging
+constexpr int kCopyRows = kChunk / kCopyWarps;
+constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
 constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
@@ -330,6 +330,18 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     };
     // which half of the dims a kind of piece holds, and where it is staged
     auto upper_half = [&](int k) { return (k == kOth) != (rank == 1); };
+    // the order of use: oth(0) own(0) | oth(i) peer(i - 1) own(i) | .. | peer(n - 1)
+    auto next_piece = [&](int &i, int &k) {
+        if (k == kOth) {
+            if (i == 0) k = kOwn;
+            else k = kPeer, --i;
+        } else if (k == kPeer) {
+            k = kOwn, ++i;
+        } else {
+            if (i + 1 < u.n_blocks) k = kOth, ++i;
+            else k = kPeer;
+        }
+    };
     auto stage_of = [&](int k) {
         const int oth = rank ? kLoStride : kHiStride, own = rank ? kHiStride : kLoStride;
         return s.stage + kChunk * (k == kOth ? 0 : k == kOwn ? oth : oth + own);
@@ -387,8 +399,12 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 const uint8_t *rec = record(i, e, entry[e], page[e]);
                 s.rec[pr][e * 32 + lane] = rec;
                 // into L2 while the block is up to kPtrRing blocks away (each CTA
-                // its own candidates: the pair reads both)
-                if (e < 2 && rec) ptx::prefetch_l2_bulk(rec, kFp4Bytes);
+                // its own candidates: the pair reads both; one line a prefetch,
+                // since a bulk prefetch takes as long as a bulk copy)
+                if (e < 2 && rec) {
+#pragma unroll
+                    for (int b = 0; b < kFp4Bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + b));
+                }
                 if (e < 2) have[e] = __ballot_sync(0xffffffffu, rec != nullptr);
                 entry[e] = next_entry[e];
                 if (i + 1 < u.n_blocks) page[e] = load_page(i + 1, e, entry[e]);
@@ -402,7 +418,6 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         }
     } else if (warp < kConvWarps) {
         // ------------------------------------------------------------ unpack
-        // Pieces in the order oth(0) own(0) | oth(i) peer(i - 1) own(i) | .. | peer(n - 1).
         const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
 #pragma unroll 1
         for (int left = 3 * u.n_blocks, i = 0, k = kOth; left > 0; --left) {
@@ -419,49 +434,51 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 ptx::mbar_arrive(&s.stage_empty[k]);
                 ptx::mbar_arrive(&s.x_full[k]);
             }
-            if (k == kOth) {
-                if (i == 0) k = kOwn;
-                else k = kPeer, --i;
-            } else if (k == kPeer) {
-                k = kOwn, ++i;
-            } else {
-                if (i + 1 < u.n_blocks) k = kOth, ++i;
-                else k = kPeer;
-            }
+            next_piece(i, k);
         }
     } else if (warp >= kCopyWarp) {
         // ------------------------------------------------------------ copies into staging
-        // Each of the two warps copies 32 rows of every piece, 16 bytes a lane; a row
+        // Each warp copies kCopyRows rows of every piece, 16 bytes a lane; a row
         // without a record is filled with zeros (codes, scales and power: zero latents).
         const uint64_t policy = ptx::l2_policy_evict_first();  // a pair reads a record within a block, nobody later
+        // The first block's pieces, then in the order of their use the same kind of
+        // the next block: each staging buffer is filled again as soon as it is free.
         bool ok = true;
+        int first = 0;
 #pragma unroll 1
-        for (int i = 0; i < u.n_blocks && ok; ++i) {
-            const int pr = i % kPtrRing;
-            ok = wait(&s.ptr_full[pr], (i / kPtrRing) & 1);
-#pragma unroll 1
-            for (int k = 0; k < kKinds && ok; ++k) {
-                if (!wait(&s.stage_empty[k], (i & 1) ^ 1)) { ok = false; break; }
-                const bool upper = upper_half(k);
-                const int row0 = (warp - kCopyWarp) * 32, stride = upper ? kHiStride : kLoStride;
-                const uint8_t *const *recs = s.rec[pr] + (k == kPeer ? kChunk : 0) + row0;
-                uint8_t *dst = stage_of(k) + row0 * stride;
+        for (int left = 3 * u.n_blocks, i = 0, k = kOth; left > 0; --left) {
+            const int b = first < kKinds ? 0 : i + 1, kind = first < kKinds ? first : k;
+            if (b < u.n_blocks) {
+                const int pr = b % kPtrRing;
+                if (!wait(&s.ptr_full[pr], (b / kPtrRing) & 1) || !wait(&s.stage_empty[kind], (b & 1) ^ 1)) { ok = false; break; }
+                const bool upper = upper_half(kind);
+                const int row0 = (warp - kCopyWarp) * kCopyRows, stride = upper ? kHiStride : kLoStride;
+                const uint8_t *const *recs = s.rec[pr] + (kind == kPeer ? kChunk : 0) + row0;
+                uint8_t *dst = stage_of(kind) + row0 * stride;
                 // `per` lanes a row: 256 bytes from byte 128 (upper), or the 128 of
                 // the codes and then 32 from byte 352 (lower)
                 auto rows = [&](int per, int from, int to) {
                     const int c = 16 * (lane & (per - 1));
 #pragma unroll 4
-                    for (int r = lane / per; r < 32; r += 32 / per) {
+                    for (int r = lane / per; r < kCopyRows; r += 32 / per) {
                         const uint8_t *rec = recs[r];
                         copy16(dst + r * stride + to + c, (rec ? rec : P.ring) + from + c, rec ? 16u : 0u, policy);
                     }
                 };
                 rows(upper ? 16 : 8, upper ? kLoCodes : 0, 0);
                 if (!upper) rows(2, kFp4ScaleOffset, kLoCodes);
-                arrive_after_copies(&s.stage_full[k]);
+                arrive_after_copies(&s.stage_full[kind]);
+                if (kind == kPeer) {  // the block's last look at its pointers
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
+                }
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
+            if (first < kKinds) {
+                ++first;
+                ++left;
+                continue;
+            }
+            next_piece(i, k);
         }
         if (!ok) fail();
         ptx::cp_async_commit();
