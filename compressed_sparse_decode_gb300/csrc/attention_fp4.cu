@@ -585,27 +585,38 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         bool ok = true;
         if (u.n_blocks > 0) {
             // Q: dims from kQTmemDims up -> shared memory, the dims below -> TMEM
-            // (BF16 pairs, lane = head), 64 dims a piece; half the pieces a thread
-            const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + ((size_t)u.r * kHeads + h) * kDim);
+            // (BF16 pairs, lane = head), 64 dims a piece, half the pieces a thread. A
+            // load takes four heads' 128 bytes (a head a lane would touch 32 lines);
+            // the warp's 4 KB of the weights' buffers, not used yet, turn them into a
+            // head a lane.
+            const int r4 = lane >> 3, c = lane & 7;
+            const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + ((size_t)u.r * kHeads + quarter * 32 + r4) * kDim) + c;
+            uint8_t *turn = half ? s.pp + quarter * 4096 : s.p + quarter * 4096;
             const uint64_t policy = ptx::l2_policy_evict_first();
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                ptx::cp_async_16_hint(sw128(s.qs + half * kQAtom, h, c), qg + kQTmemDims / 8 + 8 * half + c, policy);
+            for (int g = 0; g < 8; ++g)
+                ptx::cp_async_16_hint(sw128(s.qs + half * kQAtom, quarter * 32 + 4 * g + r4, c),
+                                      qg + (size_t)4 * g * (kDim / 8) + kQTmemDims / 8 + 8 * half, policy);
             ptx::cp_async_commit();
 #pragma unroll 1
             for (int pc = 3 * half; pc < 3 * half + 3; ++pc) {
                 uint4 w[8];
 #pragma unroll
-                for (int v = 0; v < 8; ++v) w[v] = ptx::ldg_v4_policy(qg + pc * 8 + v, policy);
+                for (int g = 0; g < 8; ++g) w[g] = ptx::ldg_v4_policy(qg + (size_t)4 * g * (kDim / 8) + 8 * pc, policy);
+#pragma unroll
+                for (int g = 0; g < 8; ++g) *sw128(turn, 4 * g + r4, c) = w[g];
+                __syncwarp();
                 uint32_t regs[32];
 #pragma unroll
                 for (int v = 0; v < 8; ++v) {
-                    regs[4 * v] = w[v].x;
-                    regs[4 * v + 1] = w[v].y;
-                    regs[4 * v + 2] = w[v].z;
-                    regs[4 * v + 3] = w[v].w;
+                    const uint4 x = *sw128(turn, lane, v);
+                    regs[4 * v] = x.x;
+                    regs[4 * v + 1] = x.y;
+                    regs[4 * v + 2] = x.z;
+                    regs[4 * v + 3] = x.w;
                 }
                 ptx::tmem_st32(lane_base + kColQ + pc * 32, regs);
+                __syncwarp();
             }
             ptx::cp_async_wait<0>();
             ptx::tmem_st_wait();
