@@ -88,6 +88,7 @@ struct AttSmem {
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
     uint64_t stage_full[kKinds], stage_empty[kKinds], x_full[kKinds], x_empty[kKinds];
+    uint64_t own_first;                        // the first two column blocks of an own piece
     uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint32_t tmem_base;
@@ -158,25 +159,6 @@ __device__ __forceinline__ uint32_t elect_one() {
     return e;
 }
 
-// tcgen05.mma kind::f16 with the issuing lane chosen by a predicate instead of
-// a branch, so that the descriptors stay warp-uniform values.
-__device__ __forceinline__ void mma_ss(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(issue), "r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(acc)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 e, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(issue), "r"(d), "r"(a), "l"(b),
-        "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 // Arrive on the barrier at this offset in both CTAs of the pair when the MMAs
 // issued so far by this thread are done.
 __device__ __forceinline__ void commit_both(uint64_t *bar) {
@@ -238,8 +220,9 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
 // Unpacks a thread's quarter of a staged row: units i < 4 of 16 dims, codes at
 // code + 32 i, scale byte at scale + 4 i, to column block i, 16-byte chunks 2 hq
 // and 2 hq + 1. `rope`: the last unit is 16 rope dims, copied as they are.
+// `half_done`: arrived on by the warp after the first two.
 __device__ __forceinline__ void unpack_row(const uint8_t *code, const uint8_t *scale, const uint8_t *power,
-                                           const uint8_t *rope, uint4 *lo, uint4 *hi) {
+                                           const uint8_t *rope, uint4 *lo, uint4 *hi, uint64_t *half_done) {
     constexpr int kStep = kAtom / 16;
     const float pw = fp4_power(*power);
     uint2 c[4];
@@ -259,6 +242,11 @@ __device__ __forceinline__ void unpack_row(const uint8_t *code, const uint8_t *s
         }
         lo[i * kStep] = l;
         hi[i * kStep] = h;
+        if (i == 1 && half_done) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(half_done);
+        }
     }
 }
 
@@ -279,6 +267,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
     extern __shared__ uint8_t smem_raw[];
     AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // (shuffled, so that the compiler knows the warp's number, and with it the
+    // roles' branches and the MMA's operands, to be the same for all lanes)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x & 1;  // = the CTA's rank in its cluster
     volatile int *abort = &s.abort_flag;
@@ -290,6 +280,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_init(&s.x_full[k], kConvWarps);
             ptx::mbar_init(&s.x_empty[k], 1);
         }
+        ptx::mbar_init(&s.own_first, kConvWarps);
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
             ptx::mbar_init(&s.ptr_empty[i], kCopyWarps + kSoftWarps);
@@ -427,7 +418,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             unpack_row(base + 8 * hq, base + (upper ? kFp4ScaleOffset + 16 - kLoCodes : kLoCodes) + hq,
                        base + (upper ? kFp4PowerOffset - kLoCodes : kLoCodes + kFp4PowerOffset - kFp4ScaleOffset),
                        upper ? base + kFp4RopeOffset - kLoCodes + 32 * hq : nullptr, sw128(s.x[k], row, 2 * hq),
-                       sw128(s.x[k], row, 2 * hq + 1));
+                       sw128(s.x[k], row, 2 * hq + 1), k == kOwn ? &s.own_first : nullptr);
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
             __syncwarp();
             if (lane == 0) {
@@ -490,33 +481,32 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         const uint32_t leader = elect_one();
         bool ok = u.n_blocks == 0 || wait(&s.q_ready, 0);
         const uint64_t qd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.qs));
-        // the 16 K-steps of dims 256 hf ..: Q from TMEM below kQTmemDims, from
-        // shared memory above
-        auto qk_half = [&](int hf, const uint8_t *x, bool first) {
-            const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(x));
-            if (hf == 0) {
+        // eight K-steps, dims 128 q ..: Q from TMEM below kQTmemDims, from shared
+        // memory above
+        static_assert(kQTmemDims == 384, "the last quarter of Q is in shared memory");
+        auto qk_quarter = [&](int q, const uint8_t *x, bool first) {
+            const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(x + (q & 1) * 2 * kAtom));
+            if (!leader) return;
+            if (q < 3) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    mma_ts(leader, tmem + kColS, tmem + kColQ + k * 8,
-                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
+                for (int k = 0; k < 8; ++k)
+                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + q * 64 + k * 8,
+                                    xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_ts(leader, tmem + kColS, tmem + kColQ + (16 + k) * 8,
-                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
-#pragma unroll
-                for (int k = 8; k < 16; ++k)
-                    mma_ss(leader, tmem + kColS, qd + (uint64_t)((((k - 8) >> 2) * kQAtom + (k & 3) * 32) >> 4),
-                           xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, 1u);
+                    ptx::mma_f16(tmem + kColS, qd + (uint64_t)(((k >> 2) * kQAtom + (k & 3) * 32) >> 4),
+                                 xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, 1u);
             }
         };
         auto pv = [&](const uint8_t *w, const uint8_t *x, bool first) {
             const uint64_t ad = ptx::desc_kmajor_sw128(ptx::smem_u32(w));
             const uint64_t bd = ptx::desc_mnmajor_sw128(ptx::smem_u32(x), kAtom, 1024);
+            if (!leader) return;
 #pragma unroll
             for (int k = 0; k < kChunk / 16; ++k)
-                mma_ss(leader, tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
-                       !(first && k == 0));
+                ptx::mma_f16(tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
+                             !(first && k == 0));
         };
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
@@ -530,11 +520,20 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (part == 0) ok = wait(&s.x_full[k], ph) && (i == 0 || wait(&s.s_free, before));
                 else if (part == 1) ok = wait(&s.p_full, before);
                 else if (part == 2) ok = wait(&s.x_full[k], before) && wait_peer(&s.pp_full, before);
-                else ok = wait(&s.x_full[k], ph);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (qk) {
-                    qk_half(part == 0 ? rank ^ 1 : rank, s.x[k], part == 0);
+                    const int hf = part == 0 ? rank ^ 1 : rank;
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        if (part == 3) {  // each half of the piece as soon as it is there
+                            ok = wait(e ? &s.x_full[k] : &s.own_first, ph);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                        }
+                        qk_quarter(2 * hf + e, s.x[k], part == 0 && e == 0);
+                    }
+                    if (!ok) break;
                     if (leader) ptx::mma_commit(part == 0 ? &s.x_empty[k] : &s.s_full);
                 } else {
                     pv(part == 1 ? s.p : s.pp, s.x[k], i == 1 && part == 1);
