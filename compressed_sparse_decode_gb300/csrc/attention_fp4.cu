@@ -258,7 +258,10 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, uint32_t byte
 }
 // Arrive (as a counted thread) when this thread's copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(ptx::smem_u32(bar)) : "memory");
+    // The address goes through a shuffle so that it stays a per-lane value: builds
+    // in which the compiler knew it to be uniform ended in an illegal instruction.
+    const uint32_t a = __shfl_sync(0xffffffffu, ptx::smem_u32(bar), threadIdx.x & 31);
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(a) : "memory");
 }
 
 // ---------------------------------------------------------------- the kernel

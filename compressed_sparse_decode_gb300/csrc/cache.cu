@@ -2,7 +2,7 @@
 // (csa_cache_append, csa_cache_read): FP8 and 4-bit records, contiguous, paged
 // or ring.
 //
-// One warp a token; lane l holds dims [16 l, 16 l + 16): lanes 0..27 the nope
+// One warp a token (several, one after the other, in large calls); lane l holds dims [16 l, 16 l + 16): lanes 0..27 the nope
 // dims (one 4-bit scale block each, eight lanes an FP8 block), lanes 28..31
 // the rope dims. So the 4-bit block maximum needs no shuffle, and a record is
 // written with one vector store a lane.
@@ -28,21 +28,17 @@ struct Span {
 };
 
 struct Slot {
-    bool kept;        // the token counts and its entry is inside the cache
-    int64_t entry;    // first + t
-    int64_t record;
+    int64_t entry;   // first + t
+    int64_t record;  // -1: the token does not count, or its entry is outside the cache
 };
 
-// Warp-uniform. Reports what lies outside the cache.
-__device__ __forceinline__ Slot find_slot(const Span &s, int b, int t, int *err, bool reporter) {
-    Slot o;
-    o.kept = false;
-    o.entry = 0;
-    o.record = 0;
+// Slot of token t of sequence b. Reports what lies outside the cache.
+__device__ __forceinline__ Slot find_slot(const Span &s, int b, int t, int *err) {
+    Slot o = {0, -1};
     int n = s.count ? __ldg(s.count + b) : s.T;
     const int first = __ldg(s.first + b);
     if (n < 0 || n > s.T) {
-        if (reporter && t == 0) report_error(err, CSA_ERR_BAD_INDEX);
+        if (t == 0) report_error(err, CSA_ERR_BAD_INDEX);
         n = n < 0 ? 0 : s.T;
     }
     if (t >= n) return o;
@@ -52,14 +48,28 @@ __device__ __forceinline__ Slot find_slot(const Span &s, int b, int t, int *err,
         if (t < n - s.cache.seq_capacity) return o;  // overwritten by a later token of this call
         if (first >= 0) slot = o.entry % s.cache.seq_capacity;
     }
-    const int64_t rec = first >= 0 && slot < s.cache.seq_capacity ? record_index(s.cache, b, (int)slot) : -1;
-    if (rec < 0) {
-        if (reporter) report_error(err, CSA_ERR_BAD_INDEX);
-        return o;
-    }
-    o.kept = true;
-    o.record = rec;
+    if (first >= 0 && slot < s.cache.seq_capacity) o.record = record_index(s.cache, b, (int)slot);
+    if (o.record < 0) report_error(err, CSA_ERR_BAD_INDEX);
     return o;
+}
+
+// A warp's tokens [t0, t0 + n): lane j looks token t0 + j up, all at once.
+__device__ __forceinline__ Slot find_slots(const Span &s, int t0, int n, int lane, int *err) {
+    const int token = t0 + lane;
+    Slot o = {0, -1};
+    if (lane < n && token < s.B * s.T) o = find_slot(s, token / s.T, token % s.T, err);
+    return o;
+}
+__device__ __forceinline__ Slot slot_of(const Slot &mine, int j) {
+    return {__shfl_sync(kAll, mine.entry, j), __shfl_sync(kAll, mine.record, j)};
+}
+
+// Tokens a warp: as many as leave every SM four blocks, up to 8. (They share the
+// look-up, the norm's weights and the rotation's table, and the next one's loads
+// run under the current one: 49k tokens into FP8 with keys took 50 us with one.)
+int tokens_per_warp(int tokens) {
+    const int n = tokens / (cached_sm_count() * 4 * kWarps);
+    return n < 1 ? 1 : n > 8 ? 8 : n;
 }
 
 struct AppendParams {
@@ -74,18 +84,23 @@ struct AppendParams {
     uint8_t *k_idx;
     float *k_idx_scale;
     int idx_cap;
+    int per_warp;
     int *err;
 };
 
-// 16 values of a nope lane as E2M1 codes of unit s = sb * 2^E.
+// 16 values of a nope lane as E2M1 codes of unit s = sb * 2^E (4 significant
+// bits). A quotient of a 16-bit input is a halfway point of the codes or 2^-12 of
+// it away, so rounding it to fp32 decides nothing; other values need the sticky
+// bit. (Tiny units: all times 2^64, so that the remainders stay normal numbers.)
+template <bool kSticky>
 __device__ __forceinline__ uint2 fp4_codes(const float (&f)[2][8], float s) {
     uint32_t w[2];
-    const float inv = 1.f / s;
+    const float inv = __frcp_rn(s);
 #pragma unroll
     for (int o = 0; o < 2; ++o) {
         float q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = sticky_quotient(f[o][e], s, inv);
+        for (int e = 0; e < 8; ++e) q[e] = kSticky ? sticky_quotient(f[o][e], s, inv) : quotient(f[o][e], s, inv);
         w[o] = e2m1x4(q[0], q[1], q[2], q[3]) | (e2m1x4(q[4], q[5], q[6], q[7]) << 16);
     }
     return make_uint2(w[0], w[1]);
@@ -104,125 +119,144 @@ __global__ void __launch_bounds__(kThreads)
 append_kernel(const __grid_constant__ AppendParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (token >= P.span.B * P.span.T) return;
-    const int b = token / P.span.T, t = token - b * P.span.T;
-    const Slot slot = find_slot(P.span, b, t, P.err, lane == 0);
-    if (!slot.kept) return;
-    const int64_t p = slot.entry * P.pos_stride;
-
-    Octet<DT> in[2], kin;
-    const int64_t at = b * P.seq_stride + t * P.token_stride + 16 * lane;
-    in[0].load(P.x, at);
-    in[1].load(P.x, at + 8);
+    const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * P.per_warp;
+    if (t0 >= P.span.B * P.span.T) return;
+    const Slot mine = find_slots(P.span, t0, P.per_warp, lane, P.err);
     const bool key_lane = KEYS && lane < kIdxDim / 8;  // 16 lanes hold the key's octets
-    if (key_lane) kin.load(P.key, b * P.key_seq_stride + t * P.key_token_stride + 8 * lane);
     const bool turn = P.ops.rope_dim > 0;
-    float2 own = make_float2(1.f, 0.f);  // lane i: pair i
-    if (turn) own = turn_cos_sin(p, P.ops.turn[lane]);
+    const uint64_t pair_turn = turn ? P.ops.turn[lane] : 0;
+    float w[2][8];  // the norm's weights of this lane's dims
+    load_weights(w[0], P.ops.norm ? P.ops.weight : nullptr, 16 * lane);
+    load_weights(w[1], P.ops.norm ? P.ops.weight : nullptr, 16 * lane + 8);
+    struct {
+        Octet<DT> x[2], key;
+    } now, next;
+    auto fetch = [&](int j, auto &o) {
+        const Slot s = slot_of(mine, j);
+        if (s.record < 0) return;
+        const int b = (t0 + j) / P.span.T, t = t0 + j - b * P.span.T;
+        const int64_t at = b * P.seq_stride + t * P.token_stride + 16 * lane;
+        o.x[0].load(P.x, at);
+        o.x[1].load(P.x, at + 8);
+        if (key_lane) o.key.load(P.key, b * P.key_seq_stride + t * P.key_token_stride + 8 * lane);
+    };
+    fetch(0, next);
+#pragma unroll 1
+    for (int j = 0; j < P.per_warp; ++j) {
+        now = next;
+        if (j + 1 < P.per_warp) fetch(j + 1, next);
+        const Slot slot = slot_of(mine, j);
+        if (slot.record < 0) continue;
+        const int b = (t0 + j) / P.span.T;
+        const int64_t p = slot.entry * P.pos_stride;
+        float2 own = make_float2(1.f, 0.f);  // lane i: pair i
+        if (turn) own = turn_cos_sin(p, pair_turn);
 
-    float f[2][8];
-    in[0].floats(f[0]);
-    in[1].floats(f[1]);
-    if (P.ops.norm) {
-        float sum = 0.f;
+        float f[2][8];
+        now.x[0].floats(f[0]);
+        now.x[1].floats(f[1]);
+        if (P.ops.norm) {
+            float2 two = make_float2(0.f, 0.f);
+            square_octet(f[0], two);
+            square_octet(f[1], two);
+            float sum = two.x + two.y;
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(f[o][e], f[o][e], sum);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        const float inv_rms = rsqrtf(sum / kDim + P.ops.eps);
-        scale_octet(f[0], inv_rms, P.ops.weight, 16 * lane);
-        scale_octet(f[1], inv_rms, P.ops.weight, 16 * lane + 8);
-    }
-    const bool rope_lane = lane >= kNopeLanes;
-    if (turn) {
-#pragma unroll
-        for (int o = 0; o < 2; ++o) {
-            float2 cs[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int pair = ((lane - kNopeLanes) & 3) * 8 + 4 * o + e;
-                cs[e].x = __shfl_sync(kAll, own.x, pair);
-                cs[e].y = __shfl_sync(kAll, own.y, pair);
-            }
-            if (rope_lane) turn_octet(f[o], cs);
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+            const float inv_rms = rsqrtf(sum * (1.f / kDim) + P.ops.eps);
+            scale_octet(f[0], inv_rms, w[0]);
+            scale_octet(f[1], inv_rms, w[1]);
         }
-    }
-    const uint32_t amax = rope_lane ? 0u : amax_bits(f[1], amax_bits(f[0]));
-    uint8_t *rec = P.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
-    if (FMT == CSA_FORMAT_FP4) {
-        const uint32_t top = __reduce_max_sync(kAll, amax);
-        const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
-        const int E = bad ? 128 : fp4_exponent(top);
-        if (rope_lane) {
-            uint4 *dst = reinterpret_cast<uint4 *>(rec + kFp4RopeOffset + 32 * (lane - kNopeLanes));
-            dst[0] = pack_bf16_octet(f[0]);
-            dst[1] = pack_bf16_octet(f[1]);
-            if (lane == kNopeLanes)
-                *reinterpret_cast<uint32_t *>(rec + kFp4PowerOffset) = (uint32_t)(E + 127);
-        } else {
-            // block scale: e4m3(amax / 6 * 2^-E), its halfway cases decided exactly
-            const float ratio = sticky_quotient(__uint_as_float(amax), 6.f, 1.f / 6.f) *
-                                __uint_as_float((uint32_t)(127 - E) << 23);
-            const uint32_t sb = bad ? 0u : e4m3x4(ratio, 0.f, 0.f, 0.f) & 0xFFu;
-            uint2 codes = make_uint2(0u, 0u);
-            if (sb) {
-                const float unit = e4m3x2_to_float2((uint16_t)sb).x * __uint_as_float((uint32_t)(E + 127) << 23);
-                codes = fp4_codes(f, unit);
-            }
-            *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
-            rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
-        }
-    } else {
-        uint32_t top = amax;  // over the eight lanes of a 128-dim block (rope lanes hold 0)
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
-        if (rope_lane) {
-            uint4 *dst = reinterpret_cast<uint4 *>(rec + kRopeOffset + 32 * (lane - kNopeLanes));
-            dst[0] = pack_bf16_octet(f[0]);
-            dst[1] = pack_bf16_octet(f[1]);
-        } else {
-            const float s = e4m3_scale(top), inv = 1.f / s;
-            float q[2][8];
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q[o][e] = sticky_quotient(f[o][e], s, inv);
-            *reinterpret_cast<uint4 *>(rec + 16 * lane) =
-                make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
-                           e4m3x4(q[1][0], q[1][1], q[1][2], q[1][3]), e4m3x4(q[1][4], q[1][5], q[1][6], q[1][7]));
-            if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + kScaleOffset + 4 * (lane >> 3)) = s;
-        }
-    }
-    if (KEYS) {
-        float g[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 0.f;
-        if (key_lane) kin.floats(g);
+        const bool rope_lane = lane >= kNopeLanes;
         if (turn) {
-            // octets 8..15 are the key's rope dims: pairs 4 (lane - 8) ..
-            float2 cs[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int pair = ((lane - 8) & 7) * 4 + e;
-                cs[e].x = __shfl_sync(kAll, own.x, pair);
-                cs[e].y = __shfl_sync(kAll, own.y, pair);
+            for (int o = 0; o < 2; ++o) {
+                float2 cs[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int pair = ((lane - kNopeLanes) & 3) * 8 + 4 * o + e;
+                    cs[e].x = __shfl_sync(kAll, own.x, pair);
+                    cs[e].y = __shfl_sync(kAll, own.y, pair);
+                }
+                if (rope_lane) turn_octet(f[o], cs);
             }
-            if (key_lane && lane >= 8) turn_octet(g, cs);
         }
-        const uint32_t top = __reduce_max_sync(kAll, amax_bits(g));
-        if (slot.entry >= P.idx_cap) {
-            if (lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
-        } else if (key_lane) {
-            const float s = e4m3_scale(top), inv = 1.f / s;
-            const int64_t row = (int64_t)b * P.idx_cap + slot.entry;
+        const uint32_t amax = rope_lane ? 0u : amax_bits(amax_octet(f[1], amax_octet(f[0])));
+        uint8_t *rec = P.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+        if (FMT == CSA_FORMAT_FP4) {
+            const uint32_t top = __reduce_max_sync(kAll, amax);
+            const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
+            const int E = bad ? 128 : fp4_exponent(top);
+            if (rope_lane) {
+                uint4 *dst = reinterpret_cast<uint4 *>(rec + kFp4RopeOffset + 32 * (lane - kNopeLanes));
+                dst[0] = pack_bf16_octet(f[0]);
+                dst[1] = pack_bf16_octet(f[1]);
+                if (lane == kNopeLanes)
+                    *reinterpret_cast<uint32_t *>(rec + kFp4PowerOffset) = (uint32_t)(E + 127);
+            } else {
+                // block scale: e4m3(amax / 6 * 2^-E), its halfway cases decided exactly
+                const float ratio = sticky_quotient(__uint_as_float(amax), 6.f, 1.f / 6.f) *
+                                    __uint_as_float((uint32_t)(127 - E) << 23);
+                const uint32_t sb = bad ? 0u : e4m3x4(ratio, 0.f, 0.f, 0.f) & 0xFFu;
+                uint2 codes = make_uint2(0u, 0u);
+                if (sb) {
+                    float unit = e4m3x2_to_float2((uint16_t)sb).x * __uint_as_float((uint32_t)(E + 127) << 23);
+                    if (E < -60) {
+                        constexpr float kUp = 18446744073709551616.f;
+                        unit *= kUp;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = quotient(g[e], s, inv);
-            *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
-                make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
-            if (lane == 0) P.k_idx_scale[row] = s;
+                        for (int e = 0; e < 8; ++e) f[0][e] *= kUp, f[1][e] *= kUp;
+                    }
+                    codes = DT == CSA_FP32 || P.ops.norm ? fp4_codes<true>(f, unit) : fp4_codes<false>(f, unit);
+                }
+                *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
+                rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
+            }
+        } else {
+            uint32_t top = amax;  // over the eight lanes of a 128-dim block (rope lanes hold 0)
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+            if (rope_lane) {
+                uint4 *dst = reinterpret_cast<uint4 *>(rec + kRopeOffset + 32 * (lane - kNopeLanes));
+                dst[0] = pack_bf16_octet(f[0]);
+                dst[1] = pack_bf16_octet(f[1]);
+            } else {
+                const float s = e4m3_scale(top);
+                float q[2][8];
+                scaled_octet(f[0], s, q[0]);
+                scaled_octet(f[1], s, q[1]);
+                *reinterpret_cast<uint4 *>(rec + 16 * lane) =
+                    make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
+                               e4m3x4(q[1][0], q[1][1], q[1][2], q[1][3]), e4m3x4(q[1][4], q[1][5], q[1][6], q[1][7]));
+                if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + kScaleOffset + 4 * (lane >> 3)) = s;
+            }
+        }
+        if (KEYS) {
+            float g[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = 0.f;
+            if (key_lane) now.key.floats(g);
+            if (turn) {
+                // octets 8..15 are the key's rope dims: pairs 4 (lane - 8) ..
+                float2 cs[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int pair = ((lane - 8) & 7) * 4 + e;
+                    cs[e].x = __shfl_sync(kAll, own.x, pair);
+                    cs[e].y = __shfl_sync(kAll, own.y, pair);
+                }
+                if (key_lane && lane >= 8) turn_octet(g, cs);
+            }
+            const uint32_t top = __reduce_max_sync(kAll, amax_bits(amax_octet(g)));
+            if (slot.entry >= P.idx_cap) {
+                if (lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+            } else if (key_lane) {
+                const float s = e4m3_scale(top);
+                const int64_t row = (int64_t)b * P.idx_cap + slot.entry;
+                scaled_octet(g, s, g);
+                *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
+                    make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
+                if (lane == 0) P.k_idx_scale[row] = s;
+            }
         }
     }
 }
@@ -230,6 +264,7 @@ append_kernel(const __grid_constant__ AppendParams P) {
 struct ReadParams {
     Span span;
     uint4 *out;
+    int per_warp;
     int *err;
 };
 
@@ -238,53 +273,76 @@ __global__ void __launch_bounds__(kThreads)
 read_kernel(const __grid_constant__ ReadParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (token >= P.span.B * P.span.T) return;
-    const int b = token / P.span.T, t = token - b * P.span.T;
-    const Slot slot = find_slot(P.span, b, t, P.err, lane == 0);
-    if (!slot.kept) return;
-    const uint8_t *rec = P.span.cache.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
-    uint4 lo, hi;
-    if (lane >= kNopeLanes) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(rec + (FMT == CSA_FORMAT_FP4 ? kFp4RopeOffset : kRopeOffset) +
-                                                           32 * (lane - kNopeLanes));
-        lo = src[0];
-        hi = src[1];
-    } else {
-        float f[2][8];
-        if (FMT == CSA_FORMAT_FP4) {
+    const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * P.per_warp;
+    if (t0 >= P.span.B * P.span.T) return;
+    const Slot mine = find_slots(P.span, t0, P.per_warp, lane, P.err);
+    const bool rope_lane = lane >= kNopeLanes;
+    // a lane's bytes of a record: 16 codes (8 or 16 bytes) and their scale, or 32
+    // bytes of rope dims
+    struct {
+        uint4 a, b;
+        uint32_t scale, power;
+    } now, next;
+    auto fetch = [&](int j, auto &o) {
+        const int64_t record = slot_of(mine, j).record;
+        if (record < 0) return;
+        const uint8_t *rec = P.span.cache.base + record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+        if (rope_lane) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                rec + (FMT == CSA_FORMAT_FP4 ? kFp4RopeOffset : kRopeOffset) + 32 * (lane - kNopeLanes));
+            o.a = src[0];
+            o.b = src[1];
+        } else if (FMT == CSA_FORMAT_FP4) {
             const uint2 c = *reinterpret_cast<const uint2 *>(rec + 8 * lane);
-            const float s = e4m3x2_to_float2((uint16_t)rec[kFp4ScaleOffset + lane]).x * fp4_power(rec[kFp4PowerOffset]);
-            const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[o] >> (8 * e)), __NV_E2M1);
-                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-                    f[o][2 * e] = v.x * s;
-                    f[o][2 * e + 1] = v.y * s;
-                }
+            o.a.x = c.x;
+            o.a.y = c.y;
+            o.scale = rec[kFp4ScaleOffset + lane];
+            o.power = rec[kFp4PowerOffset];
         } else {
-            const uint4 c = *reinterpret_cast<const uint4 *>(rec + 16 * lane);
-            const float s = *reinterpret_cast<const float *>(rec + kScaleOffset + 4 * (lane >> 3));
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 u = e4m3x2_to_float2((uint16_t)(w[i] & 0xFFFFu));
-                const float2 v = e4m3x2_to_float2((uint16_t)(w[i] >> 16));
-                f[i >> 1][4 * (i & 1)] = u.x * s;
-                f[i >> 1][4 * (i & 1) + 1] = u.y * s;
-                f[i >> 1][4 * (i & 1) + 2] = v.x * s;
-                f[i >> 1][4 * (i & 1) + 3] = v.y * s;
-            }
+            o.a = *reinterpret_cast<const uint4 *>(rec + 16 * lane);
+            o.scale = *reinterpret_cast<const uint32_t *>(rec + kScaleOffset + 4 * (lane >> 3));
         }
-        lo = pack_bf16_octet(f[0]);
-        hi = pack_bf16_octet(f[1]);
+    };
+    fetch(0, next);
+#pragma unroll 1
+    for (int j = 0; j < P.per_warp; ++j) {
+        now = next;
+        if (j + 1 < P.per_warp) fetch(j + 1, next);
+        if (slot_of(mine, j).record < 0) continue;
+        uint4 lo = now.a, hi = now.b;
+        if (!rope_lane) {
+            const uint32_t w[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
+            float f[2][8];
+            if (FMT == CSA_FORMAT_FP4) {
+                const float s = e4m3x2_to_float2((uint16_t)now.scale).x * fp4_power(now.power);
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[o] >> (8 * e)), __NV_E2M1);
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                        f[o][2 * e] = v.x * s;
+                        f[o][2 * e + 1] = v.y * s;
+                    }
+            } else {
+                const float s = __uint_as_float(now.scale);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 u = e4m3x2_to_float2((uint16_t)(w[i] & 0xFFFFu));
+                    const float2 v = e4m3x2_to_float2((uint16_t)(w[i] >> 16));
+                    f[i >> 1][4 * (i & 1)] = u.x * s;
+                    f[i >> 1][4 * (i & 1) + 1] = u.y * s;
+                    f[i >> 1][4 * (i & 1) + 2] = v.x * s;
+                    f[i >> 1][4 * (i & 1) + 3] = v.y * s;
+                }
+            }
+            lo = pack_bf16_octet(f[0]);
+            hi = pack_bf16_octet(f[1]);
+        }
+        uint4 *dst = P.out + (int64_t)(t0 + j) * (kDim / 8) + 2 * lane;
+        dst[0] = lo;
+        dst[1] = hi;
     }
-    uint4 *dst = P.out + (int64_t)token * (kDim / 8) + 2 * lane;
-    dst[0] = lo;
-    dst[1] = hi;
 }
 
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -359,7 +417,8 @@ extern "C" CSA_API csa_status_t csa_cache_append(csa_cache_desc cache, csa_forma
     P.pos_stride = pos_stride;
     P.base = static_cast<uint8_t *>(const_cast<void *>(cache.base));
     P.err = status;
-    PdlLaunch l(dim3((B * T + kWarps - 1) / kWarps), dim3(kThreads), stream);
+    P.per_warp = tokens_per_warp(B * T);
+    PdlLaunch l(dim3((B * T + kWarps * P.per_warp - 1) / (kWarps * P.per_warp)), dim3(kThreads), stream);
     count_launch();
     const cudaError_t e = x_dtype == CSA_BF16   ? launch_append<CSA_BF16>(P, fmt, l)
                           : x_dtype == CSA_FP16 ? launch_append<CSA_FP16>(P, fmt, l)
@@ -377,7 +436,8 @@ extern "C" CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_
     if (!out || misaligned(out)) return CSA_ERR_INVALID_ARG;
     P.out = static_cast<uint4 *>(out);
     P.err = status;
-    PdlLaunch l(dim3((B * T + kWarps - 1) / kWarps), dim3(kThreads), stream);
+    P.per_warp = tokens_per_warp(B * T);
+    PdlLaunch l(dim3((B * T + kWarps * P.per_warp - 1) / (kWarps * P.per_warp)), dim3(kThreads), stream);
     count_launch();
     const cudaError_t e = fmt == CSA_FORMAT_FP4 ? cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP4>, P)
                                                 : cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP8>, P);

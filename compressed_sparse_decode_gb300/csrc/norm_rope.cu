@@ -20,116 +20,152 @@ struct NormRopeParams {
     int T, H, D, rows;
     void *out;       // BF16 values or E4M3 codes
     float *scale;    // E4M3 only
+    int per_group;   // heads a group, one after the other
     RowOps ops;
 };
 
-// A group of G lanes holds a head (NV octets a lane); each group takes R
-// consecutive heads, whose loads are all issued before the first is used.
-template <int DT, int G, int NV, int R, bool E4M3>
+// A group of G lanes holds a head (NV octets a lane) and takes per_group
+// consecutive heads, the next one's loads running under the current one. What
+// bounds the pass is DRAM only if a head costs few instructions: the rotation's
+// sines and cosines are computed once a token and block, into shared memory
+// (each head for itself took 120 of 390 instructions), the norm's weights stay in
+// registers.
+template <int DT, int G, int NV, bool E4M3>
 __global__ void __launch_bounds__(kThreads)
 norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
+    extern __shared__ float2 turns[];  // [tokens of the block][rope pairs]
     ptx::griddep_wait();
+    constexpr int kGroups = kThreads / G;
     const int gl = threadIdx.x & (G - 1);
-    const int r0 = (blockIdx.x * (kThreads / G) + threadIdx.x / G) * R;
+    const int block0 = blockIdx.x * kGroups * P.per_group;  // (rows < 2^31 - 2^20)
+    const int r0 = block0 + threadIdx.x / G * P.per_group;
     const int octets = P.D >> 3;
-    const int rope_octet = (P.D - P.ops.rope_dim) >> 3;
+    const int rope_octet = (P.D - P.ops.rope_dim) >> 3, pairs = P.ops.rope_dim >> 1;
+    const int token0 = block0 / P.H;
 
-    Octet<DT> in[R][NV];
-    int pos[R];
+    // the group's position in the tensor: token (b, t), head h
+    int token = r0 / P.H, h = r0 - token * P.H, b = token / P.T, t = token - b * P.T;
+    struct {
+        Octet<DT> x[NV];
+        int pos;
+    } now, next;
+    auto fetch = [&](int i, auto &o) {
+        o.pos = -1;
+        if (r0 + i >= P.rows) return;
+        o.pos = __ldg(P.pos + token);
+        if (o.pos < 0) return;
+        const int64_t at = b * P.seq_stride + t * P.token_stride + h * P.head_stride;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int r = r0 + i;
-        pos[i] = -1;
-        if (r < P.rows) {
-            const int token = r / P.H, h = r - token * P.H;
-            pos[i] = __ldg(P.pos + token);
-            if (pos[i] >= 0) {
-                const int b = token / P.T;
-                const int64_t at = b * P.seq_stride + (int64_t)(token - b * P.T) * P.token_stride + h * P.head_stride;
-#pragma unroll
-                for (int v = 0; v < NV; ++v)
-                    if (gl + G * v < octets) in[i][v].load(P.x, at + 8 * (gl + G * v));
-            }
+        for (int v = 0; v < NV; ++v)
+            if (gl + G * v < octets) o.x[v].load(P.x, at + 8 * (gl + G * v));
+    };
+    fetch(0, next);
+
+    if (pairs) {
+        const int last = min(block0 + kGroups * P.per_group, P.rows) - 1;
+        const int n = (last / P.H - token0 + 1) * pairs;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const int tk = i / pairs, pair = i - tk * pairs;
+            turns[i] = turn_cos_sin(__ldg(P.pos + token0 + tk), P.ops.turn[pair]);
         }
     }
-
-    float2 cs[NV][4];
-    int turned = -1;  // the position that cs holds
+    float w[NV][8];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int p = pos[i];
+    for (int v = 0; v < NV; ++v)
+        load_weights(w[v], P.ops.norm && gl + G * v < octets ? P.ops.weight : nullptr, 8 * (gl + G * v));
+    const float inv_d = 1.f / P.D;
+    __syncthreads();
+
+#pragma unroll 1
+    for (int i = 0; i < P.per_group; ++i) {
+        now = next;
+        const int tk = token;
+        if (++h == P.H) {
+            h = 0;
+            ++token;
+            if (++t == P.T) t = 0, ++b;
+        }
+        if (i + 1 < P.per_group) fetch(i + 1, next);
+        const bool live = now.pos >= 0;
         float f[NV][8];
-        float sum = 0.f;
+        float2 two = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (p >= 0 && gl + G * v < octets) {
-                in[i][v].floats(f[v]);
+            if (live && gl + G * v < octets) {
+                now.x[v].floats(f[v]);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) f[v][e] = 0.f;
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(f[v][e], f[v][e], sum);
+            square_octet(f[v], two);
         }
         if (P.ops.norm) {
+            float sum = two.x + two.y;
 #pragma unroll
             for (int o = G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv_rms = rsqrtf(sum / P.D + P.ops.eps);
+            const float inv_rms = rsqrtf(sum * inv_d + P.ops.eps);
 #pragma unroll
-            for (int v = 0; v < NV; ++v)
-                if (gl + G * v < octets) scale_octet(f[v], inv_rms, P.ops.weight, 8 * (gl + G * v));
+            for (int v = 0; v < NV; ++v) scale_octet(f[v], inv_rms, w[v]);
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int o = gl + G * v;
-            if (o >= rope_octet && o < octets && p >= 0) {
-                if (p != turned) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) cs[v][e] = turn_cos_sin(p, P.ops.turn[4 * (o - rope_octet) + e]);
-                }
-                turn_octet(f[v], cs[v]);
+            if (o >= rope_octet && o < octets && live) {
+                const float4 *cs = reinterpret_cast<const float4 *>(turns + (tk - token0) * pairs + 4 * (o - rope_octet));
+                const float4 c0 = cs[0], c1 = cs[1];
+                const float2 c[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
+                                     make_float2(c1.z, c1.w)};
+                turn_octet(f[v], c);
             }
         }
-        turned = p;
         const int64_t row = r0 + i;
         if (!E4M3) {
 #pragma unroll
             for (int v = 0; v < NV; ++v)
-                if (p >= 0 && gl + G * v < octets)
+                if (live && gl + G * v < octets)
                     reinterpret_cast<uint4 *>(P.out)[row * octets + gl + G * v] = pack_bf16_octet(f[v]);
         } else {
-            uint32_t amax = 0;
+            float m = 0.f;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) amax = amax_bits(f[v], amax);
+            for (int v = 0; v < NV; ++v) m = amax_octet(f[v], m);
+            uint32_t amax = amax_bits(m);
 #pragma unroll
             for (int o = G / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = e4m3_scale(amax), inv = 1.f / s;
+            const float s = e4m3_scale(amax);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                if (p >= 0 && gl + G * v < octets) {
+                if (live && gl + G * v < octets) {
                     float q[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) q[e] = quotient(f[v][e], s, inv);
+                    scaled_octet(f[v], s, q);
                     reinterpret_cast<uint2 *>(P.out)[row * octets + gl + G * v] =
                         make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
                 }
             }
-            if (p >= 0 && gl == 0) P.scale[row] = s;
+            if (live && gl == 0) P.scale[row] = s;
         }
     }
 }
 
+// Heads a group: as many as leave every SM eight blocks, up to 8.
 template <int DT, int G, int NV, bool E4M3>
-cudaError_t launch_rows(const NormRopeParams &P, cudaStream_t stream) {
+cudaError_t launch_rows(NormRopeParams &P, cudaStream_t stream) {
     constexpr int kGroups = kThreads / G;
-    const int ctas = (P.rows + kGroups - 1) / kGroups;
-    PdlLaunch l(dim3(ctas), dim3(kThreads), stream);
+    const int n = P.rows / (kGroups * 8 * cached_sm_count());
+    P.per_group = n < 1 ? 1 : n > 8 ? 8 : n;
+    // the rotation of the block's tokens (at most this many) has 48 KB
+    auto turn_bytes = [&]() {
+        return (size_t)((kGroups * P.per_group - 1) / P.H + 2) * (P.ops.rope_dim / 2) * sizeof(float2);
+    };
+    while (P.per_group > 1 && turn_bytes() > 48 * 1024) --P.per_group;
+    const int per_block = kGroups * P.per_group;
+    PdlLaunch l(dim3((P.rows + per_block - 1) / per_block), dim3(kThreads), stream);
+    l.cfg.dynamicSmemBytes = turn_bytes();
     count_launch();
-    return cudaLaunchKernelEx(&l.cfg, norm_rope_kernel<DT, G, NV, 1, E4M3>, P);
+    return cudaLaunchKernelEx(&l.cfg, norm_rope_kernel<DT, G, NV, E4M3>, P);
 }
 
 template <int DT, bool E4M3>
-cudaError_t launch_type(const NormRopeParams &P, cudaStream_t stream) {
+cudaError_t launch_type(NormRopeParams &P, cudaStream_t stream) {
     if (P.D <= 64) return launch_rows<DT, 8, 1, E4M3>(P, stream);
     if (P.D <= 128) return launch_rows<DT, 16, 1, E4M3>(P, stream);
     if (P.D <= 256) return launch_rows<DT, 32, 1, E4M3>(P, stream);
@@ -150,7 +186,7 @@ csa_status_t run(const void *x, csa_dtype_t dt, int64_t seq_stride, int64_t toke
     if (seq_stride < 0 || token_stride < 0 || head_stride < 0 || seq_stride % per16 || token_stride % per16 ||
         head_stride % per16)
         return CSA_ERR_INVALID_ARG;
-    if (D % 8 || D > kDim || (int64_t)B * T > (1 << 24) || (int64_t)B * T * H >= ((int64_t)1 << 31))
+    if (D % 8 || D > kDim || (int64_t)B * T > (1 << 24) || (int64_t)B * T * H >= ((int64_t)1 << 31) - (1 << 20))
         return CSA_ERR_UNSUPPORTED;
     NormRopeParams P;
     if (!make_row_ops(how, D, &P.ops)) return CSA_ERR_INVALID_ARG;

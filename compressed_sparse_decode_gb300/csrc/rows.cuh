@@ -71,13 +71,25 @@ inline bool make_row_ops(const csa_norm_rope *how, int D, RowOps *o) {
 // 64-bit integer product, exact but for the fraction's own rounding (2^-65 of
 // a turn a position), so far positions keep their angle and no double
 // arithmetic runs (this GPU does two fp64 FMAs a clock and SM). The upper 32
-// bits as a signed number are the angle in (-1/2, 1/2] turn; the special
-// function unit's sine and cosine are off by about 4e-7 there.
+// bits are taken to the nearest quarter turn; on the rest, |x| <= pi / 4, the
+// Taylor polynomials to x^9 and x^10 are within 4e-9 and 2e-10 of sine and
+// cosine, below the fp32 rounding of the sum (the special function unit's are
+// off by 4e-7, which changes an E4M3 code now and then).
 __device__ __forceinline__ float2 turn_cos_sin(int64_t p, uint64_t turn) {
-    const int32_t part = (int32_t)(((uint64_t)p * turn) >> 32);
-    float sn, cs;
-    __sincosf((float)part * 1.4629180792671596e-9f, &sn, &cs);  // 2 pi / 2^32
-    return make_float2(cs, sn);
+    const uint32_t part = (uint32_t)(((uint64_t)p * turn) >> 32);
+    const uint32_t quarter = (part + 0x20000000u) >> 30;  // modulo 4
+    const float x = (float)(int32_t)(part - (quarter << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    float s = fmaf(y, 1.f / 362880.f, -1.f / 5040.f), c = fmaf(y, -1.f / 3628800.f, 1.f / 40320.f);
+    s = fmaf(s, y, 1.f / 120.f);
+    c = fmaf(c, y, -1.f / 720.f);
+    s = fmaf(s, y, -1.f / 6.f);
+    c = fmaf(c, y, 1.f / 24.f);
+    s = fmaf(s * y, x, x);
+    c = fmaf(c, y, -0.5f);
+    c = fmaf(c, y, 1.f);
+    const float cs = (quarter & 1u) ? s : c, sn = (quarter & 1u) ? c : s;
+    return make_float2((quarter + 1u) & 2u ? -cs : cs, quarter & 2u ? -sn : sn);
 }
 
 // Eight consecutive elements: loaded as 16-byte vectors, read as fp32. (Plain
@@ -149,24 +161,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 
-// Largest |f| of an octet as its bits: the order of the bits is the order of
-// the magnitudes, and a NaN is above them all (a float maximum would drop it).
-__device__ __forceinline__ uint32_t amax_bits(const float (&f)[8], uint32_t m = 0) {
+// Largest |f| of an octet, NaN if one is (a plain maximum would drop it).
+__device__ __forceinline__ float amax_octet(const float (&f)[8], float m = 0.f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(f[i])));
     return m;
 }
+// As bits, whose order is that of the magnitudes, with NaN above them all.
+__device__ __forceinline__ uint32_t amax_bits(float amax) { return __float_as_uint(amax) & 0x7FFFFFFFu; }
 
 // amax / 448 as a multiplier: 1 for an all-zero block.
 __device__ __forceinline__ float e4m3_scale(uint32_t amax) {
-    return amax ? __fdiv_rn(__uint_as_float(amax), 448.f) : 1.f;
+    return amax ? __uint_as_float(amax) * (1.f / 448.f) : 1.f;
 }
 
-// x / s correctly rounded for ordinary sizes, given inv = 1 / s (rounded):
-// one Newton step on the quotient. A scale so small that 1 / s or the
-// remainder leaves the normal range is divided by.
+// x / s correctly rounded, given inv = 1 / s (rounded): one Newton step on the
+// quotient. s is in the middle of the range (see fp4_codes).
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
-    if (s < 1e-30f) return __fdiv_rn(x, s);
     const float q = x * inv;
     return fmaf(fmaf(-q, s, x), inv, q);
 }
@@ -184,17 +195,47 @@ __device__ __forceinline__ float sticky_quotient(float x, float s, float inv) {
     return __uint_as_float((up ? b : b - 1u) | 1u);
 }
 
+// f / s for the E4M3 codes of an octet, to an ulp or two (both times 2^60 where
+// 1 / s would leave the range).
+__device__ __forceinline__ void scaled_octet(const float (&f)[8], float s, float (&q)[8]) {
+    const float up = s < 1e-30f ? 1.152921504606846976e18f : 1.f;
+    const float inv = __frcp_rn(s * up);
+    const float2 u2 = make_float2(up, up), i2 = make_float2(inv, inv);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), u2), i2);
+        q[2 * e] = v.x;
+        q[2 * e + 1] = v.y;
+    }
+}
+
+// Sum of the squares of an octet, added to two running sums.
+__device__ __forceinline__ void square_octet(const float (&f)[8], float2 &sum) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = make_float2(f[2 * e], f[2 * e + 1]);
+        sum = __ffma2_rn(v, v, sum);
+    }
+}
+
+// The norm's weights of an octet (ones without any).
+__device__ __forceinline__ void load_weights(float (&w)[8], const float *weight, int at) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 1.f;
+    if (!weight) return;
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(weight + at));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(weight + at) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
 // y_d = x_d * inv_rms * w_d for one octet.
-__device__ __forceinline__ void scale_octet(float (&f)[8], float inv_rms, const float *weight, int at) {
-    if (weight) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(weight + at));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(weight + at) + 1);
-        const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void scale_octet(float (&f)[8], float inv_rms, const float (&w)[8]) {
+    const float2 r = make_float2(inv_rms, inv_rms);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f[i] * inv_rms * w[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= inv_rms;
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), r), make_float2(w[2 * e], w[2 * e + 1]));
+        f[2 * e] = v.x;
+        f[2 * e + 1] = v.y;
     }
 }
 

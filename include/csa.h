@@ -364,7 +364,7 @@ typedef struct {
  *         rows of the output are left as they were
  *   out   [B,T,H,D] BF16, dense. It may be x itself when x is dense BF16; any
  *         other overlap with x is not allowed.
- * Requires B, T, H >= 1, B*T <= 2^24, B*T*H < 2^31, D a multiple of 8 up to
+ * Requires B, T, H >= 1, B*T <= 2^24, B*T*H < 2^31 - 2^20, D a multiple of 8 up to
  * 512 and rope_dim a multiple of 8 up to min(D, 256). The status word is
  * accepted as by every compute call; nothing is recorded in it. */
 CSA_API csa_status_t csa_head_norm_rope(const void *x, csa_dtype_t x_dtype, int64_t x_seq_stride,
@@ -419,8 +419,8 @@ typedef struct {
  * with amax over the 448 nope dims, E = the smallest whole number with amax <=
  * 6 * 448 * 2^E (at least -111; 0 when all are zero), the block scale s =
  * e4m3(max |y| of the block / 6 * 2^-E), code = e2m1(y / (s * 2^E)), ties to
- * even in both, codes 0 where s is 0. These quotients are decided as if
- * computed exactly. An infinite or NaN nope dim makes its FP8 block or its
+ * even in both, codes 0 where s is 0; the 4-bit quotients are decided as if
+ * computed exactly, those of E4M3 codes are fp32. An infinite or NaN nope dim makes its FP8 block or its
  * 4-bit record read back as NaN in every nope dim.
  * An entry outside the cache is not stored (CSA_ERR_BAD_INDEX, also for
  * first < 0 or a count outside [0, T], which is then clamped). Every other
