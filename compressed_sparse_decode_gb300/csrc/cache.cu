@@ -60,10 +60,6 @@ __device__ __forceinline__ Slot find_slots(const Span &s, int t0, int n, int lan
     if (lane < n && token < s.B * s.T) o = find_slot(s, token / s.T, token % s.T, err);
     return o;
 }
-__device__ __forceinline__ Slot slot_of(const Slot &mine, int j) {
-    return {__shfl_sync(kAll, mine.entry, j), __shfl_sync(kAll, mine.record, j)};
-}
-
 // Tokens a warp: as many as leave every SM four blocks, up to 8. (They share the
 // look-up, the norm's weights and the rotation's table, and the next one's loads
 // run under the current one: 49k tokens into FP8 with keys took 50 us with one.)
@@ -124,17 +120,24 @@ append_kernel(const __grid_constant__ AppendParams P) {
     const Slot mine = find_slots(P.span, t0, P.per_warp, lane, P.err);
     const bool key_lane = KEYS && lane < kIdxDim / 8;  // 16 lanes hold the key's octets
     const bool turn = P.ops.rope_dim > 0;
+    __shared__ __align__(16) float2 warp_cs[kWarps][32];  // of the warp's current token
+    float2 *pair_cs = warp_cs[threadIdx.x >> 5];
     const uint64_t pair_turn = turn ? P.ops.turn[lane] : 0;
     float w[2][8];  // the norm's weights of this lane's dims
     load_weights(w[0], P.ops.norm ? P.ops.weight : nullptr, 16 * lane);
     load_weights(w[1], P.ops.norm ? P.ops.weight : nullptr, 16 * lane + 8);
     struct {
         Octet<DT> x[2], key;
+        int64_t record;
+        int b;
     } now, next;
+    int nb = t0 / P.span.T, nt = t0 - nb * P.span.T;  // the token to fetch
     auto fetch = [&](int j, auto &o) {
-        const Slot s = slot_of(mine, j);
-        if (s.record < 0) return;
-        const int b = (t0 + j) / P.span.T, t = t0 + j - b * P.span.T;
+        const int b = nb, t = nt;
+        if (++nt == P.span.T) nt = 0, ++nb;
+        o.b = b;
+        o.record = __shfl_sync(kAll, mine.record, j);
+        if (o.record < 0) return;
         const int64_t at = b * P.seq_stride + t * P.token_stride + 16 * lane;
         o.x[0].load(P.x, at);
         o.x[1].load(P.x, at + 8);
@@ -145,12 +148,14 @@ append_kernel(const __grid_constant__ AppendParams P) {
     for (int j = 0; j < P.per_warp; ++j) {
         now = next;
         if (j + 1 < P.per_warp) fetch(j + 1, next);
-        const Slot slot = slot_of(mine, j);
-        if (slot.record < 0) continue;
-        const int b = (t0 + j) / P.span.T;
-        const int64_t p = slot.entry * P.pos_stride;
-        float2 own = make_float2(1.f, 0.f);  // lane i: pair i
-        if (turn) own = turn_cos_sin(p, pair_turn);
+        if (now.record < 0) continue;
+        const int b = now.b;
+        const int64_t entry = __shfl_sync(kAll, mine.entry, j);
+        if (turn) {
+            __syncwarp();
+            pair_cs[lane] = turn_cos_sin(entry * P.pos_stride, pair_turn);
+            __syncwarp();
+        }
 
         float f[2][8];
         now.x[0].floats(f[0]);
@@ -168,20 +173,13 @@ append_kernel(const __grid_constant__ AppendParams P) {
         }
         const bool rope_lane = lane >= kNopeLanes;
         if (turn) {
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                float2 cs[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int pair = ((lane - kNopeLanes) & 3) * 8 + 4 * o + e;
-                    cs[e].x = __shfl_sync(kAll, own.x, pair);
-                    cs[e].y = __shfl_sync(kAll, own.y, pair);
-                }
-                if (rope_lane) turn_octet(f[o], cs);
+            if (rope_lane) {
+                turn_octet(f[0], *reinterpret_cast<const float2(*)[4]>(pair_cs + 8 * (lane - kNopeLanes)));
+                turn_octet(f[1], *reinterpret_cast<const float2(*)[4]>(pair_cs + 8 * (lane - kNopeLanes) + 4));
             }
         }
         const uint32_t amax = rope_lane ? 0u : amax_bits(amax_octet(f[1], amax_octet(f[0])));
-        uint8_t *rec = P.base + slot.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+        uint8_t *rec = P.base + now.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
         if (FMT == CSA_FORMAT_FP4) {
             const uint32_t top = __reduce_max_sync(kAll, amax);
             const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
@@ -237,21 +235,14 @@ append_kernel(const __grid_constant__ AppendParams P) {
             if (key_lane) now.key.floats(g);
             if (turn) {
                 // octets 8..15 are the key's rope dims: pairs 4 (lane - 8) ..
-                float2 cs[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int pair = ((lane - 8) & 7) * 4 + e;
-                    cs[e].x = __shfl_sync(kAll, own.x, pair);
-                    cs[e].y = __shfl_sync(kAll, own.y, pair);
-                }
-                if (key_lane && lane >= 8) turn_octet(g, cs);
+                if (key_lane && lane >= 8) turn_octet(g, *reinterpret_cast<const float2(*)[4]>(pair_cs + 4 * (lane - 8)));
             }
             const uint32_t top = __reduce_max_sync(kAll, amax_bits(amax_octet(g)));
-            if (slot.entry >= P.idx_cap) {
+            if (entry >= P.idx_cap) {
                 if (lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
             } else if (key_lane) {
                 const float s = e4m3_scale(top);
-                const int64_t row = (int64_t)b * P.idx_cap + slot.entry;
+                const int64_t row = (int64_t)b * P.idx_cap + entry;
                 scaled_octet(g, s, g);
                 *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
                     make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
@@ -282,11 +273,12 @@ read_kernel(const __grid_constant__ ReadParams P) {
     struct {
         uint4 a, b;
         uint32_t scale, power;
+        int64_t record;
     } now, next;
     auto fetch = [&](int j, auto &o) {
-        const int64_t record = slot_of(mine, j).record;
-        if (record < 0) return;
-        const uint8_t *rec = P.span.cache.base + record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+        o.record = __shfl_sync(kAll, mine.record, j);
+        if (o.record < 0) return;
+        const uint8_t *rec = P.span.cache.base + o.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
         if (rope_lane) {
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 rec + (FMT == CSA_FORMAT_FP4 ? kFp4RopeOffset : kRopeOffset) + 32 * (lane - kNopeLanes));
@@ -308,7 +300,7 @@ read_kernel(const __grid_constant__ ReadParams P) {
     for (int j = 0; j < P.per_warp; ++j) {
         now = next;
         if (j + 1 < P.per_warp) fetch(j + 1, next);
-        if (slot_of(mine, j).record < 0) continue;
+        if (now.record < 0) continue;
         uint4 lo = now.a, hi = now.b;
         if (!rope_lane) {
             const uint32_t w[4] = {now.a.x, now.a.y, now.a.z, now.a.w};

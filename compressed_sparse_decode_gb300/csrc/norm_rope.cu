@@ -25,7 +25,7 @@ struct NormRopeParams {
 };
 
 // A group of G lanes holds a head (NV octets a lane) and takes per_group
-// consecutive heads, the next one's loads running under the current one. What
+// consecutive heads, the loads of the next two in flight. What
 // bounds the pass is DRAM only if a head costs few instructions: the rotation's
 // sines and cosines are computed once a token and block, into shared memory
 // (each head for itself took 120 of 390 instructions), the norm's weights stay in
@@ -45,21 +45,28 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
 
     // the group's position in the tensor: token (b, t), head h
     int token = r0 / P.H, h = r0 - token * P.H, b = token / P.T, t = token - b * P.T;
-    struct {
+    struct Head {
         Octet<DT> x[NV];
-        int pos;
-    } now, next;
-    auto fetch = [&](int i, auto &o) {
+        int pos, token;
+    } even, odd;  // two heads' loads in flight
+    auto fetch = [&](int i, Head &o) {
         o.pos = -1;
-        if (r0 + i >= P.rows) return;
+        if (i >= P.per_group || r0 + i >= P.rows) return;
+        o.token = token;
         o.pos = __ldg(P.pos + token);
-        if (o.pos < 0) return;
         const int64_t at = b * P.seq_stride + t * P.token_stride + h * P.head_stride;
+        if (++h == P.H) {
+            h = 0;
+            ++token;
+            if (++t == P.T) t = 0, ++b;
+        }
+        if (o.pos < 0) return;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             if (gl + G * v < octets) o.x[v].load(P.x, at + 8 * (gl + G * v));
     };
-    fetch(0, next);
+    fetch(0, even);
+    fetch(1, odd);
 
     if (pairs) {
         const int last = min(block0 + kGroups * P.per_group, P.rows) - 1;
@@ -76,16 +83,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     const float inv_d = 1.f / P.D;
     __syncthreads();
 
-#pragma unroll 1
-    for (int i = 0; i < P.per_group; ++i) {
-        now = next;
-        const int tk = token;
-        if (++h == P.H) {
-            h = 0;
-            ++token;
-            if (++t == P.T) t = 0, ++b;
-        }
-        if (i + 1 < P.per_group) fetch(i + 1, next);
+    auto finish = [&](int i, const Head &now) {
         const bool live = now.pos >= 0;
         float f[NV][8];
         float2 two = make_float2(0.f, 0.f);
@@ -111,7 +109,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
         for (int v = 0; v < NV; ++v) {
             const int o = gl + G * v;
             if (o >= rope_octet && o < octets && live) {
-                const float4 *cs = reinterpret_cast<const float4 *>(turns + (tk - token0) * pairs + 4 * (o - rope_octet));
+                const float4 *cs = reinterpret_cast<const float4 *>(turns + (now.token - token0) * pairs + 4 * (o - rope_octet));
                 const float4 c0 = cs[0], c1 = cs[1];
                 const float2 c[4] = {make_float2(c0.x, c0.y), make_float2(c0.z, c0.w), make_float2(c1.x, c1.y),
                                      make_float2(c1.z, c1.w)};
@@ -143,6 +141,13 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
             }
             if (live && gl == 0) P.scale[row] = s;
         }
+    };
+#pragma unroll 1
+    for (int i = 0; i < P.per_group; i += 2) {
+        finish(i, even);
+        fetch(i + 2, even);
+        finish(i + 1, odd);
+        fetch(i + 3, odd);
     }
 }
 

@@ -198,14 +198,18 @@ __device__ __forceinline__ float sticky_quotient(float x, float s, float inv) {
 // f / s for the E4M3 codes of an octet, to an ulp or two (both times 2^60 where
 // 1 / s would leave the range).
 __device__ __forceinline__ void scaled_octet(const float (&f)[8], float s, float (&q)[8]) {
-    const float up = s < 1e-30f ? 1.152921504606846976e18f : 1.f;
+    float up = 1.f;
+    if (s < 1e-30f) up = 1.152921504606846976e18f;
     const float inv = __frcp_rn(s * up);
-    const float2 u2 = make_float2(up, up), i2 = make_float2(inv, inv);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float2 v = __fmul2_rn(__fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), u2), i2);
+        const float2 v = __fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), make_float2(inv, inv));
         q[2 * e] = v.x;
         q[2 * e + 1] = v.y;
+    }
+    if (up != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] *= up;
     }
 }
 
