@@ -173,8 +173,8 @@ def _check(status: int, where: str):
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle itself: a Stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -193,6 +193,7 @@ def _ptr(t: torch.Tensor | None, name: str, dtype=None, shape=None):
 
 
 _status_words: dict[int, torch.Tensor] = {}
+_status_ptrs: dict[int, int] = {}  # their addresses (the words live as long as the process)
 
 
 def status_word(device=None) -> torch.Tensor:
@@ -207,6 +208,7 @@ def status_word(device=None) -> torch.Tensor:
         if w is None:
             w = torch.zeros(1, dtype=torch.int32, device=dev)
             _status_words[dev.index] = w
+            _status_ptrs[dev.index] = w.data_ptr()
     return w
 
 
@@ -243,6 +245,9 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
         d.max_pages = int(block_table.shape[-1])
     d._keepalive = (rec, block_table)  # noqa: SLF001
     d._fmt = fmt  # noqa: SLF001
+    d._dev = rec.get_device()  # noqa: SLF001
+    d._seqs = None if block_table is None else block_table.numel() // max(1, block_table.shape[-1])  # noqa: SLF001
+    d._copied = rec.data_ptr() != records.data_ptr()  # noqa: SLF001
     return d
 
 
@@ -462,6 +467,13 @@ def csa_decode_step(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, soft
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _own_status(status, dev: int) -> int:
+    """Address of the status word: the caller's, or the device's default one."""
+    if status is not None:
+        return _arg(status, "status", torch.int32, (1,), dev)
+    return _status_ptrs.get(dev) or _status(None, torch.device("cuda", dev))
+
+
 def _dev(t: torch.Tensor, name: str) -> int:
     """Index of the CUDA device that ``t`` is on, which has to be the current one
     (the library launches there)."""
@@ -495,7 +507,7 @@ def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
 def _strides(t: torch.Tensor) -> list:
     """Strides of the leading dimensions; 0 where a dimension has one element
     (PyTorch leaves any number there)."""
-    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride())]
+    return [s if n != 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
 
 
 def _how(norm: bool, weight, eps: float, rope_dim: int, rope_theta: float, D: int, dev: int) -> csa_norm_rope:
@@ -515,10 +527,10 @@ def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6
     dev = _dev(x, "x")
     if out is None:
         out = torch.empty((B, T, H, D), dtype=torch.bfloat16, device=x.device)
-    _check(load().csa_head_norm_rope(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+    _check((_lib or load()).csa_head_norm_rope(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
                                      _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                      _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
-                                     _arg(out, "out", torch.bfloat16, (B, T, H, D), dev), _status(status, x.device),
+                                     _arg(out, "out", torch.bfloat16, (B, T, H, D), dev), _own_status(status, dev),
                                      _stream(stream)), "csa_head_norm_rope")
     return out
 
@@ -533,12 +545,12 @@ def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float =
         codes = torch.empty((B, T, H, D), dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = torch.empty((B, T, H), dtype=torch.float32, device=x.device)
-    _check(load().csa_head_norm_rope_e4m3(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+    _check((_lib or load()).csa_head_norm_rope_e4m3(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
                                           _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                           _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
                                           _arg(codes, "codes", torch.uint8, (B, T, H, D), dev),
                                           _arg(scale, "scale", torch.float32, (B, T, H), dev),
-                                          _status(status, x.device), _stream(stream)), "csa_head_norm_rope_e4m3")
+                                          _own_status(status, dev), _stream(stream)), "csa_head_norm_rope_e4m3")
     return codes, scale
 
 
@@ -553,6 +565,8 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
     ``k_idx`` [B, Ncap, 128] and ``k_idx_scale`` [B, Ncap]. See include/csa.h."""
     B, T, _ = x.shape
     dev = _dev(x, "x")
+    if getattr(cache, "_copied", False):
+        raise ValueError("the cache's records were not contiguous: the description holds a copy of them")
     idx = None
     if key is not None:
         ncap = k_idx.shape[1]
@@ -563,12 +577,12 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
                                _arg(k_idx, "k_idx", k_dtype, (B, ncap, IDX_DIM), dev),
                                _arg(k_idx_scale, "k_idx_scale", torch.float32, (B, ncap), dev), ncap)
     rope_dim, theta = (0, 0.0) if rope_theta is None else (ROPE, rope_theta)
-    _check(load().csa_cache_append(cache, _fmt_of(cache), 1 if ring else 0, _rows(x, "x", (B, T, DIM), dev),
+    _check((_lib or load()).csa_cache_append(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0, _rows(x, "x", (B, T, DIM), dev),
                                    _DTYPES[x.dtype], *_strides(x),
                                    _arg(first, "first", torch.int32, (B,), dev),
                                    None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
                                    pos_stride, _how(norm, weight, eps, rope_dim, theta, DIM, dev),
-                                   idx, _status(status, x.device), _stream(stream)), "csa_cache_append")
+                                   idx, _own_status(status, dev), _stream(stream)), "csa_cache_append")
 
 
 def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = False, out=None, stream=None,
@@ -580,10 +594,10 @@ def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = Fal
     B = first.shape[0]
     if out is None:
         out = torch.zeros((B, T, DIM), dtype=torch.bfloat16, device=first.device)
-    _check(load().csa_cache_read(cache, _fmt_of(cache), 1 if ring else 0,
+    _check((_lib or load()).csa_cache_read(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0,
                                  _arg(first, "first", torch.int32, (B,), dev),
                                  None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
-                                 _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _status(status, first.device),
+                                 _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _own_status(status, dev),
                                  _stream(stream)), "csa_cache_read")
     return out
 
@@ -606,14 +620,14 @@ def csa_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
     if ws is None:
         ws = workspace(OP_ATTENTION, B, T, comp.seq_capacity, k, q.device)
     i32, f32 = torch.int32, torch.float32
-    _check(load().csa_sink_attention_decode_fp4(
+    _check((_lib or load()).csa_sink_attention_decode_fp4(
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
-        _format(comp, FORMAT_FP4, "csa_sink_attention_decode_fp4"),
+        _format(_cache(comp, B, dev), FORMAT_FP4, "csa_sink_attention_decode_fp4"),
         _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
         _arg(topk_idx, "topk_idx", i32, (B, T, k), dev), _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
         _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, k,
         None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
-        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)),
         "csa_sink_attention_decode_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
@@ -634,13 +648,13 @@ def hca_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
     if ws is None:
         ws = workspace(OP_HCA_ATTENTION, B, T, comp.seq_capacity, 0, q.device)
     i32, f32 = torch.int32, torch.float32
-    _check(load().hca_sink_attention_decode_fp4(
+    _check((_lib or load()).hca_sink_attention_decode_fp4(
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
-        _format(comp, FORMAT_FP4, "hca_sink_attention_decode_fp4"), _arg(n_comp, "n_comp", i32, (B,), dev),
+        _format(_cache(comp, B, dev), FORMAT_FP4, "hca_sink_attention_decode_fp4"), _arg(n_comp, "n_comp", i32, (B,), dev),
         _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
         _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, m_hca,
         None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
-        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)),
         "hca_sink_attention_decode_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
@@ -662,25 +676,36 @@ def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, 
     if ws is None:
         ws = workspace(OP_DECODE_STEP, B, T, Ncap, k, q.device)
     u8, i32, f32 = (torch.uint8, torch.float8_e4m3fn), torch.int32, torch.float32
-    _check(load().csa_decode_step_fp4(
+    _check((_lib or load()).csa_decode_step_fp4(
         _ptr(q_idx, "q_idx", u8, (B, T, IDX_HEADS, IDX_DIM)),
         _arg(q_idx_scale, "q_idx_scale", f32, (B, T, IDX_HEADS), dev), _arg(w_idx, "w_idx", f32, (B, T, IDX_HEADS), dev),
         _ptr(k_idx, "k_idx", u8, (B, Ncap, IDX_DIM)), _arg(k_idx_scale, "k_idx_scale", f32, (B, Ncap), dev),
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
-        _format(comp, FORMAT_FP4, "csa_decode_step_fp4"),
+        _format(_cache(comp, B, dev), FORMAT_FP4, "csa_decode_step_fp4"),
         _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
         _arg(q_pos, "q_pos", i32, (B, T), dev), _arg(n_comp, "n_comp", i32, (B,), dev), B, T, Ncap, m, k,
         None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
         _arg(lse, "lse", f32, (B, T, HEADS), dev),
         None if topk_idx is None else _arg(topk_idx, "topk_idx", i32, (B, T, k), dev),
         None if topk_cnt is None else _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
-        epi, *_ws(ws, dev), _status(status, q.device), _stream(stream)), "csa_decode_step_fp4")
+        epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)), "csa_decode_step_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
 
 def _ws(ws, dev: int):
     """(pointer, bytes) of a workspace; (None, 0) for none."""
     return (None, 0) if ws is None else (_arg(ws, "workspace", torch.uint8, ws.shape, dev), ws.numel())
+
+
+def _cache(cache: csa_cache_desc, B: int, dev: int) -> csa_cache_desc:
+    """The description itself, if its records lie on device ``dev`` and its block
+    table has a row for each of the B sequences."""
+    if getattr(cache, "_dev", dev) != dev:
+        raise ValueError(f"the cache is on cuda:{cache._dev}, not on cuda:{dev}")
+    seqs = getattr(cache, "_seqs", None)
+    if seqs is not None and seqs < B:
+        raise ValueError(f"the cache's block table has {seqs} rows for {B} sequences")
+    return cache
 
 
 def _fmt_of(cache: csa_cache_desc) -> int:

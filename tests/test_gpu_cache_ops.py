@@ -379,3 +379,21 @@ def test_other_stream_and_graph_replay(cuda_lib):
     for a, b in zip(got, (pool, out, codes, scale)):
         assert torch.equal(a, b)
     assert csd.csa_read_device_error() == 0
+
+
+def test_descriptions_that_do_not_fit_the_call_are_refused(cuda_lib):
+    csd = cuda_lib
+    pool = torch.zeros((4, 2, 384), dtype=torch.uint8, device="cuda")
+    table = torch.arange(2, dtype=torch.int32, device="cuda").view(2, 1)
+    first = torch.zeros(3, dtype=torch.int32, device="cuda")
+    x = torch.zeros((3, 1, 512), dtype=torch.bfloat16, device="cuda")
+    two = csd.cache_desc(pool, 4, block_table=table, page_records=4, fmt=csd.FORMAT_FP4)
+    for call in (lambda: csd.csa_cache_append(two, x, first), lambda: csd.csa_cache_read(two, first, None, 1)):
+        with pytest.raises(ValueError, match="2 rows for 3 sequences"):
+            call()
+    copy = csd.cache_desc(pool.transpose(0, 1), 4, seq_stride=4, fmt=csd.FORMAT_FP4)
+    with pytest.raises(ValueError, match="not contiguous"):
+        csd.csa_cache_append(copy, x[:1], first[:1])
+    with pytest.raises(ValueError, match="status"):
+        csd.csa_cache_append(two, x[:2], first[:2], status=torch.zeros(1, device="cuda"))
+    assert csd.csa_read_device_error() == 0
