@@ -510,6 +510,35 @@ def _strides(t: torch.Tensor) -> list:
     return [s if n != 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
 
 
+def _new(make, shape, dtype, device, stream) -> torch.Tensor:
+    """make(shape) (torch.empty or torch.zeros) for a call on ``stream``: from
+    that stream's memory and, where it writes, in its order."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(s):
+        return make(shape, dtype=dtype, device=device)
+
+
+def _attention_outputs(B: int, T: int, device, stream, out, lse, fp4_out: bool, out_fp4, out_fp4_scale):
+    """The outputs of an attention call; those that the caller did not pass, made here."""
+    if fp4_out:
+        if out_fp4 is None:
+            out_fp4 = _new(torch.empty, (B, T, HEADS, DIM // 2), torch.uint8, device, stream)
+        if out_fp4_scale is None:
+            out_fp4_scale = _new(torch.empty, (B, T, HEADS, DIM // SCALE_BLOCK), torch.float32, device, stream)
+    elif out is None:
+        out = _new(torch.empty, (B, T, HEADS, DIM), torch.bfloat16, device, stream)
+    if lse is None:
+        lse = _new(torch.empty, (B, T, HEADS), torch.float32, device, stream)
+    return out, lse, out_fp4, out_fp4_scale
+
+
+def _own_workspace(op: int, B: int, T: int, Ncap: int, k: int, device, stream):
+    n = csa_workspace_bytes(op, B, T, Ncap, k)
+    return _new(torch.empty, (n,), torch.uint8, device, stream) if n else None
+
+
 def _how(norm: bool, weight, eps: float, rope_dim: int, rope_theta: float, D: int, dev: int) -> csa_norm_rope:
     w = _arg(weight, "weight", torch.float32, (D,), dev) if weight is not None else None
     return csa_norm_rope(1 if norm else 0, eps, w, rope_dim, rope_theta)
@@ -526,7 +555,7 @@ def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6
     B, T, H, D = x.shape
     dev = _dev(x, "x")
     if out is None:
-        out = torch.empty((B, T, H, D), dtype=torch.bfloat16, device=x.device)
+        out = _new(torch.empty, (B, T, H, D), torch.bfloat16, x.device, stream)
     _check((_lib or load()).csa_head_norm_rope(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
                                      _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                      _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
@@ -542,9 +571,9 @@ def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float =
     B, T, H, D = x.shape
     dev = _dev(x, "x")
     if codes is None:
-        codes = torch.empty((B, T, H, D), dtype=torch.uint8, device=x.device)
+        codes = _new(torch.empty, (B, T, H, D), torch.uint8, x.device, stream)
     if scale is None:
-        scale = torch.empty((B, T, H), dtype=torch.float32, device=x.device)
+        scale = _new(torch.empty, (B, T, H), torch.float32, x.device, stream)
     _check((_lib or load()).csa_head_norm_rope_e4m3(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
                                           _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                           _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
@@ -568,6 +597,8 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
     if getattr(cache, "_copied", False):
         raise ValueError("the cache's records were not contiguous: the description holds a copy of them")
     idx = None
+    if (key is None) != (k_idx is None) or (key is None) != (k_idx_scale is None):
+        raise ValueError("key, k_idx and k_idx_scale go together")
     if key is not None:
         ncap = k_idx.shape[1]
         if key.dtype != x.dtype:
@@ -593,7 +624,7 @@ def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = Fal
     dev = _dev(first, "first")
     B = first.shape[0]
     if out is None:
-        out = torch.zeros((B, T, DIM), dtype=torch.bfloat16, device=first.device)
+        out = _new(torch.zeros, (B, T, DIM), torch.bfloat16, first.device, stream)
     _check((_lib or load()).csa_cache_read(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0,
                                  _arg(first, "first", torch.int32, (B,), dev),
                                  None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
@@ -612,13 +643,11 @@ def csa_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
     B, T, k = topk_idx.shape
     R = swa_ring.shape[1]
     dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, T, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
     epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
-    if out is None and not fp4_out:
-        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = workspace(OP_ATTENTION, B, T, comp.seq_capacity, k, q.device)
+        ws = _own_workspace(OP_ATTENTION, B, T, comp.seq_capacity, k, q.device, stream)
     i32, f32 = torch.int32, torch.float32
     _check((_lib or load()).csa_sink_attention_decode_fp4(
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
@@ -640,13 +669,11 @@ def hca_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
     B, T = q_pos.shape
     R = swa_ring.shape[1]
     dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, T, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
     epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
-    if out is None and not fp4_out:
-        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = workspace(OP_HCA_ATTENTION, B, T, comp.seq_capacity, 0, q.device)
+        ws = _own_workspace(OP_HCA_ATTENTION, B, T, comp.seq_capacity, 0, q.device, stream)
     i32, f32 = torch.int32, torch.float32
     _check((_lib or load()).hca_sink_attention_decode_fp4(
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
@@ -668,13 +695,11 @@ def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, 
     Ncap = k_idx.shape[1]
     R = swa_ring.shape[1]
     dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, T, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
     epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
-    if out is None and not fp4_out:
-        out = torch.empty((B, T, HEADS, DIM), dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty((B, T, HEADS), dtype=torch.float32, device=q.device)
     if ws is None:
-        ws = workspace(OP_DECODE_STEP, B, T, Ncap, k, q.device)
+        ws = _own_workspace(OP_DECODE_STEP, B, T, Ncap, k, q.device, stream)
     u8, i32, f32 = (torch.uint8, torch.float8_e4m3fn), torch.int32, torch.float32
     _check((_lib or load()).csa_decode_step_fp4(
         _ptr(q_idx, "q_idx", u8, (B, T, IDX_HEADS, IDX_DIM)),

@@ -30,10 +30,11 @@
 // of the own candidates (QK and PV), and "peer", the own dims of the other
 // CTA's candidates (PV only). A pointer warp resolves the records, four warps copy
 // the pieces' bytes into staging (cp.async; a cp.async.bulk a record took 80
-// cycles each, 2.5 times this kernel's time), eight warps unpack them, exactly (see csa_format_t), to BF16 in the MMA's layout, one
-// 32 KB buffer a kind. Order of a block: oth(i + 1), peer(i), own(i + 1), and
-// QK(i + 1) over oth, PV(i), QK(i + 1) over own: the chain own -> QK -> softmax ->
-// PV -> own of the next block sets the pace, the rest runs beside it.
+// cycles each, 2.5 times this kernel's time), eight warps unpack them, exactly
+// (see csa_format_t), to BF16 in the MMA's layout, one 32 KB buffer a kind. Order
+// of a block: oth(i + 1), peer(i), own(i + 1), and QK(i + 1) over oth, PV(i),
+// QK(i + 1) over own: the chain own -> QK -> softmax -> PV -> own of the next
+// block sets the pace, the rest runs beside it.
 // Every role's loop is kept short and every helper at one place: the instruction
 // caches are shared by all warps and by neighbouring SMs (a second copy of the
 // unpacking, one per rank, cost 9 %).
@@ -144,6 +145,10 @@ __device__ __forceinline__ Unit make_unit(const Params &P) {
     u.n_blocks = (u.ce - u.cb + kBlock - 1) / kBlock;
     return u;
 }
+
+// A factor for values of this magnitude so that the reciprocal of their E2M1
+// multiplier stays in range.
+__device__ __forceinline__ float upscale(float amax) { return amax < 7.9e-31f ? 1.2676506002282294e30f : 1.f; }
 
 // 16-byte chunk cc of row `row` of a swizzled block of 128-byte rows.
 __device__ __forceinline__ uint4 *sw128(uint8_t *block, int row, int cc) {
@@ -270,8 +275,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
     extern __shared__ uint8_t smem_raw[];
     AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // (shuffled, so that the compiler knows the warp's number, and with it the
-    // roles' branches and the MMA's operands, to be the same for all lanes)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x & 1;  // = the CTA's rank in its cluster
     volatile int *abort = &s.abort_flag;
@@ -762,9 +765,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 const float eo = (m == -INFINITY) ? 0.f : exp2f(m - M);
                 const float den = es + l * eo;
                 factor = den > 0.f ? eo / den : 0.f;
-                lse_out = l > 0.f ? (M + log2f(den)) * kLn2 : __ldg(P.sink + h);  // no candidates: the sink itself
+                lse_out = l != 0.f ? (M + log2f(den)) * kLn2 : __ldg(P.sink + h);  // no candidates: the sink itself
             } else {
-                factor = l > 0.f ? 1.f / l : 0.f;
+                factor = l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
             }
             const bool rope_here = final_out && P.inv_rope && rank == 1;
             float2 cs = make_float2(1.f, 0.f);  // lane i: cos, sin of rope pair i
@@ -840,7 +843,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                         for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
                     }
                     const float sc = amax > 0.f ? amax / 6.f : 1.f;
-                    const float inv = 1.f / sc;
+                    const float up = upscale(amax), inv = 1.f / (sc * up);
+                    auto q = [&](float x) { return x * up * inv; };
 #pragma unroll 1
                     for (int pp = 0; pp < 4; ++pp) {
                         float v[32];
@@ -848,10 +852,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                         uint32_t w[4];
 #pragma unroll
                         for (int q4 = 0; q4 < 4; ++q4)
-                            w[q4] = e2m1x4(v[8 * q4] * inv, v[8 * q4 + 1] * inv, v[8 * q4 + 2] * inv,
-                                           v[8 * q4 + 3] * inv) |
-                                    (e2m1x4(v[8 * q4 + 4] * inv, v[8 * q4 + 5] * inv, v[8 * q4 + 6] * inv,
-                                            v[8 * q4 + 7] * inv) << 16);
+                            w[q4] = e2m1x4(q(v[8 * q4]), q(v[8 * q4 + 1]), q(v[8 * q4 + 2]), q(v[8 * q4 + 3])) |
+                                    (e2m1x4(q(v[8 * q4 + 4]), q(v[8 * q4 + 5]), q(v[8 * q4 + 6]), q(v[8 * q4 + 7]))
+                                     << 16);
                         const int c = 4 * bl + pp;
                         *reinterpret_cast<uint4 *>(frow + ((c ^ (h & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
@@ -905,7 +908,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     if (P.n_split > kCombineBatch)
         for (int sp = 0; sp < P.n_split; ++sp) {
             const float2 ml = ml_row[(size_t)sp * kHeads];
-            if (ml.y > 0.f) M = fmaxf(M, ml.x);
+            if (ml.y != 0.f) M = fmaxf(M, ml.x);
         }
     float den = 0.f;
     float acc[2][8];
@@ -927,11 +930,11 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
         if (P.n_split <= kCombineBatch) {
 #pragma unroll
             for (int q = 0; q < kCombineBatch; ++q)
-                if (ml[q].y > 0.f) M = fmaxf(M, ml[q].x);
+                if (ml[q].y != 0.f) M = fmaxf(M, ml[q].x);
         }
 #pragma unroll
         for (int q = 0; q < kCombineBatch; ++q) {
-            if (!(ml[q].y > 0.f)) continue;
+            if (ml[q].y == 0.f) continue;  // a split without candidates (one with a NaN among them counts)
             const float w = ml[q].y * exp2f(ml[q].x - M);
             den += w;
 #pragma unroll
@@ -943,7 +946,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
             }
         }
     }
-    const bool none = !(den > 0.f);  // no candidates: lse is the sink itself
+    const bool none = den == 0.f;  // no candidates: lse is the sink itself
     den += (sk == -INFINITY) ? 0.f : exp2f(sk - M);
     const float inv = den > 0.f ? 1.f / den : 0.f;
 #pragma unroll
@@ -975,12 +978,13 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         const float sc = amax > 0.f ? amax / 6.f : 1.f;
-        const float isc = 1.f / sc;
+        const float up = upscale(amax), inv_sc = 1.f / (sc * up);
+        auto q = [&](float x) { return x * up * inv_sc; };
         uint32_t w[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            w[e] = e2m1x4(acc[e][0] * isc, acc[e][1] * isc, acc[e][2] * isc, acc[e][3] * isc) |
-                   (e2m1x4(acc[e][4] * isc, acc[e][5] * isc, acc[e][6] * isc, acc[e][7] * isc) << 16);
+            w[e] = e2m1x4(q(acc[e][0]), q(acc[e][1]), q(acc[e][2]), q(acc[e][3])) |
+                   (e2m1x4(q(acc[e][4]), q(acc[e][5]), q(acc[e][6]), q(acc[e][7])) << 16);
         reinterpret_cast<uint2 *>(P.out_fp4 + row * kFp4RowBytes)[lane] = make_uint2(w[0], w[1]);
         if ((lane & 7) == 0) P.out_fp4_scale[row * 4 + (lane >> 3)] = sc;
     } else {
@@ -993,8 +997,8 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
 
 // Splits per query so that about one CTA pair per two SMs is busy.
 // `max_candidates` bounds the candidates of any query (selected + window).
-int choose_splits(int rows, int max_candidates) {
-    const int blocks = (max_candidates + kBlock - 1) / kBlock;
+int choose_splits(int rows, int64_t max_candidates) {
+    const int blocks = (int)((max_candidates + kBlock - 1) / kBlock);
     int n = cached_sm_count() / 2 / (rows > 0 ? rows : 1);
     if (n > blocks) n = blocks;
     return n < 1 ? 1 : n;
@@ -1043,7 +1047,7 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
         }
     }
     const int rows = B * T;
-    P.n_split = choose_splits(rows, k + W);
+    P.n_split = choose_splits(rows, (int64_t)k + W);
     if (P.n_split > 1) {
         const size_t po = ((size_t)rows * P.n_split * kHeads * kDim * sizeof(__nv_bfloat16) + 255) / 256 * 256;
         if (!ws || ws_bytes < po + (size_t)rows * P.n_split * kHeads * sizeof(float2)) return cudaErrorInvalidValue;

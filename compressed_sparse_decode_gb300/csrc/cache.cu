@@ -2,10 +2,10 @@
 // (csa_cache_append, csa_cache_read): FP8 and 4-bit records, contiguous, paged
 // or ring.
 //
-// One warp a token (several, one after the other, in large calls); lane l holds dims [16 l, 16 l + 16): lanes 0..27 the nope
-// dims (one 4-bit scale block each, eight lanes an FP8 block), lanes 28..31
-// the rope dims. So the 4-bit block maximum needs no shuffle, and a record is
-// written with one vector store a lane.
+// One warp a token (several, one after the other, in large calls); lane l holds
+// dims [16 l, 16 l + 16): lanes 0..27 the nope dims (one 4-bit scale block each,
+// eight lanes an FP8 block), lanes 28..31 the rope dims. So the 4-bit block
+// maximum needs no shuffle, and a record is written with one vector store a lane.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"

@@ -254,6 +254,75 @@ def test_fp4_output(cuda_lib):
     assert csd.csa_read_device_error() == 0
 
 
+@pytest.mark.parametrize("sink, largest", [(20.0, -120), (30.0, -134)])
+def test_fp4_output_of_tiny_values(cuda_lib, sink, largest):
+    """Outputs near 2^-134, whose multiplier is a subnormal number: each value
+    within its code's half step (at most one unit, and half a step of 2^-149 a
+    unit for the multiplier's own rounding) of the 64-bit one."""
+    csd = cuda_lib
+    for B, T, cap, n in ((1, 1, 300, 280), (40, 2, 40, 30)):  # with and without splits
+        c = Case(csd, B, T, cap, seed=23)
+        for records in (c.pool, c.ring.view(-1, 384)):
+            records[:, 380] = 20  # units 128 .. 448 times 2^-107: values near 2^-97
+            records[:, 224:352] = 0
+        c.sink = torch.full((128,), sink)  # the candidates' weight is about n e^-sink
+        counts = [[n] * T for _ in range(B)]
+        idx, cnt = c.select(n, counts)
+        (codes, s), _ = c.csa(idx, cnt, fp4_out=True)
+        p, s = codes.cpu().numpy(), s.double().cpu().numpy()
+        code = np.stack([p & 15, p >> 4], -1).reshape(*p.shape[:-1], 512)
+        v = np.where(code >= 8, -1.0, 1.0) * R.E2M1[code & 7] * np.repeat(s, 128, axis=-1)
+        for b, t in ((0, 0), (B - 1, T - 1)):
+            x = np.concatenate([R.fp4_values(c.pool.numpy()[c.where(b, idx[b, t, :n].numpy())]),
+                                R.fp4_values(c.ring[b].numpy()[np.arange(int(c.pos[b, t]) - 127, int(c.pos[b, t]) + 1) % c.R])])
+            o, _, A, _ = attend(c.q[b, t].double().numpy(), c.sink.double().numpy(), x)
+            assert 2.0 ** (largest - 6) < np.abs(o).max() < 2.0 ** (largest + 2)
+            sd = np.repeat(s[b, t], 128, axis=-1)
+            assert np.all(np.abs(v[b, t] - o) <= sd * (1 + BF) + 3 * BF * A + 8 * 2.0 ** -149)
+    assert csd.csa_read_device_error() == 0
+
+
+@pytest.mark.parametrize("B,cap,n", [(2, 900, 700), (90, 40, 30)])  # with and without splits
+def test_a_selected_nan_record_reaches_its_row_only(cuda_lib, B, cap, n):
+    csd = cuda_lib
+    c = Case(csd, B, 1, cap, paged=False, seed=33)
+    idx, cnt = c.select(n, [[n]] * B)
+    good = c.csa(idx, cnt)
+    bad = B // 2
+    c.pool[bad * cap + int(idx[bad, 0, n // 3]), 380] = 255
+    out, lse = c.csa(idx, cnt)
+    assert torch.all(torch.isnan(out[bad, :, :, :448])) and torch.all(torch.isnan(lse[bad]))
+    keep = [b for b in range(B) if b != bad]
+    assert torch.equal(out[keep], good[0][keep]) and torch.equal(lse[keep], good[1][keep])
+    c.pool[bad * cap + int(idx[bad, 0, n // 3]), 380] = 127
+    c.q[0, 0, 5, 9] = math.nan  # a head of the query
+    out, lse = c.csa(idx, cnt)
+    heads = [h for h in range(128) if h != 5]
+    assert torch.all(torch.isnan(out[0, 0, 5])) and torch.isnan(lse[0, 0, 5])
+    assert torch.all(torch.isfinite(out[0, 0, heads].float())) and torch.all(torch.isfinite(lse[0, 0, heads]))
+    assert csd.csa_read_device_error() == 0
+
+
+def test_expired_waits_are_reported_and_the_next_call_is_right(cuda_lib):
+    csd = cuda_lib
+    c = Case(csd, 3, 2, 700, seed=50)
+    counts = [[600, 0], [130, 64], [1, 333]]
+    idx, cnt = c.select(600, counts)
+    first = c.csa(idx, cnt)
+    c.check(first, lambda b, t: idx[b, t, :counts[b][t]].numpy())
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    csd.csa_debug_set_wait_limit_ns(1)
+    try:
+        c.csa(idx, cnt, status=status)
+        seen = csd.csa_read_device_error(status=status)
+    finally:
+        csd.csa_debug_set_wait_limit_ns(0)
+    assert seen == csd.ERR_TIMEOUT
+    again = c.csa(idx, cnt, status=status)
+    assert csd.csa_read_device_error(status=status) == 0
+    assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
 def test_offsets_past_32_bits(cuda_lib):
     csd = cuda_lib
     n = (1 << 32) // 384 + 5000
@@ -291,6 +360,8 @@ def test_results_do_not_depend_on_the_run_or_the_workspace(cuda_lib):
     for s in (a, b):
         with torch.cuda.stream(s):
             outs.append(call())
+    for s in (a, b, a.cuda_stream):  # and named by the call, which makes its outputs and workspace
+        outs.append(call(stream=s))
     torch.cuda.synchronize()
     ws.fill_(255)
     g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()  # two graphs that share a workspace

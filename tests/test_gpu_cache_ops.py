@@ -381,6 +381,30 @@ def test_other_stream_and_graph_replay(cuda_lib):
     assert csd.csa_read_device_error() == 0
 
 
+def test_outputs_made_for_a_named_stream(cuda_lib):
+    """A call given a stream makes its output in that stream's order: the zeros
+    behind a count, and nothing that the current stream still uses."""
+    csd = cuda_lib
+    pool = R.random_fp4_records(64, 3).cuda()
+    cache = csd.cache_desc(pool, 64, seq_stride=64, fmt=csd.FORMAT_FP4)
+    first = torch.tensor([0], dtype=torch.int32, device="cuda")
+    count = torch.tensor([40], dtype=torch.int32, device="cuda")
+    want = csd.csa_cache_read(cache, first, count, 64)
+    x = torch.randn((1, 64, 4, 512), device="cuda")
+    pos = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+    want2, want3 = csd.csa_head_norm_rope(x, pos), csd.csa_head_norm_rope_e4m3(x, pos)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for s in (side, side.cuda_stream):
+        torch.full((64 << 20,), 7, device="cuda")  # freed at once, still being written
+        got = csd.csa_cache_read(cache, first, count, 64, stream=s)
+        got2, got3 = csd.csa_head_norm_rope(x, pos, stream=s), csd.csa_head_norm_rope_e4m3(x, pos, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.all(got[0, 40:] == 0) and torch.equal(got2, want2)
+        assert torch.equal(got3[0], want3[0]) and torch.equal(got3[1], want3[1])
+    assert csd.csa_read_device_error() == 0
+
+
 def test_descriptions_that_do_not_fit_the_call_are_refused(cuda_lib):
     csd = cuda_lib
     pool = torch.zeros((4, 2, 384), dtype=torch.uint8, device="cuda")
@@ -394,6 +418,8 @@ def test_descriptions_that_do_not_fit_the_call_are_refused(cuda_lib):
     copy = csd.cache_desc(pool.transpose(0, 1), 4, seq_stride=4, fmt=csd.FORMAT_FP4)
     with pytest.raises(ValueError, match="not contiguous"):
         csd.csa_cache_append(copy, x[:1], first[:1])
+    with pytest.raises(ValueError, match="go together"):
+        csd.csa_cache_append(two, x[:2], first[:2], key=x[:2, :, :128])
     with pytest.raises(ValueError, match="status"):
         csd.csa_cache_append(two, x[:2], first[:2], status=torch.zeros(1, device="cuda"))
     assert csd.csa_read_device_error() == 0
