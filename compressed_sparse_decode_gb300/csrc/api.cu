@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <atomic>
 #include <cstring>
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -28,6 +29,7 @@ cudaError_t launch_attention_fp4(const void *, const float *, float, const csa_c
                                  const int32_t *, const int32_t *, const int32_t *, int, const int32_t *, int, int,
                                  int, bool, void *, float *, const csa_attention_epilogue *, void *, size_t, int *,
                                  cudaStream_t);
+size_t attention_fp4_workspace_bytes(int B, int T, int max_selected, int W);
 }  // namespace csa
 
 namespace csa {
@@ -174,18 +176,26 @@ const char *csa_status_string(csa_status_t s) {
     return "unknown status";
 }
 
+namespace {
+// Attention workspace that serves both record formats and every window.
+size_t either_format_bytes(int B, int T, int max_selected) {
+    return std::max(attention_workspace_bytes(B, T, max_selected, CSA_MAX_SWA_WINDOW),
+                    attention_fp4_workspace_bytes(B, T, max_selected, CSA_MAX_SWA_WINDOW));
+}
+}  // namespace
+
 size_t csa_workspace_bytes(csa_op_t op, int B, int T, int Ncap, int k) {
     if (B < 1 || T < 1 || Ncap < 1) return 0;
     switch (op) {
     case CSA_OP_INDEXER: return 0;
     case CSA_OP_TOPK: return topk_workspace_bytes(B, T, Ncap, k);
-    case CSA_OP_ATTENTION: return attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW);
-    case CSA_OP_HCA_ATTENTION: return attention_workspace_bytes(B, T, Ncap, CSA_MAX_SWA_WINDOW);
+    case CSA_OP_ATTENTION: return either_format_bytes(B, T, k);
+    case CSA_OP_HCA_ATTENTION: return either_format_bytes(B, T, Ncap);
     case CSA_OP_DECODE_STEP:
         return align_up(sizeof(float) * (size_t)B * T * Ncap, kWsAlign) +
                2 * align_up(sizeof(int32_t) * (size_t)B * T * k, kWsAlign) +
                align_up(topk_workspace_bytes(B, T, Ncap, k), kWsAlign) +
-               align_up(attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW), kWsAlign);
+               align_up(either_format_bytes(B, T, k), kWsAlign);
     }
     return 0;
 }
@@ -248,11 +258,16 @@ const void *checked_out(const csa_attention_epilogue *epi, const void *out) {
 }  // namespace
 
 namespace {
-// The attention entry points' bodies; `launch` is the launcher of the cache's
-// record format (same arguments, checks and workspace for both).
-using AttentionLaunch = decltype(&launch_attention);
+// The attention entry points' bodies; `kernel` is that of the cache's record
+// format (same arguments and checks for both).
+struct AttentionKernel {
+    decltype(&launch_attention) launch;
+    decltype(&attention_workspace_bytes) workspace_bytes;
+};
+constexpr AttentionKernel kFp8Attention = {launch_attention, attention_workspace_bytes};
+constexpr AttentionKernel kFp4Attention = {launch_attention_fp4, attention_fp4_workspace_bytes};
 
-csa_status_t sink_attention(AttentionLaunch launch, const void *q, const float *sink, float softmax_scale,
+csa_status_t sink_attention(const AttentionKernel &kernel, const void *q, const float *sink, float softmax_scale,
                             const csa_cache_desc &comp, const void *swa_ring, int R, int W, const int32_t *topk_idx,
                             const int32_t *topk_cnt, const int32_t *q_pos, int B, int T, int k, void *out, float *lse,
                             const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
@@ -262,14 +277,14 @@ csa_status_t sink_attention(AttentionLaunch launch, const void *q, const float *
     a = attention_arg_status(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B, T, k,
                              checked_out(epilogue, out), lse, status);
     if (a != CSA_OK) return a;
-    const size_t need = attention_workspace_bytes(B, T, k, W);
+    const size_t need = kernel.workspace_bytes(B, T, k, W);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
         return CSA_ERR_WORKSPACE;
-    return cuda_status(launch(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, nullptr, 1, q_pos, B,
+    return cuda_status(kernel.launch(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, nullptr, 1, q_pos, B,
                               T, k, false, out, lse, epilogue, workspace, workspace_bytes, status, stream));
 }
 
-csa_status_t hca_attention(AttentionLaunch launch, const void *q, const float *sink, float softmax_scale,
+csa_status_t hca_attention(const AttentionKernel &kernel, const void *q, const float *sink, float softmax_scale,
                            const csa_cache_desc &comp, const int32_t *n_comp, const void *swa_ring, int R, int W,
                            const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
                            const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
@@ -281,10 +296,10 @@ csa_status_t hca_attention(AttentionLaunch launch, const void *q, const float *s
         return CSA_ERR_INVALID_ARG;
     if (!valid_dims(B, T) || W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || m_hca < 1 || !(softmax_scale > 0.f))
         return CSA_ERR_INVALID_ARG;
-    const size_t need = attention_workspace_bytes(B, T, comp.seq_capacity, W);
+    const size_t need = kernel.workspace_bytes(B, T, comp.seq_capacity, W);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
         return CSA_ERR_WORKSPACE;
-    return cuda_status(launch(q, sink, softmax_scale, comp, swa_ring, R, W, nullptr, nullptr, n_comp, m_hca, q_pos, B, T,
+    return cuda_status(kernel.launch(q, sink, softmax_scale, comp, swa_ring, R, W, nullptr, nullptr, n_comp, m_hca, q_pos, B, T,
                               comp.seq_capacity, true, out, lse, epilogue, workspace, workspace_bytes, status,
                               stream));
 }
@@ -296,7 +311,7 @@ csa_status_t csa_sink_attention_decode_ex(const void *q, const float *sink, floa
                                           void *out, float *lse, const csa_attention_epilogue *epilogue,
                                           void *workspace, size_t workspace_bytes, int32_t *status,
                                           cudaStream_t stream) {
-    return sink_attention(launch_attention, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B,
+    return sink_attention(kFp8Attention, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B,
                           T, k, out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
@@ -306,7 +321,7 @@ csa_status_t csa_sink_attention_decode_fp4(const void *q, const float *sink, flo
                                            void *out, float *lse, const csa_attention_epilogue *epilogue,
                                            void *workspace, size_t workspace_bytes, int32_t *status,
                                            cudaStream_t stream) {
-    return sink_attention(launch_attention_fp4, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt,
+    return sink_attention(kFp4Attention, q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt,
                           q_pos, B, T, k, out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
@@ -324,7 +339,7 @@ csa_status_t hca_sink_attention_decode_ex(const void *q, const float *sink, floa
                                           const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
                                           const csa_attention_epilogue *epilogue, void *workspace,
                                           size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
-    return hca_attention(launch_attention, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T, m_hca,
+    return hca_attention(kFp8Attention, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T, m_hca,
                          out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
@@ -333,7 +348,7 @@ csa_status_t hca_sink_attention_decode_fp4(const void *q, const float *sink, flo
                                            const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
                                            const csa_attention_epilogue *epilogue, void *workspace,
                                            size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
-    return hca_attention(launch_attention_fp4, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T,
+    return hca_attention(kFp4Attention, q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T,
                          m_hca, out, lse, epilogue, workspace, workspace_bytes, status, stream);
 }
 
@@ -347,7 +362,7 @@ csa_status_t hca_sink_attention_decode(const void *q, const float *sink, float s
 }
 
 namespace {
-csa_status_t decode_step(AttentionLaunch launch, const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
                          const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
                          float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R, int W,
                          const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
@@ -371,13 +386,13 @@ csa_status_t decode_step(AttentionLaunch launch, const uint8_t *q_idx, const flo
     const size_t tk_bytes = align_up(topk_workspace_bytes(B, T, Ncap, k), kWsAlign);
     void *tk_ws = tk_bytes ? ws : nullptr;
     ws += tk_bytes;
-    const size_t at_bytes = align_up(attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW), kWsAlign);
+    const size_t at_bytes = align_up(either_format_bytes(B, T, k), kWsAlign);
     csa_status_t s = csa_indexer_logits(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q_pos, n_comp, B, T, Ncap, m,
                                         logits, status, stream);
     if (s != CSA_OK) return s;
     s = csa_topk(logits, q_pos, n_comp, B, T, Ncap, m, k, idx, cnt, tk_ws, tk_bytes, status, stream);
     if (s != CSA_OK) return s;
-    return sink_attention(launch, q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out, lse,
+    return sink_attention(kernel, q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out, lse,
                           epilogue, at_bytes ? ws : nullptr, at_bytes, status, stream);
 }
 }  // namespace
@@ -389,7 +404,7 @@ csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, 
                                 void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                 const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                 int32_t *status, cudaStream_t stream) {
-    return decode_step(launch_attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+    return decode_step(kFp8Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                        swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
                        workspace, workspace_bytes, status, stream);
 }
@@ -401,7 +416,7 @@ csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale,
                                  void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                  const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                  int32_t *status, cudaStream_t stream) {
-    return decode_step(launch_attention_fp4, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+    return decode_step(kFp4Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                        swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
                        workspace, workspace_bytes, status, stream);
 }

@@ -108,7 +108,8 @@ struct Params {
     int m_hca, hca, T, k, n_split;
     __nv_bfloat16 *out;
     float *lse;
-    __nv_bfloat16 *part_o;  // [rows, n_split, 128, 512] BF16 (n_split > 1)
+    __half *part_o;         // [rows, n_split, 128, 512] FP16 (n_split > 1), each 32 dims to a power of two:
+    uint8_t *part_ex;       // [rows, n_split, 128, 16] their exponents (see part_unit)
     float2 *part_ml;        // [rows, n_split, 128] (max, sum) in log2 units
     uint8_t *out_fp4;       // null: BF16 output
     float *out_fp4_scale;
@@ -149,6 +150,15 @@ __device__ __forceinline__ Unit make_unit(const Params &P) {
 // A factor for values of this magnitude so that the reciprocal of their E2M1
 // multiplier stays in range.
 __device__ __forceinline__ float upscale(float amax) { return amax < 7.9e-31f ? 1.2676506002282294e30f : 1.f; }
+
+// A split's output is kept as FP16 with a power of two for every 32 dims, their
+// amax's exponent field ex: value = half * part_unit(ex), the halves below 2^15. So
+// the detour costs 2^-12 of a value (BF16 made it 2^-9, half of the whole call's
+// error) at any magnitude, and fp32 would double the bytes. (From ex = 32 up, so
+// that the unit is a normal number: the halves then end 2^-133, as BF16 does.)
+__device__ __forceinline__ uint32_t part_exponent(float amax) { return max(__float_as_uint(amax) >> 23, 32u); }
+__device__ __forceinline__ float part_unit(uint32_t ex) { return __uint_as_float((ex - 14u) << 23); }
+__device__ __forceinline__ float part_factor(uint32_t ex) { return __uint_as_float((268u - ex) << 23); }
 
 // 16-byte chunk cc of row `row` of a swizzled block of 128-byte rows.
 __device__ __forceinline__ uint4 *sw128(uint8_t *block, int row, int cc) {
@@ -802,23 +812,42 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             uint8_t *ostage = &s.x[0][0];
             if (!(final_out && P.out_fp4)) {
                 uint8_t *srow = ostage + h * (kHalf * 2);
+                const size_t part = ((size_t)r * P.n_split + u.split) * kHeads;
+                uint32_t exponents = 0;
 #pragma unroll 1
                 for (int piece = half * kPieces; piece < half * kPieces + kPieces; ++piece) {
                     float v[32];
                     piece_values(piece, v);
+                    uint32_t w[16];
+                    if (final_out) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+                    } else {
+                        float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) a[e & 3] = fmaxf(a[e & 3], fabsf(v[e]));
+                        const uint32_t ex = part_exponent(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])));
+                        const float f = part_factor(ex);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const __half2 p = __floats2half2_rn(v[2 * e] * f, v[2 * e + 1] * f);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&p);
+                        }
+                        exponents = exponents >> 8 | ex << 24;
+                    }
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) {
                         const int c = piece * 4 + q4;
                         *reinterpret_cast<uint4 *>(srow + ((c ^ (h & 7)) << 4)) =
-                            make_uint4(pack_bf16(v[8 * q4 + 0], v[8 * q4 + 1]), pack_bf16(v[8 * q4 + 2], v[8 * q4 + 3]),
-                                       pack_bf16(v[8 * q4 + 4], v[8 * q4 + 5]), pack_bf16(v[8 * q4 + 6], v[8 * q4 + 7]));
+                            make_uint4(w[4 * q4], w[4 * q4 + 1], w[4 * q4 + 2], w[4 * q4 + 3]);
                     }
                 }
+                static_assert(kPieces == 4, "a thread's exponents are one word");
+                if (!final_out) reinterpret_cast<uint32_t *>(P.part_ex)[(part + h) * 4 + rank * 2 + half] = exponents;
                 const bool staged = rows_staged();
                 const uint64_t policy = ptx::l2_policy_evict_first();
-                __nv_bfloat16 *dst0 = final_out
-                                          ? P.out + (size_t)r * kHeads * kDim + rank * kHalf
-                                          : P.part_o + ((size_t)r * P.n_split + u.split) * kHeads * kDim + rank * kHalf;
+                uint16_t *dst0 = (final_out ? reinterpret_cast<uint16_t *>(P.out) + (size_t)r * kHeads * kDim
+                                            : reinterpret_cast<uint16_t *>(P.part_o) + part * kDim) + rank * kHalf;
 #pragma unroll 4
                 for (int i = 0; i < 16 && staged; ++i) {
                     const int hr = quarter * 32 + 16 * half + i;  // a head row of this warp pair
@@ -902,6 +931,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     const float sk = __ldg(P.sink + h) * kLog2e;
     const float2 *ml_row = P.part_ml + (size_t)r * P.n_split * kHeads + h;
     const uint4 *o_row = reinterpret_cast<const uint4 *>(P.part_o + ((size_t)r * P.n_split * kHeads + h) * kDim) + lane * 2;
+    const uint8_t *ex_row = P.part_ex + ((size_t)r * P.n_split * kHeads + h) * 16 + (lane >> 1);
     const size_t split_stride = (size_t)kHeads * kDim / 8;  // uint4 per split
     const uint64_t policy = ptx::l2_policy_evict_first();
     float M = sk;
@@ -916,12 +946,15 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
     for (int s0 = 0; s0 < P.n_split; s0 += kCombineBatch) {
         float2 ml[kCombineBatch];
-        Octet<CSA_BF16> v[kCombineBatch][2];
+        Octet<CSA_FP16> v[kCombineBatch][2];
+        uint32_t ex[kCombineBatch];
 #pragma unroll
         for (int q = 0; q < kCombineBatch; ++q) {
             const int sp = s0 + q;
             ml[q] = make_float2(0.f, 0.f);
+            ex[q] = 0;
             if (sp < P.n_split) {
+                ex[q] = ex_row[(size_t)sp * kHeads * 16];
                 ml[q] = ml_row[(size_t)sp * kHeads];
                 v[q][0].v = ptx::ldg_v4_policy(o_row + sp * split_stride, policy);
                 v[q][1].v = ptx::ldg_v4_policy(o_row + sp * split_stride + 1, policy);
@@ -937,12 +970,13 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
             if (ml[q].y == 0.f) continue;  // a split without candidates (one with a NaN among them counts)
             const float w = ml[q].y * exp2f(ml[q].x - M);
             den += w;
+            const float wu = w * part_unit(ex[q]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float f[8];
                 v[q][e].floats(f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[e][i] = fmaf(w, f[i], acc[e][i]);
+                for (int i = 0; i < 8; ++i) acc[e][i] = fmaf(wu, f[i], acc[e][i]);
             }
         }
     }
@@ -1006,10 +1040,14 @@ int choose_splits(int rows, int64_t max_candidates) {
 
 }  // namespace
 
+size_t attention_fp4_workspace_bytes(int B, int T, int max_selected, int W) {
+    const int n = choose_splits(B * T, (int64_t)max_selected + W);
+    const size_t parts = (size_t)B * T * n * kHeads;
+    return n == 1 ? 0 : parts * (kDim * sizeof(__half) + 16 + sizeof(float2));
+}
+
 // `k` = the top-k row length (CSA) or the per-sequence capacity (HCA). The
-// workspace holds the splits' BF16 partials and their (max, sum); the splits
-// are at most those that attention_workspace_bytes counts (chunks of 64
-// candidates there, blocks of 128 here).
+// workspace holds the splits' partials, their exponents and their (max, sum).
 cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, const csa_cache_desc &comp,
                                  const void *ring, int R, int W, const int32_t *topk_idx, const int32_t *topk_cnt,
                                  const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
@@ -1049,10 +1087,11 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
     const int rows = B * T;
     P.n_split = choose_splits(rows, (int64_t)k + W);
     if (P.n_split > 1) {
-        const size_t po = ((size_t)rows * P.n_split * kHeads * kDim * sizeof(__nv_bfloat16) + 255) / 256 * 256;
-        if (!ws || ws_bytes < po + (size_t)rows * P.n_split * kHeads * sizeof(float2)) return cudaErrorInvalidValue;
-        P.part_o = static_cast<__nv_bfloat16 *>(ws);
-        P.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(ws) + po);
+        if (!ws || ws_bytes < attention_fp4_workspace_bytes(B, T, k, W)) return cudaErrorInvalidValue;
+        const size_t parts = (size_t)rows * P.n_split * kHeads;
+        P.part_o = static_cast<__half *>(ws);
+        P.part_ex = static_cast<uint8_t *>(ws) + parts * kDim * sizeof(__half);
+        P.part_ml = reinterpret_cast<float2 *>(P.part_ex + parts * 16);
     }
     constexpr size_t smem = sizeof(AttSmem) + 1024;
     cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel), (int)smem);

@@ -5,10 +5,15 @@ sum_j p_j |x_jd| / den the weighted magnitude of what is summed:
 * the latents are exact in BF16; each score moves by at most B = 2^-15 scale
   max_j sum_d |q_d x_jd| (fp32 accumulation of 512 exact products, with a wide
   margin for the tensor core's alignment), so each weight by e^{2B} - 1;
-* the weights are rounded to BF16 (2^-8 of each) and so are the partial outputs
-  of a split (2^-8 of each, at most A_d together) and the output (2^-8 |o_d|);
+* the weights are rounded to BF16 (2^-8 of each) and the output too (2^-8 |o_d|);
+* the partial outputs of a split are rounded to FP16 (2^-11 of each, at most A_d
+  together) in units u of a power of two for each 32 dims, whose largest value is
+  at least 2^14 u; FP16's smallest step is 2^-24, so a value far below the largest
+  of its 32 moves by up to 2^-25 u <= 2^-39 of that largest, which is at most the
+  32 dims' largest share of A (summed over the splits: 2^-39 G_d, G_d = max A
+  over the 32 dims);
 * fp32 exponentials and sums: below 1e-5.
-So |err_d| <= A_d (2 2^-8 + 3 B + 1e-5) + 2^-8 |o_d|, for rotated dims with A
+So |err_d| <= A_d (2 2^-8 + 3 B + 1e-5) + 2^-39 G_d + 2^-8 |o_d|, for rotated dims with A
 and |o| summed over the pair (+ 1e-6 of them for sine and cosine), and
 |lse err| <= B + 1e-5 (1 + |lse|).
 """
@@ -91,7 +96,8 @@ class Case:
                 x = np.concatenate([R.fp4_values(self.pool.numpy()[self.where(b, entries(b, t))].reshape(-1, 384)),
                                     R.fp4_values(self.ring[b].numpy()[win])])
                 ref, ref_lse, A, Bz = attend(self.q[b, t].double().numpy(), self.sink.double().numpy(), x)
-                o, bound = ref, A * (2 * BF + 3 * Bz[:, None] + 1e-5) + BF * np.abs(ref)
+                G = np.repeat(A.reshape(128, 16, 32).max(-1), 32, axis=-1)
+                o, bound = ref, A * (2 * BF + 3 * Bz[:, None] + 1e-5) + 2.0 ** -39 * G + BF * np.abs(ref)
                 if theta:
                     o = turn_back(ref, p, theta)
                     s = bound[:, 448::2] + bound[:, 449::2] + 1e-6 * (A[:, 448::2] + A[:, 449::2])
