@@ -14,7 +14,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kNopeLanes = kNope / 16;  // 28
 constexpr uint32_t kAll = 0xffffffffu;
@@ -60,12 +60,14 @@ __device__ __forceinline__ Slot find_slots(const Span &s, int t0, int n, int lan
     if (lane < n && token < s.B * s.T) o = find_slot(s, token / s.T, token % s.T, err);
     return o;
 }
-// Tokens a warp: as many as leave every SM four blocks, up to 8. (They share the
-// look-up, the norm's weights and the rotation's table, and the next one's loads
-// run under the current one: 49k tokens into FP8 with keys took 50 us with one.)
-int tokens_per_warp(int tokens) {
-    const int n = tokens / (cached_sm_count() * 4 * kWarps);
-    return n < 1 ? 1 : n > 8 ? 8 : n;
+// Tokens a warp: as many as leave every SM eight blocks, up to `most`. (A warp's
+// tokens share the look-up, the norm's weights and the rotation's table, and the
+// next one's loads run under the current one. Reading has less to share: 49k FP8
+// records took 19.5 us with one, 17.9 with two, 18.3 with four, 19.0 with eight.)
+constexpr int kAppendTokens = 8, kReadTokens = 2;
+int tokens_per_warp(int tokens, int most) {
+    const int n = tokens / (cached_sm_count() * 8 * kWarps);
+    return n < 1 ? 1 : n > most ? most : n;
 }
 
 struct AppendParams {
@@ -110,8 +112,10 @@ __device__ __forceinline__ int fp4_exponent(uint32_t amax) {
     return amax ? max(e, kFp4MinExponent) : 0;
 }
 
+// (Six blocks an SM: 80 registers. With blocks of twice the size, two an SM, an
+// FP8 prompt of 49k tokens with keys took 36 us instead of 31.)
 template <int DT, int FMT, bool KEYS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 5 : 6)
 append_kernel(const __grid_constant__ AppendParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -409,7 +413,7 @@ extern "C" CSA_API csa_status_t csa_cache_append(csa_cache_desc cache, csa_forma
     P.pos_stride = pos_stride;
     P.base = static_cast<uint8_t *>(const_cast<void *>(cache.base));
     P.err = status;
-    P.per_warp = tokens_per_warp(B * T);
+    P.per_warp = tokens_per_warp(B * T, kAppendTokens);
     PdlLaunch l(dim3((B * T + kWarps * P.per_warp - 1) / (kWarps * P.per_warp)), dim3(kThreads), stream);
     count_launch();
     const cudaError_t e = x_dtype == CSA_BF16   ? launch_append<CSA_BF16>(P, fmt, l)
@@ -428,7 +432,7 @@ extern "C" CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_
     if (!out || misaligned(out)) return CSA_ERR_INVALID_ARG;
     P.out = static_cast<uint4 *>(out);
     P.err = status;
-    P.per_warp = tokens_per_warp(B * T);
+    P.per_warp = tokens_per_warp(B * T, kReadTokens);
     PdlLaunch l(dim3((B * T + kWarps * P.per_warp - 1) / (kWarps * P.per_warp)), dim3(kThreads), stream);
     count_launch();
     const cudaError_t e = fmt == CSA_FORMAT_FP4 ? cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP4>, P)

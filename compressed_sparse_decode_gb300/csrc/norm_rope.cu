@@ -11,7 +11,7 @@ namespace csa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct NormRopeParams {
     const void *x;
@@ -31,7 +31,7 @@ struct NormRopeParams {
 // (each head for itself took 120 of 390 instructions), the norm's weights stay in
 // registers.
 template <int DT, int G, int NV, bool E4M3>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 4 : 8)
 norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     extern __shared__ float2 turns[];  // [tokens of the block][rope pairs]
     ptx::griddep_wait();
@@ -151,12 +151,12 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     }
 }
 
-// Heads a group: as many as leave every SM eight blocks, up to 8.
+// Heads a group: as many as leave every SM eight blocks, up to 16.
 template <int DT, int G, int NV, bool E4M3>
 cudaError_t launch_rows(NormRopeParams &P, cudaStream_t stream) {
     constexpr int kGroups = kThreads / G;
     const int n = P.rows / (kGroups * 8 * cached_sm_count());
-    P.per_group = n < 1 ? 1 : n > 8 ? 8 : n;
+    P.per_group = n < 1 ? 1 : n > 16 ? 16 : n;
     // the rotation of the block's tokens (at most this many) has 48 KB
     auto turn_bytes = [&]() {
         return (size_t)((kGroups * P.per_group - 1) / P.H + 2) * (P.ops.rope_dim / 2) * sizeof(float2);

@@ -100,6 +100,7 @@ struct Octet;
 template <>
 struct Octet<CSA_BF16> {
     uint4 v;
+    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const void *base, int64_t at) {
         v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
     }
@@ -116,6 +117,7 @@ struct Octet<CSA_BF16> {
 template <>
 struct Octet<CSA_FP16> {
     uint4 v;
+    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const void *base, int64_t at) {
         v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
     }
@@ -133,6 +135,7 @@ struct Octet<CSA_FP16> {
 template <>
 struct Octet<CSA_FP32> {
     uint4 v, u;
+    __device__ __forceinline__ void clear() { v = u = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const void *base, int64_t at) {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
         v = p[0];
