@@ -918,59 +918,79 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 // Folds the per-split normalised partials and the sink (log2 domain):
 //   M = max(sink, m_s), den = e^{sink-M} + sum_s l_s e^{m_s-M},
 //   out = sum_s l_s e^{m_s-M} o_s / den, lse = M + ln den.
-// One warp per (row, head), 16 dims per lane; up to 8 splits' rows in flight.
-constexpr int kCombineBatch = 8;
-__global__ void __launch_bounds__(256)
+// kWarps warps per (row, head), each every kWarps'th split, 16 dims per lane; the
+// splits' weights are computed once, a split a lane. It is a chain of loads from L2
+// (four splits' at once), so many splits are spread over eight warps, whose sums
+// are added in their order: 9, 18 and 76 splits of one query took 16.1, 16.2 and
+// 18.8 us a call, and with one warp 16.9, 18.2 and 28.7; two splits of 32 queries
+// took 46 us with one warp, with eight 68.
+constexpr int kCombineBatch = 4;
+constexpr int kMaxSplits = 96;
+template <int kWarps>
+__global__ void __launch_bounds__(256, 3)
 combine_fp4_kernel(const __grid_constant__ Params P) {
+    static_assert(kWarps == 1 || kWarps == 8, "one head a warp, or one a block");
+    __shared__ float4 sums[kWarps > 1 ? kWarps : 1][kWarps > 1 ? kDim / 4 : 1];
     ptx::griddep_wait();
     const int r = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float2 cs = make_float2(1.f, 0.f);  // lane i: cos, sin of rope pair i
-    if (P.inv_rope) cs = turn_cos_sin(__ldg(P.q_pos + r), P.turn[lane]);
-    const int h = blockIdx.x * 8 + warp;
-    const float sk = __ldg(P.sink + h) * kLog2e;
-    const float2 *ml_row = P.part_ml + (size_t)r * P.n_split * kHeads + h;
-    const uint4 *o_row = reinterpret_cast<const uint4 *>(P.part_o + ((size_t)r * P.n_split * kHeads + h) * kDim) + lane * 2;
-    const uint8_t *ex_row = P.part_ex + ((size_t)r * P.n_split * kHeads + h) * 16 + (lane >> 1);
-    const size_t split_stride = (size_t)kHeads * kDim / 8;  // uint4 per split
+    const int h = blockIdx.x * (8 / kWarps) + warp / kWarps, part = warp % kWarps;
+    const size_t row0 = (size_t)r * P.n_split * kHeads + h, row_stride = kHeads;  // of the splits' rows
     const uint64_t policy = ptx::l2_policy_evict_first();
-    float M = sk;
-    if (P.n_split > kCombineBatch)
-        for (int sp = 0; sp < P.n_split; ++sp) {
-            const float2 ml = ml_row[(size_t)sp * kHeads];
-            if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    const float sk = __ldg(P.sink + h) * kLog2e;
+    // four splits' rows (all splits have written theirs)
+    uint32_t ex[kCombineBatch];
+    Octet<CSA_FP16> v[kCombineBatch][2];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int q = 0; q < kCombineBatch; ++q) {
+            const int s = s0 + q * kWarps;
+            ex[q] = 32;
+            v[q][0].clear();
+            v[q][1].clear();
+            if (s >= P.n_split) continue;
+            const size_t at = row0 + s * row_stride;
+            const uint4 *o = reinterpret_cast<const uint4 *>(P.part_o + at * kDim) + lane * 2;
+            ex[q] = P.part_ex[at * 16 + (lane >> 1)];
+            v[q][0].v = ptx::ldg_v4_policy(o, policy);
+            v[q][1].v = ptx::ldg_v4_policy(o + 1, policy);
         }
-    float den = 0.f;
+    };
+    float2 ml[kMaxSplits / 32];
+#pragma unroll
+    for (int j = 0; j < kMaxSplits / 32; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+        if (32 * j + lane < P.n_split) ml[j] = P.part_ml[row0 + (32 * j + lane) * row_stride];
+    }
+    load(part);  // (while the weights are computed)
+    float w[kMaxSplits / 32], M = sk, den = 0.f;
+    // (a split without candidates has the sum 0; one with a NaN among them counts)
+#pragma unroll
+    for (int j = 0; j < kMaxSplits / 32; ++j)
+        if (ml[j].y != 0.f) M = fmaxf(M, ml[j].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int j = 0; j < kMaxSplits / 32; ++j) {
+        w[j] = ml[j].y != 0.f ? ml[j].y * exp2f(ml[j].x - M) : 0.f;
+        den += w[j];
+    }
     float acc[2][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[0][e] = acc[1][e] = 0.f;
-    for (int s0 = 0; s0 < P.n_split; s0 += kCombineBatch) {
-        float2 ml[kCombineBatch];
-        Octet<CSA_FP16> v[kCombineBatch][2];
-        uint32_t ex[kCombineBatch];
+#pragma unroll 1
+    for (int s0 = part;;) {
 #pragma unroll
         for (int q = 0; q < kCombineBatch; ++q) {
-            const int sp = s0 + q;
-            ml[q] = make_float2(0.f, 0.f);
-            ex[q] = 0;
-            if (sp < P.n_split) {
-                ex[q] = ex_row[(size_t)sp * kHeads * 16];
-                ml[q] = ml_row[(size_t)sp * kHeads];
-                v[q][0].v = ptx::ldg_v4_policy(o_row + sp * split_stride, policy);
-                v[q][1].v = ptx::ldg_v4_policy(o_row + sp * split_stride + 1, policy);
+            const int s = s0 + q * kWarps;
+            float ws = 0.f;
+#pragma unroll
+            for (int j = 0; j < kMaxSplits / 32; ++j) {
+                const float x = __shfl_sync(0xffffffffu, w[j], s & 31);
+                if (s >> 5 == j) ws = x;
             }
-        }
-        if (P.n_split <= kCombineBatch) {
-#pragma unroll
-            for (int q = 0; q < kCombineBatch; ++q)
-                if (ml[q].y != 0.f) M = fmaxf(M, ml[q].x);
-        }
-#pragma unroll
-        for (int q = 0; q < kCombineBatch; ++q) {
-            if (ml[q].y == 0.f) continue;  // a split without candidates (one with a NaN among them counts)
-            const float w = ml[q].y * exp2f(ml[q].x - M);
-            den += w;
-            const float wu = w * part_unit(ex[q]);
+            if (ws == 0.f) continue;  // (a split that counts for nothing, whatever its row holds)
+            const float wu = ws * part_unit(ex[q]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float f[8];
@@ -979,10 +999,34 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
                 for (int i = 0; i < 8; ++i) acc[e][i] = fmaf(wu, f[i], acc[e][i]);
             }
         }
+        s0 += kCombineBatch * kWarps;
+        if (s0 >= P.n_split) break;
+        load(s0);
     }
+    if (kWarps > 1) {
+        float4 *mine = &sums[part][lane * 4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            mine[i] = make_float4(acc[i >> 1][4 * (i & 1)], acc[i >> 1][4 * (i & 1) + 1], acc[i >> 1][4 * (i & 1) + 2],
+                                  acc[i >> 1][4 * (i & 1) + 3]);
+        __syncthreads();
+        if (part != 0) return;
+#pragma unroll
+        for (int p = 1; p < kWarps; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 a = sums[p][lane * 4 + i];
+                float *to = &acc[i >> 1][4 * (i & 1)];
+                to[0] += a.x, to[1] += a.y, to[2] += a.z, to[3] += a.w;
+            }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     const bool none = den == 0.f;  // no candidates: lse is the sink itself
     den += (sk == -INFINITY) ? 0.f : exp2f(sk - M);
     const float inv = den > 0.f ? 1.f / den : 0.f;
+    float2 cs = make_float2(1.f, 0.f);  // lane i: cos, sin of rope pair i
+    if (P.inv_rope) cs = turn_cos_sin(__ldg(P.q_pos + r), P.turn[lane]);
 #pragma unroll
     for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -1035,6 +1079,7 @@ int choose_splits(int rows, int64_t max_candidates) {
     const int blocks = (int)((max_candidates + kBlock - 1) / kBlock);
     int n = cached_sm_count() / 2 / (rows > 0 ? rows : 1);
     if (n > blocks) n = blocks;
+    if (n > kMaxSplits) n = kMaxSplits;
     return n < 1 ? 1 : n;
 }
 
@@ -1102,9 +1147,10 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
     e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel, P);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || P.n_split == 1) return e;
-    PdlLaunch c(dim3(kHeads / 8, rows), dim3(256), stream);
+    const bool spread = P.n_split > kCombineBatch;  // eight warps a head instead of one
+    PdlLaunch c(dim3(spread ? kHeads : kHeads / 8, rows), dim3(256), stream);
     count_launch();
-    e = cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel, P);
+    e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8>, P) : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1>, P);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
