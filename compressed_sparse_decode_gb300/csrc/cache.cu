@@ -114,7 +114,7 @@ __device__ __forceinline__ int fp4_exponent(uint32_t amax) {
 
 // (Six blocks an SM: 80 registers. With blocks of twice the size, two an SM, an
 // FP8 prompt of 49k tokens with keys took 36 us instead of 31.)
-template <int DT, int FMT, bool KEYS>
+template <int DT, int FMT, bool KEYS, bool NORM>
 __global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 5 : 6)
 append_kernel(const __grid_constant__ AppendParams P) {
     ptx::griddep_wait();
@@ -128,8 +128,8 @@ append_kernel(const __grid_constant__ AppendParams P) {
     float2 *pair_cs = warp_cs[threadIdx.x >> 5];
     const uint64_t pair_turn = turn ? P.ops.turn[lane] : 0;
     float w[2][8];  // the norm's weights of this lane's dims
-    load_weights(w[0], P.ops.norm ? P.ops.weight : nullptr, 16 * lane);
-    load_weights(w[1], P.ops.norm ? P.ops.weight : nullptr, 16 * lane + 8);
+    load_weights(w[0], NORM ? P.ops.weight : nullptr, 16 * lane);
+    load_weights(w[1], NORM ? P.ops.weight : nullptr, 16 * lane + 8);
     struct {
         Octet<DT> x[2], key;
         int64_t record;
@@ -164,7 +164,7 @@ append_kernel(const __grid_constant__ AppendParams P) {
         float f[2][8];
         now.x[0].floats(f[0]);
         now.x[1].floats(f[1]);
-        if (P.ops.norm) {
+        if (NORM) {
             float2 two = make_float2(0.f, 0.f);
             square_octet(f[0], two);
             square_octet(f[1], two);
@@ -208,7 +208,7 @@ append_kernel(const __grid_constant__ AppendParams P) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) f[0][e] *= kUp, f[1][e] *= kUp;
                     }
-                    codes = DT == CSA_FP32 || P.ops.norm ? fp4_codes<true>(f, unit) : fp4_codes<false>(f, unit);
+                    codes = fp4_codes<DT == CSA_FP32 || NORM>(f, unit);
                 }
                 *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
                 rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
@@ -224,8 +224,8 @@ append_kernel(const __grid_constant__ AppendParams P) {
             } else {
                 const float s = e4m3_scale(top);
                 float q[2][8];
-                scaled_octet(f[0], s, q[0]);
-                scaled_octet(f[1], s, q[1]);
+                e4m3_quotients<DT != CSA_FP32 && !NORM>(f[0], top, q[0]);
+                e4m3_quotients<DT != CSA_FP32 && !NORM>(f[1], top, q[1]);
                 *reinterpret_cast<uint4 *>(rec + 16 * lane) =
                     make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
                                e4m3x4(q[1][0], q[1][1], q[1][2], q[1][3]), e4m3x4(q[1][4], q[1][5], q[1][6], q[1][7]));
@@ -247,7 +247,7 @@ append_kernel(const __grid_constant__ AppendParams P) {
             } else if (key_lane) {
                 const float s = e4m3_scale(top);
                 const int64_t row = (int64_t)b * P.idx_cap + entry;
-                scaled_octet(g, s, g);
+                e4m3_quotients<DT != CSA_FP32>(g, top, g);
                 *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
                     make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
                 if (lane == 0) P.k_idx_scale[row] = s;
@@ -362,8 +362,11 @@ csa_status_t make_span(const csa_cache_desc &cache, csa_format_t fmt, int ring, 
 
 template <int DT, int FMT>
 cudaError_t launch_append(const AppendParams &P, PdlLaunch &l) {
-    return P.key ? cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, true>, P)
-                 : cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, false>, P);
+    if (P.ops.norm)
+        return P.key ? cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, true, true>, P)
+                     : cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, false, true>, P);
+    return P.key ? cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, true, false>, P)
+                 : cudaLaunchKernelEx(&l.cfg, append_kernel<DT, FMT, false, false>, P);
 }
 
 template <int DT>

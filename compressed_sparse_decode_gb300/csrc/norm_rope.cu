@@ -134,7 +134,8 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
             for (int v = 0; v < NV; ++v) {
                 if (live && gl + G * v < octets) {
                     float q[8];
-                    scaled_octet(f[v], s, q);
+                    if (DT != CSA_FP32 && !P.ops.norm) e4m3_quotients<true>(f[v], amax, q);
+                    else e4m3_quotients<false>(f[v], amax, q);
                     reinterpret_cast<uint2 *>(P.out)[row * octets + gl + G * v] =
                         make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
                 }

@@ -173,11 +173,6 @@ __device__ __forceinline__ float amax_octet(const float (&f)[8], float m = 0.f) 
 // As bits, whose order is that of the magnitudes, with NaN above them all.
 __device__ __forceinline__ uint32_t amax_bits(float amax) { return __float_as_uint(amax) & 0x7FFFFFFFu; }
 
-// amax / 448 as a multiplier: 1 for an all-zero block.
-__device__ __forceinline__ float e4m3_scale(uint32_t amax) {
-    return amax ? __uint_as_float(amax) * (1.f / 448.f) : 1.f;
-}
-
 // x / s correctly rounded, given inv = 1 / s (rounded): one Newton step on the
 // quotient. s is in the middle of the range (see fp4_codes).
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
@@ -198,19 +193,39 @@ __device__ __forceinline__ float sticky_quotient(float x, float s, float inv) {
     return __uint_as_float((up ? b : b - 1u) | 1u);
 }
 
-// f / s for the E4M3 codes of an octet, to an ulp or two (both times 2^60 where
-// 1 / s would leave the range).
-__device__ __forceinline__ void scaled_octet(const float (&f)[8], float s, float (&q)[8]) {
+// amax / 448 as a multiplier: 1 for an all-zero block.
+__device__ __forceinline__ float e4m3_scale(uint32_t amax) {
+    return amax ? quotient(__uint_as_float(amax), 448.f, 1.f / 448.f) : 1.f;
+}
+
+// 448 f / amax for the E4M3 codes of an octet. With a Newton step (kExact) a quotient
+// that is a halfway point of the codes comes out as that, and for values with up to
+// 21 bits (448 f is exact) every other on its own side of it, so the codes of 16-bit
+// inputs are those of the exact quotients; values that carry a rounding already go
+// without. (All times a power of two where a product or remainder would leave the
+// range.)
+template <bool kExact>
+__device__ __forceinline__ void e4m3_quotients(const float (&f)[8], uint32_t amax, float (&q)[8]) {
     float up = 1.f;
-    if (s < 1e-30f) up = 1.152921504606846976e18f;
-    const float inv = __frcp_rn(s * up);
+    if (amax < 0x0DA24260u) up = 1.152921504606846976e18f;  // below 1e-30: 2^60
+    if (amax > 0x7149F2CAu) up = 8.673617379884035e-19f;    // above 1e30: 2^-60
+    const float t = amax ? __uint_as_float(amax) * up : 448.f, inv = __frcp_rn(t);
+    const float2 k = make_float2(448.f * up, 448.f * up), ii = make_float2(inv, inv), tt = make_float2(-t, -t);
+    const float2 quick = make_float2(448.f * inv, 448.f * inv);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float2 v = __fmul2_rn(make_float2(f[2 * e], f[2 * e + 1]), make_float2(inv, inv));
-        q[2 * e] = v.x;
-        q[2 * e + 1] = v.y;
+        float2 x = make_float2(f[2 * e], f[2 * e + 1]);
+        if (kExact) {
+            x = __fmul2_rn(x, k);
+            const float2 a = __fmul2_rn(x, ii);
+            x = __ffma2_rn(__ffma2_rn(a, tt, x), ii, a);
+        } else {
+            x = __fmul2_rn(x, quick);
+        }
+        q[2 * e] = x.x;
+        q[2 * e + 1] = x.y;
     }
-    if (up != 1.f) {
+    if (!kExact && up != 1.f) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] *= up;
     }

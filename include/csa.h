@@ -374,7 +374,7 @@ CSA_API csa_status_t csa_head_norm_rope(const void *x, csa_dtype_t x_dtype, int6
 
 /* The same pass with E4M3 output, the form that csa_indexer_logits reads its
  * queries in (H = 64, D = 128): scale[b,t,h] = amax_d |y_d| / 448 (1 when all
- * are zero), codes[b,t,h,d] = e4m3(y_d / scale).
+ * are zero), codes[b,t,h,d] = e4m3(y_d / scale), ties as in csa_cache_append.
  *   codes [B,T,H,D] bytes, scale [B,T,H] fp32; neither may overlap x. */
 CSA_API csa_status_t csa_head_norm_rope_e4m3(const void *x, csa_dtype_t x_dtype, int64_t x_seq_stride,
                                              int64_t x_token_stride, int64_t x_head_stride, const int32_t *pos,
@@ -419,9 +419,11 @@ typedef struct {
  * with amax over the 448 nope dims, E = the smallest whole number with amax <=
  * 6 * 448 * 2^E (at least -111; 0 when all are zero), the block scale s =
  * e4m3(max |y| of the block / 6 * 2^-E), code = e2m1(y / (s * 2^E)), ties to
- * even in both, codes 0 where s is 0; the 4-bit quotients are decided as if
- * computed exactly, those of E4M3 codes are fp32. An infinite or NaN nope dim makes its FP8 block or its
- * 4-bit record read back as NaN in every nope dim.
+ * even in both, codes 0 where s is 0. The 4-bit quotients are decided as if
+ * computed exactly from the fp32 y; those of E4M3 codes are y * 448 / amax, exact
+ * for 16-bit inputs that are not normalised, else within two fp32 roundings. An
+ * infinite or NaN nope dim makes its FP8 block or its 4-bit record read back as
+ * NaN in every nope dim.
  * An entry outside the cache is not stored (CSA_ERR_BAD_INDEX, also for
  * first < 0 or a count outside [0, T], which is then clamped). Every other
  * record is left as it was. Sequences of one call must not share a page that

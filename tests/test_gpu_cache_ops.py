@@ -319,6 +319,43 @@ def test_values_at_the_ends_of_the_range(cuda_lib):
     assert csd.csa_read_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("amax", [7.0, 6.5, 448.0, 0.0546875, 5.1875])
+def test_e4m3_codes_of_16_bit_inputs_are_those_of_the_exact_quotients(cuda_lib, dtype, amax):
+    """Values of few bits, many of whose quotients 448 y / amax are halfway points of
+    the codes (a double holds those exactly, and its rounding of the others moves
+    none across one): records, indexer keys and queries, not normalised."""
+    csd = cuda_lib
+    g = torch.Generator().manual_seed(int(amax * 64))
+    unit = 2.0 ** np.floor(np.log2(amax) - 6)
+
+    def values(*shape):
+        x = torch.randint(-int(amax / unit), int(amax / unit) + 1, shape, generator=g).double() * unit
+        x[..., 0] = amax
+        for d in range(128, shape[-1], 128):  # the maximum of every 128-dim block
+            x[..., d] = -amax
+        return x.to(dtype)
+
+    def codes_of(x):
+        v = x.double().numpy() * 448 / amax
+        return R.signed(R.nearest_code(v, R.E4M3), v, None, 128)
+
+    x, key = values(2, 9, 512), values(2, 9, 128)
+    cache = torch.zeros((18, 592), dtype=torch.uint8, device="cuda")
+    k_idx = torch.zeros((2, 9, 128), dtype=torch.uint8, device="cuda")
+    k_scale = torch.zeros((2, 9), device="cuda")
+    csd.csa_cache_append(csd.cache_desc(cache, 9, seq_stride=9), x.cuda(), torch.zeros(2, dtype=torch.int32, device="cuda"),
+                         rope_theta=None, key=key.cuda(), k_idx=k_idx, k_idx_scale=k_scale)
+    assert np.array_equal(cache.cpu().numpy().reshape(2, 9, 592)[..., :448], codes_of(x)[..., :448])
+    assert np.array_equal(k_idx.cpu().numpy(), codes_of(key))
+    assert torch.all(k_scale.cpu() == np.float32(amax / 448))
+    q = values(3, 5, 7, 128)
+    codes, scale = csd.csa_head_norm_rope_e4m3(q.cuda(), torch.zeros((3, 5), dtype=torch.int32, device="cuda"), norm=False,
+                                               rope_dim=0)
+    assert np.array_equal(codes.cpu().numpy(), codes_of(q)) and torch.all(scale.cpu() == np.float32(amax / 448))
+    assert csd.csa_read_device_error() == 0
+
+
 def test_offsets_past_32_bits(cuda_lib):
     """A record beyond 4 GiB of the pool is written and read at its own place."""
     csd = cuda_lib
