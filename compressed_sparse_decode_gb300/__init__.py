@@ -480,9 +480,14 @@ def _dev(t: torch.Tensor, name: str) -> int:
     i = t.get_device()
     if i < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if i != torch.cuda.current_device():
+    if i != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on cuda:{i}, not on the current device: make that device current for the call")
     return i
+
+
+def _on(stream, dev: int) -> int:
+    """Handle of the stream, or of the current one of device ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
@@ -504,9 +509,11 @@ def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
     return t.data_ptr()
 
 
-def _strides(t: torch.Tensor) -> list:
+def _strides(t: torch.Tensor):
     """Strides of the leading dimensions; 0 where a dimension has one element
     (PyTorch leaves any number there)."""
+    if 1 not in t.shape[:-1]:
+        return t.stride()[:-1]
     return [s if n != 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
 
 
@@ -560,7 +567,7 @@ def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6
                                      _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                      _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
                                      _arg(out, "out", torch.bfloat16, (B, T, H, D), dev), _own_status(status, dev),
-                                     _stream(stream)), "csa_head_norm_rope")
+                                     _on(stream, dev)), "csa_head_norm_rope")
     return out
 
 
@@ -579,7 +586,7 @@ def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float =
                                           _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
                                           _arg(codes, "codes", torch.uint8, (B, T, H, D), dev),
                                           _arg(scale, "scale", torch.float32, (B, T, H), dev),
-                                          _own_status(status, dev), _stream(stream)), "csa_head_norm_rope_e4m3")
+                                          _own_status(status, dev), _on(stream, dev)), "csa_head_norm_rope_e4m3")
     return codes, scale
 
 
@@ -613,7 +620,7 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
                                    _arg(first, "first", torch.int32, (B,), dev),
                                    None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
                                    pos_stride, _how(norm, weight, eps, rope_dim, theta, DIM, dev),
-                                   idx, _own_status(status, dev), _stream(stream)), "csa_cache_append")
+                                   idx, _own_status(status, dev), _on(stream, dev)), "csa_cache_append")
 
 
 def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = False, out=None, stream=None,
@@ -629,7 +636,7 @@ def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = Fal
                                  _arg(first, "first", torch.int32, (B,), dev),
                                  None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
                                  _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _own_status(status, dev),
-                                 _stream(stream)), "csa_cache_read")
+                                 _on(stream, dev)), "csa_cache_read")
     return out
 
 
@@ -656,7 +663,7 @@ def csa_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
         _arg(topk_idx, "topk_idx", i32, (B, T, k), dev), _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
         _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, k,
         None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
-        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)),
         "csa_sink_attention_decode_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
@@ -681,7 +688,7 @@ def hca_sink_attention_decode_fp4(q, sink, softmax_scale: float, comp: csa_cache
         _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
         _arg(q_pos, "q_pos", i32, (B, T), dev), B, T, m_hca,
         None if out is None else _arg(out, "out", torch.bfloat16, (B, T, HEADS, DIM), dev),
-        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)),
+        _arg(lse, "lse", f32, (B, T, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)),
         "hca_sink_attention_decode_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
@@ -713,7 +720,7 @@ def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, 
         _arg(lse, "lse", f32, (B, T, HEADS), dev),
         None if topk_idx is None else _arg(topk_idx, "topk_idx", i32, (B, T, k), dev),
         None if topk_cnt is None else _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
-        epi, *_ws(ws, dev), _own_status(status, dev), _stream(stream)), "csa_decode_step_fp4")
+        epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)), "csa_decode_step_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
 
 
