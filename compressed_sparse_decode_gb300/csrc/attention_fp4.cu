@@ -35,6 +35,11 @@
 // of a block: oth(i + 1), peer(i), own(i + 1), and QK(i + 1) over oth, PV(i),
 // QK(i + 1) over own: the chain own -> QK -> softmax -> PV -> own of the next
 // block sets the pace, the rest runs beside it.
+// Measured: 32 queries of 2176 candidates 46 us (395 TFLOP/s, 0.21 of the cuBLAS
+// rate; FP8 records: 57), 64 queries of 8320 candidates 222 us (628 TFLOP/s, 0.34;
+// FP8 records: 313), 24 ragged queries 21.7 us, one query of 192 candidates 15.7 us.
+// A block takes about 6500 cycles, of which the tensor core works 31 %: the MMAs
+// of 64 columns run at half rate, and the chain above leaves it waiting.
 // Every role's loop is kept short and every helper at one place: the instruction
 // caches are shared by all warps and by neighbouring SMs (a second copy of the
 // unpacking, one per rank, cost 9 %).

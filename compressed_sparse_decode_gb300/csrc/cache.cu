@@ -6,6 +6,12 @@
 // dims [16 l, 16 l + 16): lanes 0..27 the nope dims (one 4-bit scale block each,
 // eight lanes an FP8 block), lanes 28..31 the rope dims. So the 4-bit block
 // maximum needs no shuffle, and a record is written with one vector store a lane.
+//
+// Appending is bound by instructions: 8 x up to 8192 tokens, normalised, into FP8
+// records with indexer keys took 500 instructions a token, 69 % of the issue slots,
+// 32 us (98 MB: 0.45 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
+// records 16 us; one token of 32 sequences 2.5 us, a launch. Reading 8 x up to 8192
+// FP8 records back: 79 MB in 17.9 us, 0.65 of the copy rate.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"

@@ -14,6 +14,11 @@
  * and the heavily-compressed (HCA) variant that attends to every visible entry
  * with no indexer -> hca_sink_attention_decode. csa_decode_step runs 1, 2, 4.
  *
+ * Beside the step: queries and latents are prepared by csa_head_norm_rope and
+ * csa_head_norm_rope_e4m3, caches are filled by csa_cache_append and read back by
+ * csa_cache_read, and the *_fp4 calls run the attention and the step over caches
+ * of 4-bit records.
+ *
  * Conventions for every call
  *  - Pointers are DEVICE pointers unless stated; the caller owns all memory.
  *    The library allocates no device memory (csa_pipeline_create makes a
@@ -451,7 +456,9 @@ CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_t fmt, int 
  * csa_sink_attention_decode_ex, hca_sink_attention_decode_ex and
  * csa_decode_step_ex, but comp and swa_ring hold records of
  * CSA_FP4_RECORD_BYTES bytes (swa_ring [B,R,384]). The latents enter the tensor
- * cores without a rounding; the softmax weights are rounded to BF16. */
+ * cores without a rounding; the softmax weights are rounded to BF16, and the
+ * partial outputs of a query that is split over several CTAs to FP16 in units of
+ * a power of two for each 32 dims. lse of a query without candidates is the sink. */
 CSA_API csa_status_t csa_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale,
                                                    csa_cache_desc comp, const void *swa_ring, int R, int W,
                                                    const int32_t *topk_idx, const int32_t *topk_cnt,
