@@ -7,10 +7,9 @@
 //   s = amax |y| / 448.
 //
 // One pass: a head is read once into registers and written once. 4 x 1027 tokens of
-// 128 heads of 512 BF16 values (63 % of them not padding): 637 MB in 139 us, 4.6
-// TB/s or 0.68 of the measured copy rate, with 70 % of the issue slots busy (260
-// instructions a head); nothing is left that would not trade one for the other.
-// One token of 128 heads: 2.8 us, a launch and two trips to memory.
+// 128 heads of 512 BF16 values (63 % of them not padding): 637 MB in 132 us, 4.8
+// TB/s or 0.71 of the measured copy rate, with two thirds of the issue slots busy.
+// One token of 128 heads: 2.5 us, a launch and two trips to memory.
 #include "rows.cuh"
 
 namespace csa {
@@ -31,11 +30,11 @@ struct NormRopeParams {
 };
 
 // A group of G lanes holds a head (NV octets a lane) and takes per_group
-// consecutive heads, the loads of the next two in flight. What
-// bounds the pass is DRAM only if a head costs few instructions: the rotation's
-// sines and cosines are computed once a token and block, into shared memory
-// (each head for itself took 120 of 390 instructions), the norm's weights stay in
-// registers.
+// consecutive heads, the next one's loads under the current one (two heads ahead
+// needs registers that cost warps: 139 us instead of 132). What bounds the pass is
+// DRAM only if a head costs few instructions: the rotation's sines and cosines are
+// computed once a token and block, into shared memory (each head for itself took
+// 120 of 390 instructions), the norm's weights stay in registers.
 template <int DT, int G, int NV, bool E4M3>
 __global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 4 : 8)
 norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
@@ -54,7 +53,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
     struct Head {
         Octet<DT> x[NV];
         int pos, token;
-    } even, odd;  // two heads' loads in flight
+    } now, next;
     auto fetch = [&](int i, Head &o) {
         o.pos = -1;
         if (i >= P.per_group || r0 + i >= P.rows) return;
@@ -71,8 +70,9 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
         for (int v = 0; v < NV; ++v)
             if (gl + G * v < octets) o.x[v].load(P.x, at + 8 * (gl + G * v));
     };
-    fetch(0, even);
-    fetch(1, odd);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) next.x[v].clear();  // (octets past D stay so)
+    fetch(0, next);
 
     if (pairs) {
         const int last = min(block0 + kGroups * P.per_group, P.rows) - 1;
@@ -95,12 +95,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
         float2 two = make_float2(0.f, 0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            if (live && gl + G * v < octets) {
-                now.x[v].floats(f[v]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[v][e] = 0.f;
-            }
+            now.x[v].floats(f[v]);  // (a head that does not count: whatever was there)
             square_octet(f[v], two);
         }
         if (P.ops.norm) {
@@ -150,11 +145,10 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
         }
     };
 #pragma unroll 1
-    for (int i = 0; i < P.per_group; i += 2) {
-        finish(i, even);
-        fetch(i + 2, even);
-        finish(i + 1, odd);
-        fetch(i + 3, odd);
+    for (int i = 0; i < P.per_group; ++i) {
+        now = next;
+        fetch(i + 1, next);
+        if (G < 32 || now.pos >= 0) finish(i, now);
     }
 }
 
