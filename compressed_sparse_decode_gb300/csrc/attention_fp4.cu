@@ -8,41 +8,26 @@
 //
 // Work unit = (query token, candidate split), on a cluster of two CTAs. The
 // 128 x 512 fp32 output fills all of one SM's tensor memory, so CTA r keeps
-// output dims [256 r, 256 r + 256) of every head (256 columns). The scores are
-// split by candidate: of each block of 128 candidates CTA r computes QK and the
-// softmax weights of the 64 it owns, over all 512 dims, and sends the weights
-// (128 heads x 64, BF16, 16 KB) to the other CTA's shared memory; each CTA then
-// adds both halves' weights times its own dims of both halves' latents. So QK
-// and the exponentials run once a pair, not once a CTA, and three quarters of
-// the latents' dims are unpacked a CTA instead of all. Per block of 128 and CTA:
-//   QK   S = Q X^T        M = 128 heads, N = 64 own candidates, K = 512
-//   PV   O += P X[:, own] M = 128, N = 256 own dims, K = 64, for own and for
-//                         the other CTA's candidates
-// Both CTAs scale the weights by the same reference maximum: each sends the
-// largest of its 64 scores of every head (512 B) to the other, and both apply
-// the same rule to the pair of maxima (the reference moves only when they
-// exceed it by more than 2^8, log2 domain), so neither has to look at the
-// other's decision. The weights are computed with the old reference while the
-// maxima travel.
+// dims [256 r, 256 r + 256) of everything: of the query (in tensor memory), of the
+// latents and of the output. Per block of 128 candidates, 64 of which are a CTA's
+// own, each CTA runs
+//   QK   S = Q[:, own dims] X[:, own dims]^T   M = 128 heads, N = 128, K = 256
+//   PV   O += P X[:, own dims]                 M = 128, N = 256 dims, K = 128
+// and each latent is unpacked once a pair. Between them the pair exchanges, through
+// distributed shared memory: the scores' partial sums (fp32, each sends those of
+// the other's own candidates, 32 KB), every head's largest own score (512 B), and
+// the softmax weights of the own candidates (BF16, 16 KB). Both scale the weights
+// by the same reference maximum: they apply the same rule to the pair of maxima
+// (the reference moves only when they exceed it by more than 2^8, log2 domain), so
+// neither has to look at the other's decision. The weights are computed with the
+// old reference while the maxima travel, and the next block's partial sums travel
+// while PV runs.
 //
-// Latents come as three kinds of pieces of 64 candidates x 256 dims: "oth", the
-// other CTA's dims of the own candidates (read by QK only), "own", the own dims
-// of the own candidates (QK and PV), and "peer", the own dims of the other
-// CTA's candidates (PV only). A pointer warp resolves the records, four warps copy
-// the pieces' bytes into staging (cp.async; a cp.async.bulk a record took 80
-// cycles each, 2.5 times this kernel's time), eight warps unpack them, exactly
-// (see csa_format_t), to BF16 in the MMA's layout, one 32 KB buffer a kind. Order
-// of a block: oth(i + 1), peer(i), own(i + 1), and QK(i + 1) over oth, PV(i),
-// QK(i + 1) over own: the chain own -> QK -> softmax -> PV -> own of the next
-// block sets the pace, the rest runs beside it.
-// Measured: 32 queries of 2176 candidates 46 us (395 TFLOP/s, 0.21 of the cuBLAS
-// rate; FP8 records: 57), 64 queries of 8320 candidates 222 us (628 TFLOP/s, 0.34;
-// FP8 records: 313), 24 ragged queries 21.7 us, one query of 192 candidates 15.7 us.
-// A block takes about 6500 cycles, of which the tensor core works 31 %: the MMAs
-// of 64 columns run at half rate, and the chain above leaves it waiting.
-// Every role's loop is kept short and every helper at one place: the instruction
-// caches are shared by all warps and by neighbouring SMs (a second copy of the
-// unpacking, one per rank, cost 9 %).
+// Warps: one resolves the records and fetches their lines into L2; eight unpack
+// them, exactly (see csa_format_t), from global memory into the MMA's layout in
+// two buffers of a block, the next 64 candidates' bytes in registers meanwhile;
+// one issues the MMAs, QK(i + 1) before PV(i); eight do the softmax and the
+// epilogue, two threads a head.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -54,24 +39,14 @@ namespace {
 constexpr int kChunk = 64;                 // candidates of a block that a CTA owns
 constexpr int kBlock = 2 * kChunk;         // candidates a block
 constexpr int kHalf = 256;                 // output dims per CTA
-constexpr int kConvWarps = 8;              // unpacking: warps 0..7, four threads a candidate
+constexpr int kConvWarps = 8;              // unpacking: warps 0..7, four threads a candidate, 64 at a time
 constexpr int kSoftWarps = 8;              // softmax and epilogue: warps 8..15, two threads a head
 constexpr int kPtrWarp = 16;               // record pointers
 constexpr int kMmaWarp = 17;               // MMA issuer, TMEM owner
-constexpr int kCopyWarp = 18, kCopyWarps = 4;  // copies into staging
-constexpr int kCopyRows = kChunk / kCopyWarps;
-constexpr int kThreads = 32 * (kCopyWarp + kCopyWarps);
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
-constexpr int kAtom = kChunk * 128;        // 64 candidates x 64 dims, 128-byte swizzled rows
-constexpr int kPieceBytes = 4 * kAtom;     // 64 candidates x 256 dims, 32 KB
-constexpr int kOth = 0, kOwn = 1, kPeer = 2, kKinds = 3;
-// Staged bytes of a row of a piece. Lower half: codes 0..127, then bytes 352..383
-// (scales and power); upper half: bytes 128..383 (codes, rope dims, scales,
-// power). The strides put a warp's 8-byte reads of four rows in 32 different banks.
-constexpr int kLoCodes = 128, kLoStride = 160, kHiStride = 288;
-constexpr int kStageBytes = kChunk * (kLoStride + 2 * kHiStride);  // the larger rank's three pieces
-constexpr int kQTmemDims = 384;            // Q dims held in TMEM; the rest in shared memory
-constexpr int kQAtom = kHeads * 128;       // 64 dims of Q: 128 rows x 128 B
+constexpr int kAtom = kBlock * 128;        // 128 candidates x 64 dims, 128-byte swizzled rows
+constexpr int kBlockBytes = 4 * kAtom;     // 128 candidates x 256 dims, 64 KB
 constexpr int kPtrRing = 4;                // blocks of resolved record pointers
 constexpr int kPieces = kHalf / 32 / 2;    // 32-column pieces of the output per softmax thread
 constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
@@ -79,24 +54,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;               // the reference moves only by more than 2^8
 
-constexpr uint32_t kColQ = 0;    // 192 columns: Q dims 0..383, BF16 pairs
-constexpr uint32_t kColS = 192;  // 64 columns: scores
+constexpr uint32_t kColQ = 0;    // 128 columns: the own dims of Q, BF16 pairs
+constexpr uint32_t kColS = 128;  // 128 columns: scores, own candidates first
 constexpr uint32_t kColO = 256;  // 256 columns: O half, fp32
 constexpr uint32_t kTmemCols = 512;
 
 struct AttSmem {
-    alignas(1024) uint8_t x[kKinds][kPieceBytes];
-    alignas(1024) uint8_t qs[2 * kQAtom];      // Q dims 384..511
+    alignas(1024) uint8_t x[2][kBlockBytes];
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
+    float4 part[2][kSoftCols / 4][kHeads];     // the other CTA's part of the own scores
     float pmax[2][4][kHeads];                  // maxima: own CTA's halves, the other CTA's halves
-    alignas(16) uint8_t stage[kStageBytes];
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
-    uint64_t stage_full[kKinds], stage_empty[kKinds], x_full[kKinds], x_empty[kKinds];
-    uint64_t own_first;                        // the first two column blocks of an own piece
+    uint64_t x_full[2], x_empty[2][2];         // of a buffer; of its chunks
     uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
-    uint64_t s_full, s_free, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
+    uint64_t s_full, s_free, part_full, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -196,6 +169,12 @@ __device__ __forceinline__ void store_to_peer(uint32_t addr, float v, uint32_t b
                  "r"(__float_as_uint(v)), "r"(bar)
                  : "memory");
 }
+__device__ __forceinline__ void store4_to_peer(uint32_t addr, const uint32_t *v, uint32_t bar) {
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+        : "memory");
+}
 // Copy into the other CTA, counted on a barrier there.
 __device__ __forceinline__ void copy_to_peer(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile(
@@ -237,52 +216,51 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Unpacks a thread's quarter of a staged row: units i < 4 of 16 dims, codes at
-// code + 32 i, scale byte at scale + 4 i, to column block i, 16-byte chunks 2 hq
-// and 2 hq + 1. `rope`: the last unit is 16 rope dims, copied as they are.
-// `half_done`: arrived on by the warp after the first two.
-__device__ __forceinline__ void unpack_row(const uint8_t *code, const uint8_t *scale, const uint8_t *power,
-                                           const uint8_t *rope, uint4 *lo, uint4 *hi, uint64_t *half_done) {
-    constexpr int kStep = kAtom / 16;
-    const float pw = fp4_power(*power);
-    uint2 c[4];
-    uint32_t sb[4];
+// A thread's quarter of a record's own half, as it lies in the record: four units
+// of 16 dims, 64 apart (the last unit of the upper half is 16 rope dims).
+struct Quarter {
+    uint2 code[4];
+    uint4 rope[2];
+    uint4 scale;  // byte hq of word i: unit i's
+    uint32_t power;
+    __device__ __forceinline__ void load(const uint8_t *rec, int rank, int hq) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        c[i] = *reinterpret_cast<const uint2 *>(code + 32 * i);
-        sb[i] = scale[4 * i];
-    }
+        for (int i = 0; i < 4; ++i) code[i] = make_uint2(0, 0);
+        rope[0] = rope[1] = scale = make_uint4(0, 0, 0, 0);  // no record: zero latents
+        power = 0;
+        if (!rec) return;
+        const uint8_t *own = rec + rank * (kHalf / 2) + 8 * hq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float s = e4m3x2_to_float2((uint16_t)sb[i]).x * pw;
-        uint4 l = unpack8(c[i].x, make_float2(s, s)), h = unpack8(c[i].y, make_float2(s, s));
-        if (i == 3 && rope) {
-            l = *reinterpret_cast<const uint4 *>(rope);
-            h = *reinterpret_cast<const uint4 *>(rope + 16);
-        }
-        lo[i * kStep] = l;
-        hi[i * kStep] = h;
-        if (i == 1 && half_done) {
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(half_done);
+        for (int i = 0; i < 3; ++i) code[i] = __ldcs(reinterpret_cast<const uint2 *>(own + 32 * i));
+        scale = __ldcs(reinterpret_cast<const uint4 *>(rec + kFp4ScaleOffset + 16 * rank));
+        if (rank == 0) {
+            code[3] = __ldcs(reinterpret_cast<const uint2 *>(own + 96));
+            power = __ldcs(reinterpret_cast<const uint32_t *>(rec + kFp4PowerOffset));
+        } else {
+            const uint4 *r = reinterpret_cast<const uint4 *>(rec + kFp4RopeOffset + 32 * hq);
+            rope[0] = __ldcs(r);
+            rope[1] = __ldcs(r + 1);
+            power = scale.w;  // (bytes 380..383)
         }
     }
-}
-
-// 16-byte copy into shared memory; `bytes` = 0 stores zeros.
-__device__ __forceinline__ void copy16(void *dst, const void *src, uint32_t bytes, uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(ptx::smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "l"(policy)
-                 : "memory");
-}
-// Arrive (as a counted thread) when this thread's copies so far have landed.
-__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
-    // The address goes through a shuffle so that it stays a per-lane value: builds
-    // in which the compiler knew it to be uniform ended in an illegal instruction.
-    const uint32_t a = __shfl_sync(0xffffffffu, ptx::smem_u32(bar), threadIdx.x & 31);
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(a) : "memory");
-}
+    // to column block i of a row at lo / hi (16-byte chunks 2 hq and 2 hq + 1)
+    __device__ __forceinline__ void unpack(int rank, int hq, uint4 *lo, uint4 *hi) const {
+        constexpr int kStep = kAtom / 16;
+        const float pw = fp4_power(power & 0xFFu);
+        const uint32_t sw[4] = {scale.x, scale.y, scale.z, scale.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i == 3 && rank == 1) {
+                lo[i * kStep] = rope[0];
+                hi[i * kStep] = rope[1];
+                break;
+            }
+            const float s = e4m3x2_to_float2((uint16_t)((sw[i] >> (8 * hq)) & 0xFFu)).x * pw;
+            lo[i * kStep] = unpack8(code[i].x, make_float2(s, s));
+            hi[i * kStep] = unpack8(code[i].y, make_float2(s, s));
+        }
+    }
+};
 
 // ---------------------------------------------------------------- the kernel
 
@@ -295,19 +273,17 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     volatile int *abort = &s.abort_flag;
 
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kKinds; ++k) {
-            ptx::mbar_init(&s.stage_full[k], 32 * kCopyWarps);
-            ptx::mbar_init(&s.stage_empty[k], kConvWarps);
-            ptx::mbar_init(&s.x_full[k], kConvWarps);
-            ptx::mbar_init(&s.x_empty[k], 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s.x_full[i], 2 * kConvWarps);  // both chunks of a block
+            for (int c = 0; c < 2; ++c) ptx::mbar_init(&s.x_empty[i][c], 1);
         }
-        ptx::mbar_init(&s.own_first, kConvWarps);
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
-            ptx::mbar_init(&s.ptr_empty[i], kCopyWarps + kSoftWarps);
+            ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
         }
         ptx::mbar_init(&s.s_full, 1);
         ptx::mbar_init(&s.s_free, kSoftWarps);
+        ptx::mbar_init(&s.part_full, kSoftWarps);  // (and the other CTA's bytes)
         ptx::mbar_init(&s.p_full, kSoftWarps);
         ptx::mbar_init(&s.pp_full, 1);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.max_full[i], kSoftWarps);  // (and the other CTA's bytes)
@@ -340,25 +316,6 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         const bool now = !poll && try_wait_cluster(bar, parity);
         return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
     };
-    // which half of the dims a kind of piece holds, and where it is staged
-    auto upper_half = [&](int k) { return (k == kOth) != (rank == 1); };
-    // the order of use: oth(0) own(0) | oth(i) peer(i - 1) own(i) | .. | peer(n - 1)
-    auto next_piece = [&](int &i, int &k) {
-        if (k == kOth) {
-            if (i == 0) k = kOwn;
-            else k = kPeer, --i;
-        } else if (k == kPeer) {
-            k = kOwn, ++i;
-        } else {
-            if (i + 1 < u.n_blocks) k = kOth, ++i;
-            else k = kPeer;
-        }
-    };
-    auto stage_of = [&](int k) {
-        const int oth = rank ? kLoStride : kHiStride, own = rank ? kHiStride : kLoStride;
-        return s.stage + kChunk * (k == kOth ? 0 : k == kOwn ? oth : oth + own);
-    };
-
     if (warp == kPtrWarp) {
         // ------------------------------------------------------------ record pointers
         // Lane L resolves candidates L, L + 32, .. of a block (own chunk first) in
@@ -430,96 +387,52 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         }
     } else if (warp < kConvWarps) {
         // ------------------------------------------------------------ unpack
+        // Of every block 64 own candidates and 64 of the other CTA's, four threads a
+        // candidate; the bytes of a chunk are under way while the block before it is
+        // unpacked.
         const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
-#pragma unroll 1
-        for (int left = 3 * u.n_blocks, i = 0, k = kOth; left > 0; --left) {
-            if (!wait(&s.stage_full[k], i & 1) || !wait(&s.x_empty[k], (i & 1) ^ 1)) { fail(); break; }
-            const bool upper = upper_half(k);
-            const uint8_t *base = stage_of(k) + row * (upper ? kHiStride : kLoStride);
-            unpack_row(base + 8 * hq, base + (upper ? kFp4ScaleOffset + 16 - kLoCodes : kLoCodes) + hq,
-                       base + (upper ? kFp4PowerOffset - kLoCodes : kLoCodes + kFp4PowerOffset - kFp4ScaleOffset),
-                       upper ? base + kFp4RopeOffset - kLoCodes + 32 * hq : nullptr, sw128(s.x[k], row, 2 * hq),
-                       sw128(s.x[k], row, 2 * hq + 1), k == kOwn ? &s.own_first : nullptr);
+        Quarter own, other;
+        auto fetch = [&](int i, int chunk, Quarter &q) {
+            q.load(s.rec[i % kPtrRing][chunk * kChunk + row], rank, hq);
+        };
+        auto unpack = [&](int i, int chunk, const Quarter &q) {
+            const int r = chunk * kChunk + row, b = i & 1;
+            q.unpack(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(&s.stage_empty[k]);
-                ptx::mbar_arrive(&s.x_full[k]);
-            }
-            next_piece(i, k);
-        }
-    } else if (warp >= kCopyWarp) {
-        // ------------------------------------------------------------ copies into staging
-        // Each warp copies kCopyRows rows of every piece, 16 bytes a lane; a row
-        // without a record is filled with zeros (codes, scales and power: zero latents).
-        const uint64_t policy = ptx::l2_policy_evict_first();  // a pair reads a record within a block, nobody later
-        // The first block's pieces, then in the order of their use the same kind of
-        // the next block: each staging buffer is filled again as soon as it is free.
+            if (lane == 0) ptx::mbar_arrive(&s.x_full[b]);
+        };
         bool ok = true;
-        int first = 0;
+        if (u.n_blocks > 0) {
+            ok = wait(&s.ptr_full[0], 0);
+            if (ok) fetch(0, 0, own);
+            if (ok) fetch(0, 1, other);
+        }
 #pragma unroll 1
-        for (int left = 3 * u.n_blocks, i = 0, k = kOth; left > 0; --left) {
-            const int b = first < kKinds ? 0 : i + 1, kind = first < kKinds ? first : k;
-            if (b < u.n_blocks) {
-                const int pr = b % kPtrRing;
-                if (!wait(&s.ptr_full[pr], (b / kPtrRing) & 1) || !wait(&s.stage_empty[kind], (b & 1) ^ 1)) { ok = false; break; }
-                const bool upper = upper_half(kind);
-                const int row0 = (warp - kCopyWarp) * kCopyRows, stride = upper ? kHiStride : kLoStride;
-                const uint8_t *const *recs = s.rec[pr] + (kind == kPeer ? kChunk : 0) + row0;
-                uint8_t *dst = stage_of(kind) + row0 * stride;
-                // `per` lanes a row: 256 bytes from byte 128 (upper), or the 128 of
-                // the codes and then 32 from byte 352 (lower)
-                auto rows = [&](int per, int from, int to) {
-                    const int c = 16 * (lane & (per - 1));
-#pragma unroll 4
-                    for (int r = lane / per; r < kCopyRows; r += 32 / per) {
-                        const uint8_t *rec = recs[r];
-                        copy16(dst + r * stride + to + c, (rec ? rec : P.ring) + from + c, rec ? 16u : 0u, policy);
-                    }
-                };
-                rows(upper ? 16 : 8, upper ? kLoCodes : 0, 0);
-                if (!upper) rows(2, kFp4ScaleOffset, kLoCodes);
-                arrive_after_copies(&s.stage_full[kind]);
-                if (kind == kPeer) {  // the block's last look at its pointers
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
-                }
+        for (int i = 0; i < u.n_blocks && ok; ++i) {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[i % kPtrRing]);  // (both chunks' pointers have been read)
+            const int n = i + 1;
+            const bool more = n < u.n_blocks;
+            ok = !more || wait(&s.ptr_full[n % kPtrRing], n / kPtrRing & 1);
+            ok = ok && wait(&s.x_empty[i & 1][0], (i >> 1 & 1) ^ 1);
+            if (!ok) break;
+            unpack(i, 0, own);
+            ok = wait(&s.x_empty[i & 1][1], (i >> 1 & 1) ^ 1);
+            if (!ok) break;
+            unpack(i, 1, other);
+            if (more) {
+                fetch(n, 0, own);
+                fetch(n, 1, other);
             }
-            if (first < kKinds) {
-                ++first;
-                ++left;
-                continue;
-            }
-            next_piece(i, k);
         }
         if (!ok) fail();
-        ptx::cp_async_commit();
-        ptx::cp_async_wait<0>();  // no copy lands after this warp has moved on
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdescQK = ptx::idesc_f32acc(1, 1, 128, kChunk);
+        constexpr uint32_t kIdescQK = ptx::idesc_f32acc(1, 1, 128, kBlock);
         constexpr uint32_t kIdescPV = ptx::idesc_f32acc(1, 1, 128, kHalf, 1);
         const uint32_t leader = elect_one();
         bool ok = u.n_blocks == 0 || wait(&s.q_ready, 0);
-        const uint64_t qd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.qs));
-        // eight K-steps, dims 128 q ..: Q from TMEM below kQTmemDims, from shared
-        // memory above
-        static_assert(kQTmemDims == 384, "the last quarter of Q is in shared memory");
-        auto qk_quarter = [&](int q, const uint8_t *x, bool first) {
-            const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(x + (q & 1) * 2 * kAtom));
-            if (!leader) return;
-            if (q < 3) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + q * 64 + k * 8,
-                                    xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, !(first && k == 0));
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    ptx::mma_f16(tmem + kColS, qd + (uint64_t)(((k >> 2) * kQAtom + (k & 3) * 32) >> 4),
-                                 xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, 1u);
-            }
-        };
         auto pv = [&](const uint8_t *w, const uint8_t *x, bool first) {
             const uint64_t ad = ptx::desc_kmajor_sw128(ptx::smem_u32(w));
             const uint64_t bd = ptx::desc_mnmajor_sw128(ptx::smem_u32(x), kAtom, 1024);
@@ -531,38 +444,39 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         };
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
-            const uint32_t ph = i & 1, before = ph ^ 1;
-            // QK(i) over oth | PV(i - 1) of the own, of the other CTA's candidates | QK(i) over own
-#pragma unroll 1
-            for (int part = 0; part < 4 && ok; ++part) {
-                const bool qk = part == 0 || part == 3;
-                if (qk ? i == u.n_blocks : i == 0) continue;
-                const int k = part == 0 ? kOth : part == 2 ? kPeer : kOwn;
-                if (part == 0) ok = wait(&s.x_full[k], ph) && (i == 0 || wait(&s.s_free, before));
-                else if (part == 1) ok = wait(&s.p_full, before);
-                else if (part == 2) ok = wait(&s.x_full[k], before) && wait_peer(&s.pp_full, before);
+            if (i < u.n_blocks) {  // QK(i)
+                ok = wait(&s.x_full[i & 1], i >> 1 & 1) && (i == 0 || wait(&s.s_free, (i & 1) ^ 1));
                 if (!ok) break;
                 ptx::tc_fence_after();
-                if (qk) {
-                    const int hf = part == 0 ? rank ^ 1 : rank;
-#pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        if (part == 3) {  // each half of the piece as soon as it is there
-                            ok = wait(e ? &s.x_full[k] : &s.own_first, ph);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                        }
-                        qk_quarter(2 * hf + e, s.x[k], part == 0 && e == 0);
-                    }
-                    if (!ok) break;
-                    if (leader) ptx::mma_commit(part == 0 ? &s.x_empty[k] : &s.s_full);
-                } else {
-                    pv(part == 1 ? s.p : s.pp, s.x[k], i == 1 && part == 1);
-                    if (leader) {
-                        ptx::mma_commit(&s.x_empty[k]);
-                        if (part == 1) ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
-                        else commit_both(&s.o_done);
-                    }
+                const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.x[i & 1]));
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < kHalf / 16; ++k)
+                        ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8,
+                                        xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, k > 0);
+                    ptx::mma_commit(&s.s_full);
+                }
+                __syncwarp();
+            }
+            if (i > 0) {  // PV(i - 1): the own, then the other CTA's candidates
+                const uint32_t ph = (i & 1) ^ 1;
+                const uint8_t *x = s.x[ph];
+                ok = wait(&s.p_full, ph);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                pv(s.p, x, i == 1);
+                if (leader) {
+                    ptx::mma_commit(&s.x_empty[ph][0]);
+                    ptx::mbar_arrive_expect_tx(&s.pp_full, kHeads * 128);
+                }
+                __syncwarp();
+                ok = wait_peer(&s.pp_full, ph);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                pv(s.pp, x + kChunk * 128, false);
+                if (leader) {
+                    ptx::mma_commit(&s.x_empty[ph][1]);
+                    commit_both(&s.o_done);
                 }
                 __syncwarp();
             }
@@ -590,6 +504,8 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t peer_max = ptx::mapa(ptx::smem_u32(&s.pmax[0][2 + half][h]), rank ^ 1);
         const uint32_t peer_max_full = ptx::mapa(ptx::smem_u32(&s.max_full[0]), rank ^ 1);
+        const uint32_t peer_part = ptx::mapa(ptx::smem_u32(&s.part[half][0][h]), rank ^ 1);
+        const uint32_t peer_part_full = ptx::mapa(ptx::smem_u32(&s.part_full), rank ^ 1);
         const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp), rank ^ 1);
         const uint32_t peer_pp_full = ptx::mapa(ptx::smem_u32(&s.pp_full), rank ^ 1);
         // this thread's maximum of block i (or, at the end, its sum) to the other
@@ -604,22 +520,17 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         auto received = [&](int i, int from) { return *reinterpret_cast<volatile float *>(&s.pmax[i & 1][from][h]); };
         bool ok = true;
         if (u.n_blocks > 0) {
-            // Q: dims from kQTmemDims up -> shared memory, the dims below -> TMEM
-            // (BF16 pairs, lane = head), 64 dims a piece, half the pieces a thread. A
-            // load takes four heads' 128 bytes (a head a lane would touch 32 lines);
-            // the warp's 4 KB of the weights' buffers, not used yet, turn them into a
-            // head a lane.
+            // The own dims of Q -> TMEM (BF16 pairs, lane = head), 64 dims a piece, two
+            // of the four pieces a thread. A load takes four heads' 128 bytes (a head a
+            // lane would touch 32 lines); the warp's 4 KB of the weights' buffers, not
+            // used yet, turn them into a head a lane.
             const int r4 = lane >> 3, c = lane & 7;
-            const uint4 *qg = reinterpret_cast<const uint4 *>(P.q + ((size_t)u.r * kHeads + quarter * 32 + r4) * kDim) + c;
+            const uint4 *qg = reinterpret_cast<const uint4 *>(
+                P.q + ((size_t)u.r * kHeads + quarter * 32 + r4) * kDim + rank * kHalf) + c;
             uint8_t *turn = half ? s.pp + quarter * 4096 : s.p + quarter * 4096;
             const uint64_t policy = ptx::l2_policy_evict_first();
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-                ptx::cp_async_16_hint(sw128(s.qs + half * kQAtom, quarter * 32 + 4 * g + r4, c),
-                                      qg + (size_t)4 * g * (kDim / 8) + kQTmemDims / 8 + 8 * half, policy);
-            ptx::cp_async_commit();
-#pragma unroll 1
-            for (int pc = 3 * half; pc < 3 * half + 3; ++pc) {
+            for (int pc = 2 * half; pc < 2 * half + 2; ++pc) {
                 uint4 w[8];
 #pragma unroll
                 for (int g = 0; g < 8; ++g) w[g] = ptx::ldg_v4_policy(qg + (size_t)4 * g * (kDim / 8) + 8 * pc, policy);
@@ -638,23 +549,36 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 ptx::tmem_st32(lane_base + kColQ + pc * 32, regs);
                 __syncwarp();
             }
-            ptx::cp_async_wait<0>();
             ptx::tmem_st_wait();
-            ptx::fence_proxy_async_smem();
+            ptx::fence_proxy_async_smem();  // the turning buffers -> the other CTA's copies into them
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.q_ready);
         }
+        // this CTA's part of the other's scores of block i, when QK(i) is done
+        auto send_part = [&](int i) {
+            if (!wait(&s.s_full, i & 1)) return false;
+            ptx::tc_fence_after();
+            uint32_t v[kSoftCols];
+            ptx::tmem_ld32(lane_base + kColS + kChunk + half * kSoftCols, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < kSoftCols / 4; ++c)
+                store4_to_peer(peer_part + c * (kHeads * 16), v + 4 * c, peer_part_full);
+            __syncwarp();
+            // (each warp expects the bytes of the other CTA's warp like it)
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&s.part_full, 32 * 4 * kSoftCols);
+            return true;
+        };
+        if (u.n_blocks > 0 && !send_part(0)) { fail(); ok = false; }
         float m = -INFINITY, l = 0.f;  // reference and own sum, log2 domain, sink not included
 #pragma unroll 1
-        for (int i = 0; i < u.n_blocks; ++i) {
+        for (int i = 0; i < u.n_blocks && ok; ++i) {
             const int pr = i % kPtrRing;
             if (!wait(&s.ptr_full[pr], (i / kPtrRing) & 1)) { fail(); ok = false; break; }
             const uint32_t mask = *reinterpret_cast<volatile uint32_t *>(&s.vmask[pr][half]);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.ptr_empty[pr]);
-            if (!wait(&s.s_full, i & 1)) { fail(); ok = false; break; }
-            ptx::tc_fence_after();
             float z[kSoftCols];  // raw scores, -inf where there is no candidate
             {
                 uint32_t sv[kSoftCols];
@@ -663,8 +587,17 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&s.s_free);
+                // (the buffer is free for block i + 1 once this CTA's maxima are sent:
+                // the other CTA sends its parts after it has those of block i)
+                if (!wait_peer(&s.part_full, i & 1)) { fail(); ok = false; break; }
 #pragma unroll
-                for (int c = 0; c < kSoftCols; ++c) z[c] = __uint_as_float(sv[c]);
+                for (int c = 0; c < kSoftCols / 4; ++c) {
+                    const float4 o = s.part[half][c][h];
+                    z[4 * c] = __uint_as_float(sv[4 * c]) + o.x;
+                    z[4 * c + 1] = __uint_as_float(sv[4 * c + 1]) + o.y;
+                    z[4 * c + 2] = __uint_as_float(sv[4 * c + 2]) + o.z;
+                    z[4 * c + 3] = __uint_as_float(sv[4 * c + 3]) + o.w;
+                }
             }
             if (mask != 0xffffffffu) {
 #pragma unroll
@@ -744,6 +677,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (lane == 0)
                     copy_to_peer(peer_pp + quarter * 32 * 128, s.p + quarter * 32 * 128, 32 * 128, peer_pp_full);
             }
+            if (i + 1 < u.n_blocks && !send_part(i + 1)) { fail(); ok = false; }
         }
         // both halves' warps of a quarter have staged their output columns (the
         // phase before this one is complete: the sums came after it)
@@ -814,7 +748,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             // Rows are staged in shared memory (the pieces' buffers are free once
             // every PV is done), then each warp writes its 32 head rows whole.
             // Chunk c (16 B) of row h sits at position c ^ (h & 7).
-            uint8_t *ostage = &s.x[0][0];
+            uint8_t *ostage = s.x[0];
             if (!(final_out && P.out_fp4)) {
                 uint8_t *srow = ostage + h * (kHalf * 2);
                 const size_t part = ((size_t)r * P.n_split + u.split) * kHeads;
