@@ -25,7 +25,7 @@
 //
 // Warps: one resolves the records and fetches their lines into L2; eight unpack
 // them, exactly (see csa_format_t), from global memory into the MMA's layout in
-// two buffers of a block, the next 64 candidates' bytes in registers meanwhile;
+// two buffers of a block, the next block's bytes in registers meanwhile;
 // one issues the MMAs, QK(i + 1) before PV(i); eight do the softmax and the
 // epilogue, two threads a head.
 //
@@ -208,7 +208,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 
 // Bounded wait of a whole warp: true when the phase is complete for every lane,
 // and what the other CTA stored before it arrived is visible. One (suspending)
-// try is in line, the rest out of it: see above on code size.
+// try is in line, the rest out of it (in line at every wait, the roles' loops take
+// more of the instruction cache: 203 us instead of 198 for the longest calls).
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, limit_ns) && try_wait_cluster(bar, parity)) != 0;
 }
