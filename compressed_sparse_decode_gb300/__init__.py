@@ -498,6 +498,11 @@ def _arg(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
     return t.data_ptr()
 
 
+def _codes(t: torch.Tensor, name: str, shape, dev: int) -> int:
+    """_arg for E4M3 codes, as bytes or as torch's type."""
+    return _arg(t, name, torch.float8_e4m3fn if t.dtype == torch.float8_e4m3fn else torch.uint8, shape, dev)
+
+
 def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
     """Data pointer of a floating tensor of this shape whose rows (the last
     dimension) are dense; the other strides are the caller's to pass on."""
@@ -534,6 +539,8 @@ def _attention_outputs(B: int, T: int, device, stream, out, lse, fp4_out: bool, 
             out_fp4 = _new(torch.empty, (B, T, HEADS, DIM // 2), torch.uint8, device, stream)
         if out_fp4_scale is None:
             out_fp4_scale = _new(torch.empty, (B, T, HEADS, DIM // SCALE_BLOCK), torch.float32, device, stream)
+        if out_fp4.device != device or out_fp4_scale.device != device:
+            raise ValueError(f"out_fp4 and out_fp4_scale must be on {device}")
     elif out is None:
         out = _new(torch.empty, (B, T, HEADS, DIM), torch.bfloat16, device, stream)
     if lse is None:
@@ -610,9 +617,8 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
         ncap = k_idx.shape[1]
         if key.dtype != x.dtype:
             raise ValueError(f"key must have the type of x: got {key.dtype} and {x.dtype}")
-        k_dtype = torch.float8_e4m3fn if k_idx.dtype == torch.float8_e4m3fn else torch.uint8
         idx = csa_index_append(_rows(key, "key", (B, T, IDX_DIM), dev), *_strides(key),
-                               _arg(k_idx, "k_idx", k_dtype, (B, ncap, IDX_DIM), dev),
+                               _codes(k_idx, "k_idx", (B, ncap, IDX_DIM), dev),
                                _arg(k_idx_scale, "k_idx_scale", torch.float32, (B, ncap), dev), ncap)
     rope_dim, theta = (0, 0.0) if rope_theta is None else (ROPE, rope_theta)
     _check((_lib or load()).csa_cache_append(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0, _rows(x, "x", (B, T, DIM), dev),
@@ -707,11 +713,11 @@ def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, 
     epi, out_fp4, out_fp4_scale = _epilogue(B, T, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
     if ws is None:
         ws = _own_workspace(OP_DECODE_STEP, B, T, Ncap, k, q.device, stream)
-    u8, i32, f32 = (torch.uint8, torch.float8_e4m3fn), torch.int32, torch.float32
+    i32, f32 = torch.int32, torch.float32
     _check((_lib or load()).csa_decode_step_fp4(
-        _ptr(q_idx, "q_idx", u8, (B, T, IDX_HEADS, IDX_DIM)),
+        _codes(q_idx, "q_idx", (B, T, IDX_HEADS, IDX_DIM), dev),
         _arg(q_idx_scale, "q_idx_scale", f32, (B, T, IDX_HEADS), dev), _arg(w_idx, "w_idx", f32, (B, T, IDX_HEADS), dev),
-        _ptr(k_idx, "k_idx", u8, (B, Ncap, IDX_DIM)), _arg(k_idx_scale, "k_idx_scale", f32, (B, Ncap), dev),
+        _codes(k_idx, "k_idx", (B, Ncap, IDX_DIM), dev), _arg(k_idx_scale, "k_idx_scale", f32, (B, Ncap), dev),
         _arg(q, "q", torch.bfloat16, (B, T, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
         _format(_cache(comp, B, dev), FORMAT_FP4, "csa_decode_step_fp4"),
         _arg(swa_ring, "swa_ring", torch.uint8, (B, R, FP4_RECORD_BYTES), dev), R, W,
