@@ -29,9 +29,9 @@
 // one issues the MMAs, QK(i + 1) before PV(i); eight do the softmax and the
 // epilogue, two threads a head.
 //
-// Measured: 32 queries of 2176 candidates 44.6 us (409 TFLOP/s, 0.22 of the cuBLAS
+// Measured: 32 queries of 2176 candidates 44.3 us (412 TFLOP/s, 0.22 of the cuBLAS
 // rate; FP8 records: 57), 64 queries of 8320 candidates 198 us (703 TFLOP/s, 0.38;
-// FP8 records: 313), 24 ragged queries 21.3 us, one query of 192 candidates 15.3.
+// FP8 records: 313), 24 ragged queries 20.8 us, one query of 192 candidates 14.7.
 // A block takes 5700 cycles, of which the tensor core works a third. What sets the
 // pace is the way of a block through its buffer, two of which are all that fits:
 // unpacking 2 x 950 cycles, QK 1300, the exchange of the partial sums 1700, softmax
@@ -882,6 +882,9 @@ __global__ void __launch_bounds__(256, 3)
 combine_fp4_kernel(const __grid_constant__ Params P) {
     static_assert(kWarps == 1 || kWarps == 8, "one head a warp, or one a block");
     __shared__ float4 sums[kWarps > 1 ? kWarps : 1][kWarps > 1 ? kDim / 4 : 1];
+    // The next kernel of the stream may be set up now (it waits for this one's end
+    // before it touches memory): 0.4 us a call where the next is this attention.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ptx::griddep_wait();
     const int r = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
