@@ -51,6 +51,9 @@ class csa_cache_desc(C.Structure):
     _fields_ = [("base", C.c_void_p), ("n_records", C.c_int64), ("seq_stride", C.c_int64),
                 ("block_table", C.c_void_p), ("page_records", C.c_int32), ("max_pages", C.c_int32),
                 ("seq_capacity", C.c_int32)]
+    # what cache_desc knows of the tensors: format, device, block-table rows, and
+    # whether the records had to be copied
+    _fmt, _dev, _seqs, _copied = FORMAT_FP8, None, None, False
 
 
 class csa_attention_epilogue(C.Structure):
@@ -253,7 +256,7 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
 
 def _format(comp: csa_cache_desc, fmt: int, where: str) -> csa_cache_desc:
     """The description itself, if it describes records of format ``fmt``."""
-    if getattr(comp, "_fmt", FORMAT_FP8) != fmt:
+    if comp._fmt != fmt:
         raise ValueError(f"{where} reads {FORMAT_BYTES[fmt]}-byte records; the cache holds the other format")
     return comp
 
@@ -503,23 +506,19 @@ def _codes(t: torch.Tensor, name: str, shape, dev: int) -> int:
     return _arg(t, name, torch.float8_e4m3fn if t.dtype == torch.float8_e4m3fn else torch.uint8, shape, dev)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dev: int) -> int:
-    """Data pointer of a floating tensor of this shape whose rows (the last
-    dimension) are dense; the other strides are the caller's to pass on."""
-    if t.get_device() != dev or t.dtype not in _DTYPES or t.shape != shape:
-        raise ValueError(f"{name} must be a bf16, fp16 or fp32 tensor of shape {tuple(shape)} on cuda:{dev}: got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be dense")
-    return t.data_ptr()
-
-
-def _strides(t: torch.Tensor):
-    """Strides of the leading dimensions; 0 where a dimension has one element
-    (PyTorch leaves any number there)."""
-    if 1 not in t.shape[:-1]:
-        return t.stride()[:-1]
-    return [s if n != 1 else 0 for n, s in zip(t.shape[:-1], t.stride())]
+def _rows(t: torch.Tensor, name: str, dev: int):
+    """(data pointer, element type, strides of the leading dimensions) of a
+    floating tensor whose last dimension is dense; 0 for a dimension of one
+    element (PyTorch leaves any number there)."""
+    dt = _DTYPES.get(t.dtype)
+    *s, last = t.stride()
+    if dt is None or last != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16, fp16 or fp32 tensor on cuda:{dev} with a dense last dimension: got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()}, on {t.device}")
+    shape = t.shape
+    if 1 in shape:
+        s = [0 if n == 1 else v for n, v in zip(shape, s)]
+    return t.data_ptr(), dt, s
 
 
 def _new(make, shape, dtype, device, stream) -> torch.Tensor:
@@ -570,7 +569,8 @@ def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6
     dev = _dev(x, "x")
     if out is None:
         out = _new(torch.empty, (B, T, H, D), torch.bfloat16, x.device, stream)
-    _check((_lib or load()).csa_head_norm_rope(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+    ptr, dt, s = _rows(x, "x", dev)
+    _check((_lib or load()).csa_head_norm_rope(ptr, dt, *s,
                                      _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                      _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
                                      _arg(out, "out", torch.bfloat16, (B, T, H, D), dev), _own_status(status, dev),
@@ -588,7 +588,8 @@ def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float =
         codes = _new(torch.empty, (B, T, H, D), torch.uint8, x.device, stream)
     if scale is None:
         scale = _new(torch.empty, (B, T, H), torch.float32, x.device, stream)
-    _check((_lib or load()).csa_head_norm_rope_e4m3(_rows(x, "x", x.shape, dev), _DTYPES[x.dtype], *_strides(x),
+    ptr, dt, s = _rows(x, "x", dev)
+    _check((_lib or load()).csa_head_norm_rope_e4m3(ptr, dt, *s,
                                           _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                           _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
                                           _arg(codes, "codes", torch.uint8, (B, T, H, D), dev),
@@ -606,27 +607,30 @@ def csa_cache_append(cache: csa_cache_desc, x, first, count=None, ring: bool = F
     (``rope_theta=None``: not rotated) on the way. ``ring``: entry modulo the
     cache's capacity. ``key`` [B, T, 128] adds the entries' indexer keys to
     ``k_idx`` [B, Ncap, 128] and ``k_idx_scale`` [B, Ncap]. See include/csa.h."""
-    B, T, _ = x.shape
+    B, T, D = x.shape
     dev = _dev(x, "x")
-    if getattr(cache, "_copied", False):
+    if D != DIM:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, T, {DIM}]")
+    if cache._copied:
         raise ValueError("the cache's records were not contiguous: the description holds a copy of them")
+    ptr, dt, s = _rows(x, "x", dev)
     idx = None
     if (key is None) != (k_idx is None) or (key is None) != (k_idx_scale is None):
         raise ValueError("key, k_idx and k_idx_scale go together")
     if key is not None:
         ncap = k_idx.shape[1]
-        if key.dtype != x.dtype:
-            raise ValueError(f"key must have the type of x: got {key.dtype} and {x.dtype}")
-        idx = csa_index_append(_rows(key, "key", (B, T, IDX_DIM), dev), *_strides(key),
-                               _codes(k_idx, "k_idx", (B, ncap, IDX_DIM), dev),
+        if key.shape != (B, T, IDX_DIM) or key.dtype != x.dtype:
+            raise ValueError(f"key must be a {x.dtype} tensor of shape {(B, T, IDX_DIM)}: got {key.dtype} "
+                             f"{tuple(key.shape)}")
+        key_ptr, _, key_s = _rows(key, "key", dev)
+        idx = csa_index_append(key_ptr, *key_s, _codes(k_idx, "k_idx", (B, ncap, IDX_DIM), dev),
                                _arg(k_idx_scale, "k_idx_scale", torch.float32, (B, ncap), dev), ncap)
     rope_dim, theta = (0, 0.0) if rope_theta is None else (ROPE, rope_theta)
-    _check((_lib or load()).csa_cache_append(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0, _rows(x, "x", (B, T, DIM), dev),
-                                   _DTYPES[x.dtype], *_strides(x),
-                                   _arg(first, "first", torch.int32, (B,), dev),
-                                   None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
-                                   pos_stride, _how(norm, weight, eps, rope_dim, theta, DIM, dev),
-                                   idx, _own_status(status, dev), _on(stream, dev)), "csa_cache_append")
+    _check((_lib or load()).csa_cache_append(_cache(cache, B, dev), cache._fmt, 1 if ring else 0, ptr, dt, *s,
+                                             _arg(first, "first", torch.int32, (B,), dev),
+                                             None if count is None else _arg(count, "count", torch.int32, (B,), dev),
+                                             B, T, pos_stride, _how(norm, weight, eps, rope_dim, theta, DIM, dev), idx,
+                                             _own_status(status, dev), _on(stream, dev)), "csa_cache_append")
 
 
 def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = False, out=None, stream=None,
@@ -638,7 +642,7 @@ def csa_cache_read(cache: csa_cache_desc, first, count, T: int, ring: bool = Fal
     B = first.shape[0]
     if out is None:
         out = _new(torch.zeros, (B, T, DIM), torch.bfloat16, first.device, stream)
-    _check((_lib or load()).csa_cache_read(_cache(cache, B, dev), _fmt_of(cache), 1 if ring else 0,
+    _check((_lib or load()).csa_cache_read(_cache(cache, B, dev), cache._fmt, 1 if ring else 0,
                                  _arg(first, "first", torch.int32, (B,), dev),
                                  None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T,
                                  _arg(out, "out", torch.bfloat16, (B, T, DIM), dev), _own_status(status, dev),
@@ -738,16 +742,11 @@ def _ws(ws, dev: int):
 def _cache(cache: csa_cache_desc, B: int, dev: int) -> csa_cache_desc:
     """The description itself, if its records lie on device ``dev`` and its block
     table has a row for each of the B sequences."""
-    if getattr(cache, "_dev", dev) != dev:
+    if cache._dev is not None and cache._dev != dev:
         raise ValueError(f"the cache is on cuda:{cache._dev}, not on cuda:{dev}")
-    seqs = getattr(cache, "_seqs", None)
-    if seqs is not None and seqs < B:
-        raise ValueError(f"the cache's block table has {seqs} rows for {B} sequences")
+    if cache._seqs is not None and cache._seqs < B:
+        raise ValueError(f"the cache's block table has {cache._seqs} rows for {B} sequences")
     return cache
-
-
-def _fmt_of(cache: csa_cache_desc) -> int:
-    return getattr(cache, "_fmt", FORMAT_FP8)
 
 
 def _hptr(t: torch.Tensor, name: str, dtype, shape):
