@@ -177,7 +177,7 @@ append_kernel(const __grid_constant__ AppendParams P) {
             float sum = two.x + two.y;
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            const float inv_rms = rsqrtf(sum * (1.f / kDim) + P.ops.eps);
+            const float inv_rms = inverse_rms(sum, 1.f / kDim, P.ops.eps);
             scale_octet(f[0], inv_rms, w[0]);
             scale_octet(f[1], inv_rms, w[1]);
         }

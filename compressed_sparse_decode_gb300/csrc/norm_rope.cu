@@ -102,7 +102,7 @@ norm_rope_kernel(const __grid_constant__ NormRopeParams P) {
             float sum = two.x + two.y;
 #pragma unroll
             for (int o = G / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv_rms = rsqrtf(sum * inv_d + P.ops.eps);
+            const float inv_rms = inverse_rms(sum, inv_d, P.ops.eps);
 #pragma unroll
             for (int v = 0; v < NV; ++v) scale_octet(f[v], inv_rms, w[v]);
         }

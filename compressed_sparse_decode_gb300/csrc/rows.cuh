@@ -211,7 +211,7 @@ __device__ __forceinline__ void e4m3_quotients(const float (&f)[8], uint32_t ama
     if (amax > 0x7149F2CAu) up = 8.673617379884035e-19f;    // above 1e30: 2^-60
     const float t = amax ? __uint_as_float(amax) * up : 448.f, inv = __frcp_rn(t);
     const float2 k = make_float2(448.f * up, 448.f * up), ii = make_float2(inv, inv), tt = make_float2(-t, -t);
-    const float2 quick = make_float2(448.f * inv, 448.f * inv);
+    const float2 quick = make_float2(quotient(448.f, t, inv), quotient(448.f, t, inv));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         float2 x = make_float2(f[2 * e], f[2 * e + 1]);
@@ -248,6 +248,16 @@ __device__ __forceinline__ void load_weights(float (&w)[8], const float *weight,
     const float4 a = __ldg(reinterpret_cast<const float4 *>(weight + at));
     const float4 b = __ldg(reinterpret_cast<const float4 *>(weight + at) + 1);
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+}
+
+// (mean + eps)^(-1/2) with a Newton step (the function's 2 ulp would be half of a
+// normalised value's error, which decides E4M3 codes): e = 1 - a r^2, with what
+// a r loses kept. Where a r^2 has no value (a zero or infinite) r stays.
+__device__ __forceinline__ float inverse_rms(float sum, float inv_d, float eps) {
+    const float a = fmaf(sum, inv_d, eps), r = rsqrtf(a);
+    const float p = a * r, lost = fmaf(a, r, -p);
+    const float e = fmaf(-lost, r, fmaf(-p, r, 1.f));
+    return fabsf(e) < 1e-3f ? fmaf(0.5f * r, e, r) : r;
 }
 
 // y_d = x_d * inv_rms * w_d for one octet.
