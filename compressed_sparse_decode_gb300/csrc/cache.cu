@@ -8,9 +8,9 @@
 // maximum needs no shuffle, and a record is written with one vector store a lane.
 //
 // Appending is bound by instructions: 8 x up to 8192 tokens, normalised, into FP8
-// records with indexer keys took 500 instructions a token, 69 % of the issue slots,
+// records with indexer keys take 500 instructions a token, 68 % of the issue slots,
 // 32 us (98 MB: 0.45 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
-// records 16 us; one token of 32 sequences 2.5 us, a launch. Reading 8 x up to 8192
+// records 15 us; one token of 32 sequences 2.5 us, a launch. Reading 8 x up to 8192
 // FP8 records back: 79 MB in 17.9 us, 0.65 of the copy rate.
 #include <cuda_fp4.h>
 
@@ -118,10 +118,11 @@ __device__ __forceinline__ int fp4_exponent(uint32_t amax) {
     return amax ? max(e, kFp4MinExponent) : 0;
 }
 
-// (Six blocks an SM: 80 registers. With blocks of twice the size, two an SM, an
-// FP8 prompt of 49k tokens with keys took 36 us instead of 31.)
+// (Six blocks an SM, 80 registers: with blocks of twice the size, two an SM, an FP8
+// prompt of up to 64k tokens with keys took 36 us instead of 32. FP32 input, whose
+// loads are twice as long: seven; 16 x 1001 tokens 19 us with them, with five 20.6.)
 template <int DT, int FMT, bool KEYS, bool NORM>
-__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 5 : 6)
+__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 7 : 6)
 append_kernel(const __grid_constant__ AppendParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
