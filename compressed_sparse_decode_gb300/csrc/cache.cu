@@ -8,8 +8,8 @@
 // maximum needs no shuffle, and a record is written with one vector store a lane.
 //
 // Appending is bound by instructions: 8 x up to 8192 tokens, normalised, into FP8
-// records with indexer keys take 500 instructions a token, 68 % of the issue slots,
-// 32 us (98 MB: 0.45 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
+// records with indexer keys take 480 instructions a token, two thirds of the issue
+// slots, 31 us (98 MB: 0.46 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
 // records 15 us; one token of 32 sequences 2.5 us, a launch. Reading 8 x up to 8192
 // FP8 records back: 79 MB in 17.9 us, 0.65 of the copy rate.
 #include <cuda_fp4.h>
@@ -129,135 +129,148 @@ append_kernel(const __grid_constant__ AppendParams P) {
     const int t0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * P.per_warp;
     if (t0 >= P.span.B * P.span.T) return;
     const Slot mine = find_slots(P.span, t0, P.per_warp, lane, P.err);
-    const bool key_lane = KEYS && lane < kIdxDim / 8;  // 16 lanes hold the key's octets
+    // The indexer keys of two tokens at once, 16 lanes each (one at a time: 4 % more):
+    // lane hl of a half holds octet hl of the key of token j + half (j even).
+    const int half = lane >> 4, hl = lane & 15;
     const bool turn = P.ops.rope_dim > 0;
-    __shared__ __align__(16) float2 warp_cs[kWarps][32];  // of the warp's current token
-    float2 *pair_cs = warp_cs[threadIdx.x >> 5];
+    __shared__ __align__(16) float2 warp_cs[kWarps][2][32];  // of the warp's current two tokens
+    float2(*pair_cs)[32] = warp_cs[threadIdx.x >> 5];
     const uint64_t pair_turn = turn ? P.ops.turn[lane] : 0;
     float w[2][8];  // the norm's weights of this lane's dims
     load_weights(w[0], NORM ? P.ops.weight : nullptr, 16 * lane);
     load_weights(w[1], NORM ? P.ops.weight : nullptr, 16 * lane + 8);
     struct {
-        Octet<DT> x[2], key;
+        Octet<DT> x[2];
         int64_t record;
-        int b;
     } now, next;
+    Octet<DT> key, next_key;
+    int key_b = 0, next_key_b = 0;
     int nb = t0 / P.span.T, nt = t0 - nb * P.span.T;  // the token to fetch
     auto fetch = [&](int j, auto &o) {
         const int b = nb, t = nt;
         if (++nt == P.span.T) nt = 0, ++nb;
-        o.b = b;
+        if (KEYS && !(j & 1)) {
+            next_key_b = half ? nb : b;
+            if (__shfl_sync(kAll, mine.record, j + half) >= 0)
+                next_key.load(P.key, next_key_b * P.key_seq_stride + (half ? nt : t) * P.key_token_stride + 8 * hl);
+        }
         o.record = __shfl_sync(kAll, mine.record, j);
         if (o.record < 0) return;
         const int64_t at = b * P.seq_stride + t * P.token_stride + 16 * lane;
         o.x[0].load(P.x, at);
         o.x[1].load(P.x, at + 8);
-        if (key_lane) o.key.load(P.key, b * P.key_seq_stride + t * P.key_token_stride + 8 * lane);
     };
     fetch(0, next);
 #pragma unroll 1
     for (int j = 0; j < P.per_warp; ++j) {
         now = next;
+        if (KEYS && !(j & 1)) {
+            key = next_key;
+            key_b = next_key_b;
+        }
         if (j + 1 < P.per_warp) fetch(j + 1, next);
-        if (now.record < 0) continue;
-        const int b = now.b;
-        const int64_t entry = __shfl_sync(kAll, mine.entry, j);
-        if (turn) {
-            __syncwarp();
-            pair_cs[lane] = turn_cos_sin(entry * P.pos_stride, pair_turn);
-            __syncwarp();
-        }
+        if (now.record >= 0) {
+            if (turn) {
+                const int64_t entry = __shfl_sync(kAll, mine.entry, j);
+                __syncwarp();
+                pair_cs[j & 1][lane] = turn_cos_sin(entry * P.pos_stride, pair_turn);
+                __syncwarp();
+            }
 
-        float f[2][8];
-        now.x[0].floats(f[0]);
-        now.x[1].floats(f[1]);
-        if (NORM) {
-            float2 two = make_float2(0.f, 0.f);
-            square_octet(f[0], two);
-            square_octet(f[1], two);
-            float sum = two.x + two.y;
+            float f[2][8];
+            now.x[0].floats(f[0]);
+            now.x[1].floats(f[1]);
+            if (NORM) {
+                float2 two = make_float2(0.f, 0.f);
+                square_octet(f[0], two);
+                square_octet(f[1], two);
+                float sum = two.x + two.y;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-            const float inv_rms = inverse_rms(sum, 1.f / kDim, P.ops.eps);
-            scale_octet(f[0], inv_rms, w[0]);
-            scale_octet(f[1], inv_rms, w[1]);
-        }
-        const bool rope_lane = lane >= kNopeLanes;
-        if (turn) {
-            if (rope_lane) {
-                turn_octet(f[0], *reinterpret_cast<const float2(*)[4]>(pair_cs + 8 * (lane - kNopeLanes)));
-                turn_octet(f[1], *reinterpret_cast<const float2(*)[4]>(pair_cs + 8 * (lane - kNopeLanes) + 4));
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+                const float inv_rms = inverse_rms(sum, 1.f / kDim, P.ops.eps);
+                scale_octet(f[0], inv_rms, w[0]);
+                scale_octet(f[1], inv_rms, w[1]);
             }
-        }
-        const uint32_t amax = rope_lane ? 0u : amax_bits(amax_octet(f[1], amax_octet(f[0])));
-        uint8_t *rec = P.base + now.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
-        if (FMT == CSA_FORMAT_FP4) {
-            const uint32_t top = __reduce_max_sync(kAll, amax);
-            const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
-            const int E = bad ? 128 : fp4_exponent(top);
-            if (rope_lane) {
-                uint4 *dst = reinterpret_cast<uint4 *>(rec + kFp4RopeOffset + 32 * (lane - kNopeLanes));
-                dst[0] = pack_bf16_octet(f[0]);
-                dst[1] = pack_bf16_octet(f[1]);
-                if (lane == kNopeLanes)
-                    *reinterpret_cast<uint32_t *>(rec + kFp4PowerOffset) = (uint32_t)(E + 127);
-            } else {
-                // block scale: e4m3(amax / 6 * 2^-E), its halfway cases decided exactly
-                const float ratio = sticky_quotient(__uint_as_float(amax), 6.f, 1.f / 6.f) *
-                                    __uint_as_float((uint32_t)(127 - E) << 23);
-                const uint32_t sb = bad ? 0u : e4m3x4(ratio, 0.f, 0.f, 0.f) & 0xFFu;
-                uint2 codes = make_uint2(0u, 0u);
-                if (sb) {
-                    float unit = e4m3x2_to_float2((uint16_t)sb).x * __uint_as_float((uint32_t)(E + 127) << 23);
-                    if (E < -60) {
-                        constexpr float kUp = 18446744073709551616.f;
-                        unit *= kUp;
+            const bool rope_lane = lane >= kNopeLanes;
+            if (turn && rope_lane) {
+                const float2 *cs = pair_cs[j & 1] + 8 * (lane - kNopeLanes);
+                turn_octet(f[0], *reinterpret_cast<const float2(*)[4]>(cs));
+                turn_octet(f[1], *reinterpret_cast<const float2(*)[4]>(cs + 4));
+            }
+            const uint32_t amax = rope_lane ? 0u : amax_bits(amax_octet(f[1], amax_octet(f[0])));
+            uint8_t *rec = P.base + now.record * (FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes);
+            if (FMT == CSA_FORMAT_FP4) {
+                const uint32_t top = __reduce_max_sync(kAll, amax);
+                const bool bad = top >= 0x7F800000u;  // an infinity or NaN: the whole record reads as NaN
+                const int E = bad ? 128 : fp4_exponent(top);
+                if (rope_lane) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(rec + kFp4RopeOffset + 32 * (lane - kNopeLanes));
+                    dst[0] = pack_bf16_octet(f[0]);
+                    dst[1] = pack_bf16_octet(f[1]);
+                    if (lane == kNopeLanes)
+                        *reinterpret_cast<uint32_t *>(rec + kFp4PowerOffset) = (uint32_t)(E + 127);
+                } else {
+                    // block scale: e4m3(amax / 6 * 2^-E), its halfway cases decided exactly
+                    const float ratio = sticky_quotient(__uint_as_float(amax), 6.f, 1.f / 6.f) *
+                                        __uint_as_float((uint32_t)(127 - E) << 23);
+                    const uint32_t sb = bad ? 0u : e4m3x4(ratio, 0.f, 0.f, 0.f) & 0xFFu;
+                    uint2 codes = make_uint2(0u, 0u);
+                    if (sb) {
+                        float unit = e4m3x2_to_float2((uint16_t)sb).x * __uint_as_float((uint32_t)(E + 127) << 23);
+                        if (E < -60) {
+                            constexpr float kUp = 18446744073709551616.f;
+                            unit *= kUp;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) f[0][e] *= kUp, f[1][e] *= kUp;
+                            for (int e = 0; e < 8; ++e) f[0][e] *= kUp, f[1][e] *= kUp;
+                        }
+                        codes = fp4_codes<DT == CSA_FP32 || NORM>(f, unit);
                     }
-                    codes = fp4_codes<DT == CSA_FP32 || NORM>(f, unit);
+                    *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
+                    rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
                 }
-                *reinterpret_cast<uint2 *>(rec + 8 * lane) = codes;
-                rec[kFp4ScaleOffset + lane] = (uint8_t)sb;
-            }
-        } else {
-            uint32_t top = amax;  // over the eight lanes of a 128-dim block (rope lanes hold 0)
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
-            if (rope_lane) {
-                uint4 *dst = reinterpret_cast<uint4 *>(rec + kRopeOffset + 32 * (lane - kNopeLanes));
-                dst[0] = pack_bf16_octet(f[0]);
-                dst[1] = pack_bf16_octet(f[1]);
             } else {
-                const float s = e4m3_scale(top);
-                float q[2][8];
-                e4m3_quotients<DT != CSA_FP32 && !NORM>(f[0], top, q[0]);
-                e4m3_quotients<DT != CSA_FP32 && !NORM>(f[1], top, q[1]);
-                *reinterpret_cast<uint4 *>(rec + 16 * lane) =
-                    make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
+                uint32_t top = amax;  // over the eight lanes of a 128-dim block (rope lanes hold 0)
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+                if (rope_lane) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(rec + kRopeOffset + 32 * (lane - kNopeLanes));
+                    dst[0] = pack_bf16_octet(f[0]);
+                    dst[1] = pack_bf16_octet(f[1]);
+                } else {
+                    const float s = e4m3_scale(top);
+                    float q[2][8];
+                    e4m3_quotients<DT != CSA_FP32 && !NORM>(f[0], top, q[0]);
+                    e4m3_quotients<DT != CSA_FP32 && !NORM>(f[1], top, q[1]);
+                    *reinterpret_cast<uint4 *>(rec + 16 * lane) =
+                        make_uint4(e4m3x4(q[0][0], q[0][1], q[0][2], q[0][3]), e4m3x4(q[0][4], q[0][5], q[0][6], q[0][7]),
                                e4m3x4(q[1][0], q[1][1], q[1][2], q[1][3]), e4m3x4(q[1][4], q[1][5], q[1][6], q[1][7]));
-                if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + kScaleOffset + 4 * (lane >> 3)) = s;
+                    if ((lane & 7) == 0) *reinterpret_cast<float *>(rec + kScaleOffset + 4 * (lane >> 3)) = s;
+                }
             }
         }
-        if (KEYS) {
+        if (KEYS && ((j & 1) || j + 1 == P.per_warp)) {
+            const int from = (j & ~1) + half;
+            const bool live = __shfl_sync(kAll, mine.record, from) >= 0;
+            const int64_t entry = __shfl_sync(kAll, mine.entry, from);
             float g[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[e] = 0.f;
-            if (key_lane) now.key.floats(g);
-            if (turn) {
-                // octets 8..15 are the key's rope dims: pairs 4 (lane - 8) ..
-                if (key_lane && lane >= 8) turn_octet(g, *reinterpret_cast<const float2(*)[4]>(pair_cs + 4 * (lane - 8)));
-            }
-            const uint32_t top = __reduce_max_sync(kAll, amax_bits(amax_octet(g)));
-            if (entry >= P.idx_cap) {
-                if (lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
-            } else if (key_lane) {
+            if (live) key.floats(g);
+            // octets 8..15 are the key's rope dims: pairs 4 (hl - 8) ..
+            if (turn && live && hl >= 8)
+                turn_octet(g, *reinterpret_cast<const float2(*)[4]>(pair_cs[half] + 4 * (hl - 8)));
+            uint32_t top = amax_bits(amax_octet(g));
+#pragma unroll
+            for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+            if (live && entry >= P.idx_cap) {
+                if (hl == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+            } else if (live) {
                 const float s = e4m3_scale(top);
-                const int64_t row = (int64_t)b * P.idx_cap + entry;
+                const int64_t row = (int64_t)key_b * P.idx_cap + entry;
                 e4m3_quotients<DT != CSA_FP32>(g, top, g);
-                *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * lane) =
+                *reinterpret_cast<uint2 *>(P.k_idx + row * kIdxDim + 8 * hl) =
                     make_uint2(e4m3x4(g[0], g[1], g[2], g[3]), e4m3x4(g[4], g[5], g[6], g[7]));
-                if (lane == 0) P.k_idx_scale[row] = s;
+                if (hl == 0) P.k_idx_scale[row] = s;
             }
         }
     }
