@@ -20,7 +20,6 @@ cudaError_t launch_topk(const float *, const int32_t *, const int32_t *, int, in
                         int32_t *, void *, size_t, cudaStream_t);
 cudaError_t launch_gather(const csa_cache_desc &, const void *, int, int, const int32_t *, const int32_t *,
                           const int32_t *, int, int, int, void *, int32_t *, int *, cudaStream_t);
-size_t attention_workspace_bytes(int B, int T, int max_selected, int W);
 cudaError_t launch_attention(const void *, const float *, float, const csa_cache_desc &, const void *, int, int,
                              const int32_t *, const int32_t *, const int32_t *, int, const int32_t *, int, int, int,
                              bool, void *, float *, const csa_attention_epilogue *, void *, size_t, int *,
@@ -129,6 +128,15 @@ csa_status_t attention_arg_status(const void *q, const float *sink, float softma
     return CSA_OK;
 }
 
+namespace {
+// Logits, selection, top-k scratch and the attention's scratch of a step.
+size_t decode_step_bytes(int B, int T, int Ncap, int k, size_t attention_bytes) {
+    return align_up(sizeof(float) * (size_t)B * T * Ncap, kWsAlign) +
+           2 * align_up(sizeof(int32_t) * (size_t)B * T * k, kWsAlign) +
+           align_up(topk_workspace_bytes(B, T, Ncap, k), kWsAlign) + align_up(attention_bytes, kWsAlign);
+}
+}  // namespace
+
 // The host-side checks of csa_indexer_logits, csa_topk and
 // csa_sink_attention_decode for the arguments csa_decode_step passes them, so
 // that a bad argument is reported before any of the three launches.
@@ -137,7 +145,8 @@ csa_status_t decode_step_arg_status(const uint8_t *q_idx, const float *q_idx_sca
                                     float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R,
                                     int W, const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap,
                                     int m, int k, const void *out, const float *lse, const int32_t *topk_idx,
-                                    const void *workspace, size_t workspace_bytes, const int32_t *status) {
+                                    const void *workspace, size_t workspace_bytes,
+                                    size_t (*attention_bytes)(int, int, int, int), const int32_t *status) {
     if (!valid_dims(B, T) || Ncap < 1 || k < 1 || m < 1) return CSA_ERR_INVALID_ARG;
     if (!valid_status_word(status)) return CSA_ERR_INVALID_ARG;
     if (!q_idx || !q_idx_scale || !w_idx || !k_idx || !k_idx_scale || !q || !sink || !swa_ring || !q_pos ||
@@ -150,7 +159,7 @@ csa_status_t decode_step_arg_status(const uint8_t *q_idx, const float *q_idx_sca
     if (W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || !(softmax_scale > 0.f)) return CSA_ERR_INVALID_ARG;
     if (k > Ncap || k > CSA_MAX_TOPK) return CSA_ERR_UNSUPPORTED;
     if ((int64_t)B * Ncap >= ((int64_t)1 << 31)) return CSA_ERR_UNSUPPORTED;
-    const size_t need = csa_workspace_bytes(CSA_OP_DECODE_STEP, B, T, Ncap, k);
+    const size_t need = decode_step_bytes(B, T, Ncap, k, attention_bytes(B, T, k, CSA_MAX_SWA_WINDOW));
     if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign))
         return CSA_ERR_WORKSPACE;
     return CSA_OK;
@@ -192,10 +201,7 @@ size_t csa_workspace_bytes(csa_op_t op, int B, int T, int Ncap, int k) {
     case CSA_OP_ATTENTION: return either_format_bytes(B, T, k);
     case CSA_OP_HCA_ATTENTION: return either_format_bytes(B, T, Ncap);
     case CSA_OP_DECODE_STEP:
-        return align_up(sizeof(float) * (size_t)B * T * Ncap, kWsAlign) +
-               2 * align_up(sizeof(int32_t) * (size_t)B * T * k, kWsAlign) +
-               align_up(topk_workspace_bytes(B, T, Ncap, k), kWsAlign) +
-               align_up(either_format_bytes(B, T, k), kWsAlign);
+        return decode_step_bytes(B, T, Ncap, k, either_format_bytes(B, T, k));
     }
     return 0;
 }
@@ -374,7 +380,7 @@ csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, co
     if (a != CSA_OK) return a;
     a = csa::decode_step_arg_status(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                                     swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, checked_out(epilogue, out), lse,
-                                    topk_idx, workspace, workspace_bytes, status);
+                                    topk_idx, workspace, workspace_bytes, kernel.workspace_bytes, status);
     if (a != CSA_OK) return a;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *logits = reinterpret_cast<float *>(ws);
@@ -386,7 +392,8 @@ csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, co
     const size_t tk_bytes = align_up(topk_workspace_bytes(B, T, Ncap, k), kWsAlign);
     void *tk_ws = tk_bytes ? ws : nullptr;
     ws += tk_bytes;
-    const size_t at_bytes = align_up(either_format_bytes(B, T, k), kWsAlign);
+    // (this format's own need: csa_workspace_bytes gives what either asks for)
+    const size_t at_bytes = align_up(kernel.workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW), kWsAlign);
     csa_status_t s = csa_indexer_logits(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q_pos, n_comp, B, T, Ncap, m,
                                         logits, status, stream);
     if (s != CSA_OK) return s;

@@ -43,13 +43,17 @@ csa_status_t attention_arg_status(const void *q, const float *sink, float softma
 // and the dynamic shared-memory opt-in of a kernel, set once per device.
 int cached_sm_count();
 cudaError_t set_max_dynamic_smem_once(const void *kernel, int bytes);
-// Every host-side check csa_decode_step makes, before any launch.
+// Workspace of the attention over FP8 records.
+size_t attention_workspace_bytes(int B, int T, int max_selected, int W);
+// Every host-side check csa_decode_step makes, before any launch. The workspace
+// has to hold attention_bytes(B, T, k, CSA_MAX_SWA_WINDOW) for its attention.
 csa_status_t decode_step_arg_status(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
                                     const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
                                     float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R,
                                     int W, const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap,
                                     int m, int k, const void *out, const float *lse, const int32_t *topk_idx,
-                                    const void *workspace, size_t workspace_bytes, const int32_t *status);
+                                    const void *workspace, size_t workspace_bytes,
+                                    size_t (*attention_bytes)(int, int, int, int), const int32_t *status);
 
 // Records a code in the caller's status word (device memory); the first
 // error since the word was last cleared wins. No word: nothing is recorded.

@@ -142,7 +142,7 @@ csa_status_t csa_decode_step_host(csa_pipeline_t p, const uint8_t *h_q_idx, cons
     const csa_status_t a =
         csa::decode_step_arg_status(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                                     swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, nullptr, workspace,
-                                    workspace_bytes, status);
+                                    workspace_bytes, csa::attention_workspace_bytes, status);
     if (a != CSA_OK) return a;
 
     // host -> device, once step (i - depth) has finished reading this slot
