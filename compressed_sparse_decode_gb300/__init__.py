@@ -224,7 +224,8 @@ def _status(status, device) -> int:
 def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
                block_table: torch.Tensor | None = None, page_records: int = 0,
                fmt: int = FORMAT_FP8) -> csa_cache_desc:
-    """Describe a cache of latent records: ``records`` is uint8 [n, 592] (or
+    """Describe a cache of latent records: ``records`` is uint8 [n, 592], or of
+    another number of dimensions and whole records in all (a flat buffer,
     [B, Ncap, 592]); contiguous mode uses ``seq_stride``, paged mode a
     ``block_table`` [B, max_pages] int32 and ``page_records``. With
     ``fmt=FORMAT_FP4`` the records are the 384-byte 4-bit ones; the calls below
@@ -232,7 +233,8 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
     if fmt not in (FORMAT_FP8, FORMAT_FP4):
         raise ValueError(f"unknown record format {fmt}")
     size = FORMAT_BYTES[fmt]
-    if records.shape[-1] != size:
+    last = records.shape[-1] if records.dim() > 1 else size  # (a flat buffer says nothing about its records)
+    if records.numel() % size or (last != size and (records.dim() == 2 or last in FORMAT_BYTES)):
         raise ValueError(f"records must be [n, {size}] uint8")
     rec = records.reshape(-1, size) if records.dim() != 2 else records
     _ptr(rec, "records", torch.uint8)

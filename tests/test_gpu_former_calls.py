@@ -49,3 +49,21 @@ def test_fp8_step_takes_a_workspace_for_fp8_records_alone(cuda_lib, wl):
         step(buf[:n - 1])
     assert e.value.status == csd.ERR_WORKSPACE
     assert csd.csa_read_device_error() == 0
+
+
+def test_flat_buffer_of_fp8_records(cuda_lib):
+    """A cache described by its bytes, by [B, pages, bytes of a page] and by [n, 592]
+    is one cache."""
+    csd = cuda_lib
+    x = synth.generate("csa_b1_ctx1k_k64", seed=4, device="cuda")
+    wl = x.wl
+    idx = torch.arange(wl.k, dtype=torch.int32, device="cuda").view(1, 1, wl.k)
+    cnt = torch.full((1, 1), wl.k, dtype=torch.int32, device="cuda")
+
+    def out(records):
+        comp = csd.cache_desc(records, wl.ncap, x.seq_stride)
+        return csd.csa_sink_attention_decode(x.q, x.sink, SCALE, comp, x.ring, wl.W, idx, cnt, x.q_pos)[0]
+
+    want = out(x.comp)
+    for records in (x.comp.reshape(-1), x.comp.reshape(1, -1, 32 * 592)):
+        assert torch.equal(out(records).view(torch.int16), want.view(torch.int16))
