@@ -245,6 +245,8 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
     d.seq_capacity = int(seq_capacity)
     if block_table is not None:
         _ptr(block_table, "block_table", torch.int32)
+        if block_table.get_device() != rec.get_device():
+            raise ValueError(f"block_table is on cuda:{block_table.get_device()}, the records on cuda:{rec.get_device()}")
         d.block_table = block_table.data_ptr()
         d.page_records = int(page_records)
         d.max_pages = int(block_table.shape[-1])

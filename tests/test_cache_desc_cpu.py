@@ -14,6 +14,11 @@ class OnGpu(torch.Tensor):
         return 0
 
 
+class OnSecondGpu(OnGpu):
+    def get_device(self):
+        return 1
+
+
 def on_gpu(shape, dtype=torch.uint8, cls=OnGpu):
     return torch.zeros(shape, dtype=dtype).as_subclass(cls)
 
@@ -34,3 +39,15 @@ def test_records_of_a_wrong_size(fmt):
     for shape in ((24, other), (37, 24, other), (24, 2 * size), (12, 2 * size), (24 * size + 16,), (2, 3, size + 1)):
         with pytest.raises(ValueError, match=str(size)):
             csd.cache_desc(on_gpu(shape), 12, seq_stride=12, fmt=fmt)
+
+
+@pytest.mark.parametrize("fmt", [csd.FORMAT_FP8, csd.FORMAT_FP4])
+def test_block_table_on_another_gpu_than_the_records(fmt):
+    """The kernels read both on one device: a table elsewhere is never described."""
+    rec = on_gpu((24, csd.FORMAT_BYTES[fmt]))
+    for records, cls in ((rec, OnSecondGpu), (rec.as_subclass(OnSecondGpu), OnGpu)):
+        table = on_gpu((2, 3), torch.int32, cls)
+        with pytest.raises(ValueError, match="block_table is on cuda"):
+            csd.cache_desc(records, 12, block_table=table, page_records=4, fmt=fmt)
+    d = csd.cache_desc(rec, 12, block_table=on_gpu((2, 3), torch.int32), page_records=4, fmt=fmt)
+    assert (d.max_pages, d._seqs, d._dev) == (3, 2, 0)
