@@ -34,7 +34,9 @@ inline bool finite_above(float v, float lo) { return std::isfinite(v) && v > lo;
 
 // Host side: the checks of csa_norm_rope for rows of D values, and its
 // parameters. turn = theta^(-2i/rope_dim) / (2 pi) * 2^64 (below 2^62, so it
-// fits).
+// fits), to the nearest whole number: in long double, since a double's own 53 bits
+// would leave the 64-bit fraction wrong by hundreds of units (2^-56 of a turn a
+// position, 0.009 radians at position 2^47).
 inline bool make_row_ops(const csa_norm_rope *how, int D, RowOps *o) {
     if (!how) return false;
     o->norm = how->norm ? 1 : 0;
@@ -47,23 +49,32 @@ inline bool make_row_ops(const csa_norm_rope *how, int D, RowOps *o) {
     if (how->rope_dim < 0 || how->rope_dim % 8 || how->rope_dim > D || how->rope_dim > 2 * kMaxRopePairs) return false;
     const int pairs = how->rope_dim / 2;
     if (pairs && !finite_above(how->rope_theta, 1.f)) return false;
-    // the table of the last (theta, rope_dim) of this thread: 32 pow calls cost
-    // more than the rest of a call
+    if (!pairs) return true;
+    // the tables of this thread's last four (theta, rope_dim), since a model's layers
+    // may take turns with theirs (a pow of 113 bits for each pair of a table made in
+    // every call took 47 us; its ratio alone, and products, 2 us)
     struct Cached {
         float theta;
         int rope_dim;
         uint64_t turn[kMaxRopePairs];
     };
-    static thread_local Cached c = {0.f, 0, {0}};
-    if (pairs && (c.theta != how->rope_theta || c.rope_dim != how->rope_dim)) {
-        for (int i = 0; i < pairs; ++i) {
-            const double f = std::pow((double)how->rope_theta, -2.0 * i / how->rope_dim);
-            c.turn[i] = (uint64_t)std::ldexp(f / 6.283185307179586476925287, 64);
-        }
+    constexpr int kTables = 4;
+    static thread_local Cached tables[kTables] = {};
+    static thread_local int oldest = 0;
+    int at = 0;
+    while (at < kTables && (tables[at].theta != how->rope_theta || tables[at].rope_dim != how->rope_dim)) ++at;
+    if (at == kTables) {
+        at = oldest;
+        oldest = (oldest + 1) % kTables;
+        Cached &c = tables[at];
+        const long double two_pi = 8 * std::atan(1.0L);
+        const long double ratio = std::pow((long double)how->rope_theta, -2.0L / how->rope_dim);
+        long double f = std::ldexp(1 / two_pi, 64);
+        for (int i = 0; i < pairs; ++i, f *= ratio) c.turn[i] = (uint64_t)(f + 0.5L);
         c.theta = how->rope_theta;
         c.rope_dim = how->rope_dim;
     }
-    for (int i = 0; i < pairs; ++i) o->turn[i] = c.turn[i];
+    for (int i = 0; i < pairs; ++i) o->turn[i] = tables[at].turn[i];
     return true;
 }
 
