@@ -584,8 +584,8 @@ def csa_head_norm_rope(x, pos, weight=None, norm: bool = True, eps: float = 1e-6
 
 def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float = 1e-6, rope_dim: int = ROPE,
                             rope_theta: float = 10000.0, codes=None, scale=None, stream=None, status=None):
-    """csa_head_norm_rope with E4M3 output: (codes [B, T, H, D] uint8, scale
-    [B, T, H] fp32), the form csa_indexer_logits reads its queries in."""
+    """csa_head_norm_rope with E4M3 output: (codes [B, T, H, D] uint8, or
+    float8_e4m3fn where ``codes`` is; scale [B, T, H] fp32), the form csa_indexer_logits reads its queries in."""
     B, T, H, D = x.shape
     dev = _dev(x, "x")
     if codes is None:
@@ -596,7 +596,7 @@ def csa_head_norm_rope_e4m3(x, pos, weight=None, norm: bool = True, eps: float =
     _check((_lib or load()).csa_head_norm_rope_e4m3(ptr, dt, *s,
                                           _arg(pos, "pos", torch.int32, (B, T), dev), B, T, H, D,
                                           _how(norm, weight, eps, rope_dim, rope_theta, D, dev),
-                                          _arg(codes, "codes", torch.uint8, (B, T, H, D), dev),
+                                          _codes(codes, "codes", (B, T, H, D), dev),
                                           _arg(scale, "scale", torch.float32, (B, T, H), dev),
                                           _own_status(status, dev), _on(stream, dev)), "csa_head_norm_rope_e4m3")
     return codes, scale
