@@ -118,11 +118,14 @@ __device__ __forceinline__ int fp4_exponent(uint32_t amax) {
     return amax ? max(e, kFp4MinExponent) : 0;
 }
 
-// (Six blocks an SM, 80 registers: with blocks of twice the size, two an SM, an FP8
-// prompt of up to 64k tokens with keys took 36 us instead of 32. FP32 input, whose
-// loads are twice as long: seven; 16 x 1001 tokens 19 us with them, with five 20.6.)
+// Six blocks an SM, 80 registers (with blocks of twice the size, two an SM, an FP8
+// prompt of up to 64k tokens with keys took 36 us when six took 32). FP32 input, whose
+// loads are twice as long, takes seven, 72 registers: 16 x 1001 ragged tokens into 4-bit
+// records with keys, and back, 19 us, with five 20.6; 8 x 8192 normalised ones into FP8
+// records 32.3, with six 34.0. But with the norm and keys together seven spill: the
+// 8 x 8192 tokens 56 us, with six 49.7, into 4-bit records 64 and 58.
 template <int DT, int FMT, bool KEYS, bool NORM>
-__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 ? 7 : 6)
+__global__ void __launch_bounds__(kThreads, DT == CSA_FP32 && !(NORM && KEYS) ? 7 : 6)
 append_kernel(const __grid_constant__ AppendParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
