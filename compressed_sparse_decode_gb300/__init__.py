@@ -202,7 +202,9 @@ _status_ptrs: dict[int, int] = {}  # their addresses (the words live as long as 
 def status_word(device=None) -> torch.Tensor:
     """The binding's default status word for a device: one int32 in device
     memory (created zeroed on first use), passed to the library by every call
-    below that is not given its own ``status`` tensor."""
+    below that is not given its own ``status`` tensor. Make it, by this call or any
+    other, before the first capture of a graph: made inside one, it is zeroed by every
+    replay, not at once."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())

@@ -23,6 +23,11 @@
 // old reference while the maxima travel, and the next block's partial sums travel
 // while PV runs.
 //
+// The weights are BF16 because the latents are: an MMA takes both operands in one
+// type, and FP16 would not hold every latent. Their sum adds the unrounded ones, so
+// the log-sum is free of that rounding; the output's error against 64 bits is 0.0019
+// (its norm over the output's), of which its own BF16 is 0.0017.
+//
 // Warps: one resolves the records and fetches their lines into L2; eight unpack
 // them, exactly (see csa_format_t), from global memory into the MMA's layout in
 // two buffers of a block, the next block's bytes in registers meanwhile;

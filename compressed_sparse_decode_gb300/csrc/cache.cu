@@ -9,9 +9,9 @@
 //
 // Appending is bound by instructions: 8 x up to 8192 tokens, normalised, into FP8
 // records with indexer keys take 480 instructions a token, two thirds of the issue
-// slots, 31 us (98 MB: 0.46 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
+// slots, 31 us (97 MB: 0.46 of the measured copy rate); 16 x 1001 FP32 tokens into 4-bit
 // records 15 us; one token of 32 sequences 2.5 us, a launch. Reading 8 x up to 8192
-// FP8 records back: 79 MB in 17.9 us, 0.65 of the copy rate.
+// FP8 records back: 77 MB in 18.0 us, 0.63 of the copy rate.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -95,7 +95,8 @@ struct AppendParams {
 // 16 values of a nope lane as E2M1 codes of unit s = sb * 2^E (4 significant
 // bits). A quotient of a 16-bit input is a halfway point of the codes or 2^-12 of
 // it away, so rounding it to fp32 decides nothing; other values need the sticky
-// bit. (Tiny units: all times 2^64, so that the remainders stay normal numbers.)
+// bit. (s is at least 2^-69 and the values of its size: the caller has multiplied
+// tiny ones by 2^64, so that the remainders stay normal numbers.)
 template <bool kSticky>
 __device__ __forceinline__ uint2 fp4_codes(const float (&f)[2][8], float s) {
     uint32_t w[2];

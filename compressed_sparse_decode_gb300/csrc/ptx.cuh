@@ -315,8 +315,11 @@ __device__ __forceinline__ void cp_async_16_hint(void *smem_dst, const void *gsr
 // serialisation may be set up while its predecessor in the stream finishes;
 // griddep_wait() returns once every prerequisite grid has completed and its
 // memory operations are visible, so it precedes the first read of a
-// predecessor's output. (No early trigger is issued: releasing dependents
-// before a grid's end let them take SMs early and slowed the end-to-end step.)
+// predecessor's output. combine_fp4_kernel alone triggers its dependents early
+// (griddepcontrol.launch_dependents); elsewhere releasing them before the grid's end
+// let them take SMs early and slowed the end-to-end step. So every kernel launched
+// with that attribute waits here before it reads or writes anything that work before
+// it in the stream may use (a prefetch into L2 of an input may come earlier).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Closes this thread's current group of cp.async copies.

@@ -184,8 +184,11 @@ __device__ __forceinline__ float amax_octet(const float (&f)[8], float m = 0.f) 
 // As bits, whose order is that of the magnitudes, with NaN above them all.
 __device__ __forceinline__ uint32_t amax_bits(float amax) { return __float_as_uint(amax) & 0x7FFFFFFFu; }
 
-// x / s correctly rounded, given inv = 1 / s (rounded): one Newton step on the
-// quotient. s is in the middle of the range (see fp4_codes).
+// x / s to one of the two floats around it (itself if it is one), given inv = 1 / s
+// rounded: the quotient's residual r = x - q s, exact in an FMA, corrects it (P. W.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", IBM J. Res. Dev. 34, 1990). s is in the middle of the range (see
+// fp4_codes).
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
     const float q = x * inv;
     return fmaf(fmaf(-q, s, x), inv, q);
@@ -212,9 +215,11 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax) {
 // 448 f / amax for the E4M3 codes of an octet. With a Newton step (kExact) a quotient
 // that is a halfway point of the codes comes out as that, and for values with up to
 // 21 bits (448 f is exact) every other on its own side of it, so the codes of 16-bit
-// inputs are those of the exact quotients; values that carry a rounding already go
-// without. (All times a power of two where a product or remainder would leave the
-// range.)
+// inputs are those of the exact quotients. Others go without: values that a norm has
+// rounded already, and fp32 inputs as they are, whose 448 f would round too. Their
+// quotient is within two roundings, 2^-23, of the exact one, so that a value that
+// near to a halfway point, where either code is half a step off, may take either.
+// (All times a power of two where a product or remainder would leave the range.)
 template <bool kExact>
 __device__ __forceinline__ void e4m3_quotients(const float (&f)[8], uint32_t amax, float (&q)[8]) {
     float up = 1.f;
