@@ -141,6 +141,16 @@ __device__ __forceinline__ Unit make_unit(const Params &P) {
     return u;
 }
 
+// The larger magnitude, NaN if one is (a plain maximum would drop it).
+__device__ __forceinline__ float max_magnitude(float m, float v) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(v)));
+    return m;
+}
+
+// E2M1 multiplier of values of this largest magnitude: 1 when all are zero, NaN when
+// one is (E2M1 has no code for it).
+__device__ __forceinline__ float e2m1_scale(float amax) { return amax == 0.f ? 1.f : amax / 6.f; }
+
 // A factor for values of this magnitude so that the reciprocal of their E2M1
 // multiplier stays in range.
 __device__ __forceinline__ float upscale(float amax) { return amax < 7.9e-31f ? 1.2676506002282294e30f : 1.f; }
@@ -825,9 +835,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                         float v[32];
                         piece_values(4 * bl + pp, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) amax = fmaxf(amax, fabsf(v[e]));
+                        for (int e = 0; e < 32; ++e) amax = max_magnitude(amax, v[e]);
                     }
-                    const float sc = amax > 0.f ? amax / 6.f : 1.f;
+                    const float sc = e2m1_scale(amax);
                     const float up = upscale(amax), inv = 1.f / (sc * up);
                     auto q = [&](float x) { return x * up * inv; };
 #pragma unroll 1
@@ -1011,10 +1021,10 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(acc[e][i]));
+            for (int i = 0; i < 8; ++i) amax = max_magnitude(amax, acc[e][i]);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float sc = amax > 0.f ? amax / 6.f : 1.f;
+        for (int o = 1; o < 8; o <<= 1) amax = max_magnitude(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float sc = e2m1_scale(amax);
         const float up = upscale(amax), inv_sc = 1.f / (sc * up);
         auto q = [&](float x) { return x * up * inv_sc; };
         uint32_t w[2];

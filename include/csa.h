@@ -458,7 +458,8 @@ CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_t fmt, int 
  * CSA_FP4_RECORD_BYTES bytes (swa_ring [B,R,384]). The latents enter the tensor
  * cores without a rounding; the softmax weights are rounded to BF16, and the
  * partial outputs of a query that is split over several CTAs to FP16 in units of
- * a power of two for each 32 dims. lse of a query without candidates is the sink. */
+ * a power of two for each 32 dims. lse of a query without candidates is the sink.
+ * With E2M1 output, a block of 128 output dims with a NaN has a NaN multiplier. */
 CSA_API csa_status_t csa_sink_attention_decode_fp4(const void *q, const float *sink, float softmax_scale,
                                                    csa_cache_desc comp, const void *swa_ring, int R, int W,
                                                    const int32_t *topk_idx, const int32_t *topk_cnt,

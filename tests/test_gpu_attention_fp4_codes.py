@@ -55,3 +55,27 @@ def test_codes_are_the_nearest(cuda_lib, B, T, cap, n):
         assert np.array_equal(lse.cpu().numpy(), lse2.cpu().numpy())
         check_codes(e2m1, out, f"{B} x {T} rows of {n} {kw}")
     assert csd.csa_read_device_error() == 0
+
+
+@pytest.mark.parametrize("B,n", [(1, 700), (24, 200), (90, 60)])  # eight warps a head, one, and no splits
+def test_a_nan_of_the_output_is_not_hidden_by_its_codes(cuda_lib, B, n):
+    """E2M1 has no NaN: the multiplier of a block of 128 dims that holds one is NaN."""
+    csd = cuda_lib
+    c = Case(csd, B, 1, n + 20, paged=False, seed=81)
+    idx, cnt = c.select(n, [[n]] * B)
+    (codes, scale), lse = c.csa(idx, cnt, fp4_out=True)
+    assert np.all(np.isfinite(scale.cpu().numpy()))
+    bad = B // 2
+    at = bad * (n + 20) + int(idx[bad, 0, n // 2])
+    c.pool[at, 224 + 2 * 9:224 + 2 * 9 + 2] = 255  # rope dim 9 of one selected record
+    (codes2, scale2), _ = c.csa(idx, cnt, fp4_out=True)
+    assert np.all(np.isnan(scale2[bad].cpu().numpy()))  # the score is NaN, so is the whole row
+    rest = [b for b in range(B) if b != bad]
+    assert np.array_equal(scale2[rest].cpu().numpy(), scale[rest].cpu().numpy())
+    assert np.array_equal(codes2[rest].cpu().numpy(), codes[rest].cpu().numpy())
+    c.pool[at, 224 + 2 * 9:224 + 2 * 9 + 2] = 0
+    c.q[bad, 0, 77, 300] = float("nan")  # one head of the query
+    _, s = c.csa(idx, cnt, fp4_out=True)[0]
+    nan = np.isnan(s.cpu().numpy())
+    assert np.all(nan[bad, 0, 77]) and nan.sum() == 4
+    assert csd.csa_read_device_error() == 0
