@@ -231,7 +231,9 @@ def cache_desc(records: torch.Tensor, seq_capacity: int, seq_stride: int = 0,
     [B, Ncap, 592]); contiguous mode uses ``seq_stride``, paged mode a
     ``block_table`` [B, max_pages] int32 and ``page_records``. With
     ``fmt=FORMAT_FP4`` the records are the 384-byte 4-bit ones; the calls below
-    take the format from the description."""
+    take the format from the description. Records that are not contiguous are
+    described by a copy, as they are now: nothing can be appended to it, and what is
+    written to the tensor later is not in it."""
     if fmt not in (FORMAT_FP8, FORMAT_FP4):
         raise ValueError(f"unknown record format {fmt}")
     size = FORMAT_BYTES[fmt]
