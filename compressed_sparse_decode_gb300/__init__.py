@@ -28,6 +28,7 @@ FORMAT_FP8, FORMAT_FP4 = range(2)
 FP4_RECORD_BYTES = 384
 FORMAT_BYTES = (RECORD_BYTES, FP4_RECORD_BYTES)
 OP_INDEXER, OP_TOPK, OP_ATTENTION, OP_HCA_ATTENTION, OP_DECODE_STEP = range(5)
+OP_TREE_ATTENTION, OP_HCA_TREE_ATTENTION, OP_TREE_STEP, OP_VERIFY = range(5, 9)
 
 EXPORTED = ["csa_workspace_bytes", "csa_indexer_logits", "csa_topk", "csa_gather_swa",
             "csa_sink_attention_decode", "hca_sink_attention_decode", "csa_decode_step",
@@ -37,7 +38,9 @@ EXPORTED = ["csa_workspace_bytes", "csa_indexer_logits", "csa_topk", "csa_gather
             "csa_decode_step_host", "csa_pipeline_wait", "csa_pipeline_sync", "csa_pipeline_destroy",
             "csa_sink_attention_decode_ex", "hca_sink_attention_decode_ex", "csa_decode_step_ex",
             "csa_head_norm_rope", "csa_head_norm_rope_e4m3", "csa_cache_append", "csa_cache_read",
-            "csa_sink_attention_decode_fp4", "hca_sink_attention_decode_fp4", "csa_decode_step_fp4"]
+            "csa_sink_attention_decode_fp4", "hca_sink_attention_decode_fp4", "csa_decode_step_fp4",
+            "csa_tree_attention_decode", "hca_tree_attention_decode", "csa_tree_decode_step", "csa_verify_drafts",
+            "csa_cache_commit"]
 PIPELINE_MAX_DEPTH = 4
 
 
@@ -69,6 +72,10 @@ class csa_norm_rope(C.Structure):
 class csa_index_append(C.Structure):
     _fields_ = [("key", C.c_void_p), ("seq_stride", C.c_int64), ("token_stride", C.c_int64), ("k_idx", C.c_void_p),
                 ("k_idx_scale", C.c_void_p), ("Ncap", C.c_int32)]
+
+
+class csa_draft_tree(C.Structure):
+    _fields_ = [("records", C.c_void_p), ("parent", C.c_void_p)]
 
 
 _lib = None
@@ -153,6 +160,20 @@ def load(path: str | None = None):
         for name in ("csa_sink_attention_decode", "hca_sink_attention_decode", "csa_decode_step"):
             fp4, ex = getattr(lib, name + "_fp4"), getattr(lib, name + "_ex")
             fp4.argtypes, fp4.restype = ex.argtypes, st
+        TR = C.POINTER(csa_draft_tree)
+        lib.csa_tree_attention_decode.argtypes = ([P, P, f32, csa_cache_desc, i32, P, i32, i32, TR, P, P, P, i32, i32,
+                                                   i32, P, P, EP, P, sz, P, P])
+        lib.csa_tree_attention_decode.restype = st
+        lib.hca_tree_attention_decode.argtypes = ([P, P, f32, csa_cache_desc, i32, P, P, i32, i32, TR, P, i32, i32,
+                                                   i32, P, P, EP, P, sz, P, P])
+        lib.hca_tree_attention_decode.restype = st
+        lib.csa_tree_decode_step.argtypes = ([P] * 7 + [f32, csa_cache_desc, i32, P, i32, i32, TR, P, P] + [i32] * 5
+                                             + [P, P, P, P, EP, P, sz, P, P])
+        lib.csa_tree_decode_step.restype = st
+        lib.csa_verify_drafts.argtypes = [P, i32, i64, i64, P, i32] + [P] * 5 + [i32] * 3 + [P] * 4 + [sz, P, P]
+        lib.csa_verify_drafts.restype = st
+        lib.csa_cache_commit.argtypes = [csa_cache_desc, i32, i32, P, i32, P, P, P, i32, i32, P, P]
+        lib.csa_cache_commit.restype = st
         _lib = lib
         return lib
 
@@ -740,6 +761,157 @@ def csa_decode_step_fp4(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, 
         None if topk_cnt is None else _arg(topk_cnt, "topk_cnt", i32, (B, T), dev),
         epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)), "csa_decode_step_fp4")
     return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def _tree(draft, parent, comp: csa_cache_desc, swa_ring, B: int, N: int, dev: int):
+    """(the tree's struct, pointer of the ring, its length): records of the cache's format."""
+    size = FORMAT_BYTES[comp._fmt]
+    R = swa_ring.shape[1]
+    ring = _arg(swa_ring, "swa_ring", torch.uint8, (B, R, size), dev)
+    return csa_draft_tree(_arg(draft, "draft", torch.uint8, (B, N, size), dev),
+                          _arg(parent, "parent", torch.int32, (B, N), dev)), ring, R
+
+
+def csa_tree_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_desc, swa_ring, W: int, draft, parent,
+                              topk_idx, topk_cnt, q_pos, out=None, lse=None, ws=None, stream=None, status=None,
+                              inverse_rope: bool = False, rope_theta: float = 10000.0, fp4_out: bool = False,
+                              out_fp4=None, out_fp4_scale=None):
+    """csa_sink_attention_decode for a tree of N drafted tokens a sequence (q [B, N, 128, 512]): token i follows
+    token ``parent[b, i]`` < i (-1: the last committed token) and attends, beside its selected entries, to itself, to
+    its ancestors among ``draft`` [B, N, record bytes] and to the committed tokens of its window in ``swa_ring``.
+    ``comp``, ring and drafts hold records of the cache's format, FP8 or 4-bit. Tokens with q_pos < 0 are padding:
+    their rows are left as they were (pass outputs of your own). Returns (out, lse); with fp4_out,
+    ((out_fp4, out_fp4_scale), lse)."""
+    B, N, k = topk_idx.shape
+    dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, N, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
+    epi, out_fp4, out_fp4_scale = _epilogue(B, N, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if ws is None:
+        ws = _own_workspace(OP_TREE_ATTENTION, B, N, comp.seq_capacity, k, q.device, stream)
+    tree, ring, R = _tree(draft, parent, comp, swa_ring, B, N, dev)
+    i32, f32 = torch.int32, torch.float32
+    _check((_lib or load()).csa_tree_attention_decode(
+        _arg(q, "q", torch.bfloat16, (B, N, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _cache(comp, B, dev), comp._fmt, ring, R, W, tree, _arg(topk_idx, "topk_idx", i32, (B, N, k), dev),
+        _arg(topk_cnt, "topk_cnt", i32, (B, N), dev), _arg(q_pos, "q_pos", i32, (B, N), dev), B, N, k,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, N, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, N, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)),
+        "csa_tree_attention_decode")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def hca_tree_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_desc, n_comp, swa_ring, W: int, draft,
+                              parent, q_pos, m_hca: int = 128, out=None, lse=None, ws=None, stream=None, status=None,
+                              inverse_rope: bool = False, rope_theta: float = 10000.0, fp4_out: bool = False,
+                              out_fp4=None, out_fp4_scale=None):
+    """csa_tree_attention_decode over every visible entry instead of a selection (hca_sink_attention_decode for a
+    tree)."""
+    B, N = q_pos.shape
+    dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, N, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
+    epi, out_fp4, out_fp4_scale = _epilogue(B, N, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if ws is None:
+        ws = _own_workspace(OP_HCA_TREE_ATTENTION, B, N, comp.seq_capacity, 0, q.device, stream)
+    tree, ring, R = _tree(draft, parent, comp, swa_ring, B, N, dev)
+    i32, f32 = torch.int32, torch.float32
+    _check((_lib or load()).hca_tree_attention_decode(
+        _arg(q, "q", torch.bfloat16, (B, N, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _cache(comp, B, dev), comp._fmt, _arg(n_comp, "n_comp", i32, (B,), dev), ring, R, W, tree,
+        _arg(q_pos, "q_pos", i32, (B, N), dev), B, N, m_hca,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, N, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, N, HEADS), dev), epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)),
+        "hca_tree_attention_decode")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def csa_tree_decode_step(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale: float,
+                         comp: csa_cache_desc, swa_ring, W: int, draft, parent, q_pos, n_comp, m: int, k: int,
+                         out=None, lse=None, topk_idx=None, topk_cnt=None, ws=None, stream=None, status=None,
+                         inverse_rope: bool = False, rope_theta: float = 10000.0, fp4_out: bool = False, out_fp4=None,
+                         out_fp4_scale=None):
+    """csa_decode_step for a tree of drafted tokens: indexer and top-k for every token of the tree at its own
+    position, then csa_tree_attention_decode."""
+    B, N = q_pos.shape
+    Ncap = k_idx.shape[1]
+    dev = _dev(q, "q")
+    out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, N, q.device, stream, out, lse, fp4_out, out_fp4,
+                                                          out_fp4_scale)
+    epi, out_fp4, out_fp4_scale = _epilogue(B, N, q.device, inverse_rope, rope_theta, fp4_out, out_fp4, out_fp4_scale)
+    if ws is None:
+        ws = _own_workspace(OP_TREE_STEP, B, N, Ncap, k, q.device, stream)
+    tree, ring, R = _tree(draft, parent, comp, swa_ring, B, N, dev)
+    i32, f32 = torch.int32, torch.float32
+    _check((_lib or load()).csa_tree_decode_step(
+        _codes(q_idx, "q_idx", (B, N, IDX_HEADS, IDX_DIM), dev),
+        _arg(q_idx_scale, "q_idx_scale", f32, (B, N, IDX_HEADS), dev), _arg(w_idx, "w_idx", f32, (B, N, IDX_HEADS), dev),
+        _codes(k_idx, "k_idx", (B, Ncap, IDX_DIM), dev), _arg(k_idx_scale, "k_idx_scale", f32, (B, Ncap), dev),
+        _arg(q, "q", torch.bfloat16, (B, N, HEADS, DIM), dev), _arg(sink, "sink", f32, (HEADS,), dev), softmax_scale,
+        _cache(comp, B, dev), comp._fmt, ring, R, W, tree, _arg(q_pos, "q_pos", i32, (B, N), dev),
+        _arg(n_comp, "n_comp", i32, (B,), dev), B, N, Ncap, m, k,
+        None if out is None else _arg(out, "out", torch.bfloat16, (B, N, HEADS, DIM), dev),
+        _arg(lse, "lse", f32, (B, N, HEADS), dev),
+        None if topk_idx is None else _arg(topk_idx, "topk_idx", i32, (B, N, k), dev),
+        None if topk_cnt is None else _arg(topk_cnt, "topk_cnt", i32, (B, N), dev),
+        epi, *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)), "csa_tree_decode_step")
+    return ((out_fp4, out_fp4_scale) if fp4_out else out), lse
+
+
+def csa_verify_drafts(logits, tokens, parent, uniform, noise, temperature=None, draft_probs=None, path=None,
+                      accepted=None, next_token=None, ws=None, stream=None, status=None):
+    """Accept a path of the drafted tokens ``tokens`` [B, N] int32 of a tree (token 0 is the newest known one, the
+    others follow ``parent``) against the target's ``logits`` [B, N, V] (bf16, fp16 or fp32; any strides but a dense
+    last dimension), and draw the token that follows it. ``draft_probs`` [B, N, V]: row i is the distribution that the
+    children of token i were drawn from; without it drafts are accepted as fixed guesses. ``uniform`` [B, N] fp32 in
+    [0, 1), ``noise`` [B, V] fp32 of exponential variates, ``temperature`` [B] fp32 (0: greedy). Returns (path [B, N]
+    int32: the accepted tokens' numbers and -1 behind them, accepted [B], next_token [B])."""
+    B, N, V = logits.shape
+    dev = _dev(logits, "logits")
+    i32, f32 = torch.int32, torch.float32
+    if path is None:
+        path = _new(torch.empty, (B, N), i32, logits.device, stream)
+    if accepted is None:
+        accepted = _new(torch.empty, (B,), i32, logits.device, stream)
+    if next_token is None:
+        next_token = _new(torch.empty, (B,), i32, logits.device, stream)
+    if ws is None:
+        ws = _own_workspace(OP_VERIFY, B, N, V, 0, logits.device, stream)
+    ptr, dt, s = _rows(logits, "logits", dev)
+    q, q_dt = None, 0
+    if draft_probs is not None:
+        q_dt = _DTYPES.get(draft_probs.dtype)
+        if q_dt is None:
+            raise ValueError(f"draft_probs must be a bf16, fp16 or fp32 tensor: got {draft_probs.dtype}")
+        q = _arg(draft_probs, "draft_probs", draft_probs.dtype, (B, N, V), dev)
+    _check((_lib or load()).csa_verify_drafts(
+        ptr, dt, *s, q, q_dt, _arg(tokens, "tokens", i32, (B, N), dev), _arg(parent, "parent", i32, (B, N), dev),
+        _arg(uniform, "uniform", f32, (B, N), dev), _arg(noise, "noise", f32, (B, V), dev),
+        None if temperature is None else _arg(temperature, "temperature", f32, (B,), dev), B, N, V,
+        _arg(path, "path", i32, (B, N), dev), _arg(accepted, "accepted", i32, (B,), dev),
+        _arg(next_token, "next_token", i32, (B,), dev), *_ws(ws, dev), _own_status(status, dev), _on(stream, dev)),
+        "csa_verify_drafts")
+    return path, accepted, next_token
+
+
+def csa_cache_commit(cache: csa_cache_desc, records, select, count, first, ring: bool = False, stream=None,
+                     status=None) -> None:
+    """Put record ``select[b, t]`` of ``records`` [B, N, record bytes] (of the cache's format) into the cache as entry
+    ``first[b] + t`` of sequence b, for t < ``count[b]``, byte for byte: after csa_verify_drafts, ``select`` and
+    ``count`` are its path and its accepted. ``select`` None: record t; ``count`` None: all of them. ``ring``: entry
+    modulo the cache's capacity. ``records`` must not be part of the cache."""
+    B, N, size = records.shape
+    dev = _dev(records, "records")
+    if cache._copied:
+        raise ValueError("the cache's records were not contiguous: the description holds a copy of them")
+    T = N if select is None else select.shape[1]
+    _check((_lib or load()).csa_cache_commit(
+        _cache(cache, B, dev), cache._fmt, 1 if ring else 0,
+        _arg(records, "records", torch.uint8, (B, N, FORMAT_BYTES[cache._fmt]), dev), N,
+        None if select is None else _arg(select, "select", torch.int32, (B, T), dev),
+        _arg(first, "first", torch.int32, (B,), dev),
+        None if count is None else _arg(count, "count", torch.int32, (B,), dev), B, T, _own_status(status, dev),
+        _on(stream, dev)), "csa_cache_commit")
 
 
 def _ws(ws, dev: int):

@@ -29,6 +29,12 @@ cudaError_t launch_attention_fp4(const void *, const float *, float, const csa_c
                                  int, bool, void *, float *, const csa_attention_epilogue *, void *, size_t, int *,
                                  cudaStream_t);
 size_t attention_fp4_workspace_bytes(int B, int T, int max_selected, int W);
+cudaError_t launch_tree_attention(const void *, const float *, float, const csa_cache_desc &, csa_format_t,
+                                  const void *, int, int, const csa_draft_tree &, const int32_t *, const int32_t *,
+                                  const int32_t *, int, const int32_t *, int, int, int, bool, void *, float *,
+                                  const csa_attention_epilogue *, void *, size_t, int *, cudaStream_t);
+size_t tree_attention_workspace_bytes(int B, int N, int max_selected, int W);
+size_t verify_workspace_bytes(int B, int N, int V);
 }  // namespace csa
 
 namespace csa {
@@ -202,6 +208,11 @@ size_t csa_workspace_bytes(csa_op_t op, int B, int T, int Ncap, int k) {
     case CSA_OP_HCA_ATTENTION: return either_format_bytes(B, T, Ncap);
     case CSA_OP_DECODE_STEP:
         return decode_step_bytes(B, T, Ncap, k, either_format_bytes(B, T, k));
+    case CSA_OP_TREE_ATTENTION: return tree_attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW);
+    case CSA_OP_HCA_TREE_ATTENTION: return tree_attention_workspace_bytes(B, T, Ncap, CSA_MAX_SWA_WINDOW);
+    case CSA_OP_TREE_STEP:
+        return decode_step_bytes(B, T, Ncap, k, tree_attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW));
+    case CSA_OP_VERIFY: return verify_workspace_bytes(B, T, Ncap);
     }
     return 0;
 }
@@ -290,6 +301,17 @@ csa_status_t sink_attention(const AttentionKernel &kernel, const void *q, const 
                               T, k, false, out, lse, epilogue, workspace, workspace_bytes, status, stream));
 }
 
+csa_status_t hca_arg_status(const void *q, const float *sink, float softmax_scale, const csa_cache_desc &comp,
+                            const int32_t *n_comp, const void *swa_ring, int R, int W, const int32_t *q_pos, int B,
+                            int T, int m_hca, const float *lse, const int32_t *status) {
+    if (!q || !sink || !n_comp || !swa_ring || !q_pos || !lse) return CSA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(swa_ring) || !valid_cache(comp, B) || !valid_status_word(status))
+        return CSA_ERR_INVALID_ARG;
+    if (!valid_dims(B, T) || W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || m_hca < 1 || !(softmax_scale > 0.f))
+        return CSA_ERR_INVALID_ARG;
+    return CSA_OK;
+}
+
 csa_status_t hca_attention(const AttentionKernel &kernel, const void *q, const float *sink, float softmax_scale,
                            const csa_cache_desc &comp, const int32_t *n_comp, const void *swa_ring, int R, int W,
                            const int32_t *q_pos, int B, int T, int m_hca, void *out, float *lse,
@@ -297,11 +319,9 @@ csa_status_t hca_attention(const AttentionKernel &kernel, const void *q, const f
                            int32_t *status, cudaStream_t stream) {
     const csa_status_t a = epilogue_status(epilogue, out);
     if (a != CSA_OK) return a;
-    if (!q || !sink || !n_comp || !swa_ring || !q_pos || !lse) return CSA_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(swa_ring) || !valid_cache(comp, B) || !valid_status_word(status))
-        return CSA_ERR_INVALID_ARG;
-    if (!valid_dims(B, T) || W < 1 || W > CSA_MAX_SWA_WINDOW || R < W || m_hca < 1 || !(softmax_scale > 0.f))
-        return CSA_ERR_INVALID_ARG;
+    const csa_status_t b = hca_arg_status(q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, T, m_hca,
+                                          lse, status);
+    if (b != CSA_OK) return b;
     const size_t need = kernel.workspace_bytes(B, T, comp.seq_capacity, W);
     if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)))
         return CSA_ERR_WORKSPACE;
@@ -367,9 +387,13 @@ csa_status_t hca_sink_attention_decode(const void *q, const float *sink, float s
                                         lse, nullptr, workspace, workspace_bytes, status, stream);
 }
 
+extern "C++" {  // (a template)
 namespace {
-csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
-                         const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
+// The step around an attention: `attention(idx, cnt, workspace, bytes)` is its
+// last call, attention_bytes what that needs.
+template <class Attention>
+csa_status_t decode_step(size_t (*attention_bytes)(int, int, int, int), const Attention &attention,
+                         const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx, const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
                          float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R, int W,
                          const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
                          void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
@@ -380,7 +404,7 @@ csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, co
     if (a != CSA_OK) return a;
     a = csa::decode_step_arg_status(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                                     swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, checked_out(epilogue, out), lse,
-                                    topk_idx, workspace, workspace_bytes, kernel.workspace_bytes, status);
+                                    topk_idx, workspace, workspace_bytes, attention_bytes, status);
     if (a != CSA_OK) return a;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     float *logits = reinterpret_cast<float *>(ws);
@@ -393,14 +417,34 @@ csa_status_t decode_step(const AttentionKernel &kernel, const uint8_t *q_idx, co
     void *tk_ws = tk_bytes ? ws : nullptr;
     ws += tk_bytes;
     // (this format's own need: csa_workspace_bytes gives what either asks for)
-    const size_t at_bytes = align_up(kernel.workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW), kWsAlign);
+    const size_t at_bytes = align_up(attention_bytes(B, T, k, CSA_MAX_SWA_WINDOW), kWsAlign);
     csa_status_t s = csa_indexer_logits(q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q_pos, n_comp, B, T, Ncap, m,
                                         logits, status, stream);
     if (s != CSA_OK) return s;
     s = csa_topk(logits, q_pos, n_comp, B, T, Ncap, m, k, idx, cnt, tk_ws, tk_bytes, status, stream);
     if (s != CSA_OK) return s;
-    return sink_attention(kernel, q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out, lse,
-                          epilogue, at_bytes ? ws : nullptr, at_bytes, status, stream);
+    return attention(idx, cnt, at_bytes ? ws : nullptr, at_bytes);
+}
+}  // namespace
+}
+
+namespace {
+// The step over a format's own attention.
+csa_status_t sink_step(const AttentionKernel &kernel, const uint8_t *q_idx, const float *q_idx_scale,
+                       const float *w_idx, const uint8_t *k_idx, const float *k_idx_scale, const void *q,
+                       const float *sink, float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R,
+                       int W, const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
+                       void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
+                       const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
+                       int32_t *status, cudaStream_t stream) {
+    return decode_step(
+        kernel.workspace_bytes,
+        [&](const int32_t *idx, const int32_t *cnt, void *ws, size_t ws_bytes) {
+            return sink_attention(kernel, q, sink, softmax_scale, comp, swa_ring, R, W, idx, cnt, q_pos, B, T, k, out,
+                                  lse, epilogue, ws, ws_bytes, status, stream);
+        },
+        q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp, swa_ring, R, W, q_pos, n_comp, B,
+        T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue, workspace, workspace_bytes, status, stream);
 }
 }  // namespace
 
@@ -411,7 +455,7 @@ csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, 
                                 void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                 const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                 int32_t *status, cudaStream_t stream) {
-    return decode_step(kFp8Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+    return sink_step(kFp8Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                        swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
                        workspace, workspace_bytes, status, stream);
 }
@@ -423,9 +467,81 @@ csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale,
                                  void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                  const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                  int32_t *status, cudaStream_t stream) {
-    return decode_step(kFp4Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
+    return sink_step(kFp4Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
                        swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
                        workspace, workspace_bytes, status, stream);
+}
+
+namespace {
+// A tree of records of a known format, and a workspace that its attention can use.
+csa_status_t tree_status(const csa_draft_tree *tree, csa_format_t fmt) {
+    if (fmt != CSA_FORMAT_FP8 && fmt != CSA_FORMAT_FP4) return CSA_ERR_INVALID_ARG;
+    if (!tree || !tree->records || !tree->parent || !aligned16(tree->records) || !aligned4(tree->parent))
+        return CSA_ERR_INVALID_ARG;
+    return CSA_OK;
+}
+csa_status_t tree_workspace_status(size_t need, const void *workspace, size_t workspace_bytes) {
+    const bool ok = !need || (workspace && workspace_bytes >= need &&
+                              reinterpret_cast<uintptr_t>(workspace) % kWsAlign == 0);
+    return ok ? CSA_OK : CSA_ERR_WORKSPACE;
+}
+}  // namespace
+
+csa_status_t csa_tree_attention_decode(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
+                                       csa_format_t fmt, const void *swa_ring, int R, int W,
+                                       const csa_draft_tree *tree, const int32_t *topk_idx, const int32_t *topk_cnt,
+                                       const int32_t *q_pos, int B, int N, int k, void *out, float *lse,
+                                       const csa_attention_epilogue *epilogue, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
+    csa_status_t a = epilogue_status(epilogue, out);
+    if (a == CSA_OK) a = tree_status(tree, fmt);
+    if (a == CSA_OK)
+        a = attention_arg_status(q, sink, softmax_scale, comp, swa_ring, R, W, topk_idx, topk_cnt, q_pos, B, N, k,
+                                 checked_out(epilogue, out), lse, status);
+    if (a == CSA_OK) a = tree_workspace_status(tree_attention_workspace_bytes(B, N, k, W), workspace, workspace_bytes);
+    if (a != CSA_OK) return a;
+    return cuda_status(launch_tree_attention(q, sink, softmax_scale, comp, fmt, swa_ring, R, W, *tree, topk_idx,
+                                             topk_cnt, nullptr, 1, q_pos, B, N, k, false, out, lse, epilogue,
+                                             workspace, workspace_bytes, status, stream));
+}
+
+csa_status_t hca_tree_attention_decode(const void *q, const float *sink, float softmax_scale, csa_cache_desc comp,
+                                       csa_format_t fmt, const int32_t *n_comp, const void *swa_ring, int R, int W,
+                                       const csa_draft_tree *tree, const int32_t *q_pos, int B, int N, int m_hca,
+                                       void *out, float *lse, const csa_attention_epilogue *epilogue,
+                                       void *workspace, size_t workspace_bytes, int32_t *status,
+                                       cudaStream_t stream) {
+    csa_status_t a = epilogue_status(epilogue, out);
+    if (a == CSA_OK) a = tree_status(tree, fmt);
+    if (a == CSA_OK)
+        a = hca_arg_status(q, sink, softmax_scale, comp, n_comp, swa_ring, R, W, q_pos, B, N, m_hca, lse, status);
+    if (a == CSA_OK)
+        a = tree_workspace_status(tree_attention_workspace_bytes(B, N, comp.seq_capacity, W), workspace,
+                                  workspace_bytes);
+    if (a != CSA_OK) return a;
+    return cuda_status(launch_tree_attention(q, sink, softmax_scale, comp, fmt, swa_ring, R, W, *tree, nullptr,
+                                             nullptr, n_comp, m_hca, q_pos, B, N, comp.seq_capacity, true, out, lse,
+                                             epilogue, workspace, workspace_bytes, status, stream));
+}
+
+csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                                  const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
+                                  float softmax_scale, csa_cache_desc comp, csa_format_t fmt, const void *swa_ring,
+                                  int R, int W, const csa_draft_tree *tree, const int32_t *q_pos,
+                                  const int32_t *n_comp, int B, int N, int Ncap, int m, int k, void *out, float *lse,
+                                  int32_t *topk_idx, int32_t *topk_cnt, const csa_attention_epilogue *epilogue,
+                                  void *workspace, size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
+    csa_status_t a = epilogue_status(epilogue, out);
+    if (a == CSA_OK) a = tree_status(tree, fmt);
+    if (a != CSA_OK) return a;
+    return decode_step(
+        tree_attention_workspace_bytes,
+        [&](const int32_t *idx, const int32_t *cnt, void *ws, size_t ws_bytes) {
+            return csa_tree_attention_decode(q, sink, softmax_scale, comp, fmt, swa_ring, R, W, tree, idx, cnt, q_pos,
+                                             B, N, k, out, lse, epilogue, ws, ws_bytes, status, stream);
+        },
+        q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp, swa_ring, R, W, q_pos, n_comp, B,
+        N, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue, workspace, workspace_bytes, status, stream);
 }
 
 csa_status_t csa_decode_step(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,

@@ -45,6 +45,7 @@
 // unpacking, took 222 us; more warps for the unpacking, the softmax or the exchange
 // cost registers, and all were slower.)
 #include <cuda_fp4.h>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -84,8 +85,10 @@ struct AttSmem {
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
     uint64_t x_full[2], x_empty[2][2];         // of a buffer; of its chunks
+    uint64_t rest_done[2];                     // of a buffer: the scores have its latents' rests
     uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, part_full, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
+    uint8_t chain[CSA_MAX_TOKENS_PER_SEQ];  // a tree's token and its ancestors, the youngest first
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -109,6 +112,8 @@ struct Params {
     float *out_fp4_scale;
     int inv_rope;
     uint64_t turn[kRope / 2];
+    const uint8_t *draft;   // [B, T] records of a tree's tokens, and their parents (null: no tree)
+    const int32_t *parent;
     int *err;
     uint64_t wait_ns;  // limit of each bounded wait (drains keep kDrainWaitNs)
 };
@@ -245,7 +250,11 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, float2 s) {
 
 // A thread's quarter of a record's own half, as it lies in the record: four units
 // of 16 dims, 64 apart (the last unit of the upper half is 16 rope dims).
-struct Quarter {
+template <int FMT>
+struct Quarter;
+
+template <>
+struct Quarter<CSA_FORMAT_FP4> {
     uint2 code[4];
     uint4 rope[2];
     uint4 scale;  // byte hq of word i: unit i's
@@ -271,6 +280,7 @@ struct Quarter {
         }
     }
     // to column block i of a row at lo / hi (16-byte chunks 2 hq and 2 hq + 1)
+    template <bool REST>
     __device__ __forceinline__ void unpack(int rank, int hq, uint4 *lo, uint4 *hi) const {
         constexpr int kStep = kAtom / 16;
         const float pw = fp4_power(power & 0xFFu);
@@ -289,10 +299,66 @@ struct Quarter {
     }
 };
 
+// 8 E4M3 codes times a multiplier as BF16 (rounded once), or, with `rest`, what that
+// rounding left, as BF16.
+template <bool REST>
+__device__ __forceinline__ uint4 unpack8_e4m3(uint32_t w0, uint32_t w1, float s) {
+    const uint32_t w[2] = {w0, w1};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        const float2 a = __fmul2_rn(e4m3x2_to_float2(two), make_float2(s, s));
+        o[i] = pack_bf16(a.x, a.y);
+        if (REST)
+            o[i] = pack_bf16(a.x - __uint_as_float(o[i] << 16), a.y - __uint_as_float(o[i] & 0xFFFF0000u));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <>
+struct Quarter<CSA_FORMAT_FP8> {
+    uint4 piece[5];  // the units' codes; of the upper half three units', and its rope dims
+    float2 mult;     // multipliers of the half's two 128-dim blocks
+    __device__ __forceinline__ void load(const uint8_t *rec, int rank, int hq) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) piece[i] = make_uint4(0, 0, 0, 0);  // no record: zero latents
+        mult = make_float2(0.f, 0.f);
+        if (!rec) return;
+        const uint4 *own = reinterpret_cast<const uint4 *>(rec + rank * kHalf) + hq;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) piece[i] = __ldcs(own + 4 * i);
+        const uint4 *last = rank == 0 ? own + 12 : reinterpret_cast<const uint4 *>(rec + kRopeOffset) + 2 * hq;
+        piece[3] = __ldcs(last);
+        if (rank == 1) piece[4] = __ldcs(last + 1);
+        mult = __ldcs(reinterpret_cast<const float2 *>(rec + kScaleOffset) + rank);
+    }
+    template <bool REST>
+    __device__ __forceinline__ void unpack(int rank, int hq, uint4 *lo, uint4 *hi) const {
+        constexpr int kStep = kAtom / 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i == 3 && rank == 1) {
+                if (!REST) {  // (rope dims are BF16: no rest)
+                    lo[i * kStep] = piece[3];
+                    hi[i * kStep] = piece[4];
+                }
+                break;
+            }
+            const float s = i < 2 ? mult.x : mult.y;
+            lo[i * kStep] = unpack8_e4m3<REST>(piece[i].x, piece[i].y, s);
+            hi[i * kStep] = unpack8_e4m3<REST>(piece[i].z, piece[i].w, s);
+        }
+    }
+};
+
 // ---------------------------------------------------------------- the kernel
 
+template <int FMT, bool TREE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
+    constexpr int kRecordBytes = FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes;
+    constexpr bool kRests = FMT == CSA_FORMAT_FP8;  // BF16 does not hold the latents
     extern __shared__ uint8_t smem_raw[];
     AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -303,6 +369,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s.x_full[i], 2 * kConvWarps);  // both chunks of a block
             for (int c = 0; c < 2; ++c) ptx::mbar_init(&s.x_empty[i][c], 1);
+            ptx::mbar_init(&s.rest_done[i], 1);
         }
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
@@ -348,6 +415,33 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         // Lane L resolves candidates L, L + 32, .. of a block (own chunk first) in
         // three stages, one block apart, so that no stage waits for the load it
         // started: entry (top-k list), page (block table), record.
+        // Of a tree's window the last `own` positions are its token and the token's
+        // ancestors, found by walking up from it: lane L holds the parents of
+        // tokens L, L + 32, ..
+        int own = 0;
+        if (TREE && u.ce > u.n_sel) {
+            int up[CSA_MAX_TOKENS_PER_SEQ / 32];
+#pragma unroll
+            for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j)
+                up[j] = 32 * j + lane < P.T ? __ldg(P.parent + (int64_t)u.b * P.T + 32 * j + lane) : -1;
+            const int most = min(min(P.W, u.p + 1), P.T);
+#pragma unroll 1
+            for (int node = u.r - u.b * P.T; node >= 0 && own < most; ++own) {
+                if (lane == 0) s.chain[own] = (uint8_t)node;
+                int next = -1;
+#pragma unroll
+                for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j) {
+                    const int v = __shfl_sync(0xffffffffu, up[j], node & 31);
+                    if (node >> 5 == j) next = v;
+                }
+                if (next >= node || next < -1) {  // (a parent comes before its children: the walk ends)
+                    if (rank == 0 && lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+                    next = -1;
+                }
+                node = next;
+            }
+            __syncwarp();
+        }
         auto cand = [&](int i, int e) {
             return u.cb + i * kBlock + (e < 2 ? rank : rank ^ 1) * kChunk + (e & 1) * 32 + lane;
         };
@@ -370,11 +464,13 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             if (c >= u.ce) return nullptr;
             if (c >= u.n_sel) {
                 const int pos = u.j0 + (c - u.n_sel);
-                return P.ring + ((int64_t)u.b * P.R + pos % P.R) * kFp4Bytes;
+                if (TREE && u.p - pos < own)
+                    return P.draft + ((int64_t)u.b * P.T + s.chain[u.p - pos]) * kRecordBytes;
+                return P.ring + ((int64_t)u.b * P.R + pos % P.R) * kRecordBytes;
             }
             const int64_t ri = P.comp.block_table ? (int64_t)page * P.comp.page_records + entry % P.comp.page_records
                                                   : (int64_t)u.b * P.comp.seq_stride + entry;
-            if (page >= 0 && ri < P.comp.n_records) return P.comp.base + ri * kFp4Bytes;
+            if (page >= 0 && ri < P.comp.n_records) return P.comp.base + ri * kRecordBytes;
             if (rank == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
             return nullptr;
         };
@@ -399,7 +495,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 // since a bulk prefetch takes as long as a bulk copy)
                 if (e < 2 && rec) {
 #pragma unroll
-                    for (int b = 0; b < kFp4Bytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + b));
+                    for (int b = 0; b < kRecordBytes; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + b));
+                    // (an FP8 record need not begin with a line: its last one)
+                    if (kRecordBytes % 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + kRecordBytes - 16));
                 }
                 if (e < 2) have[e] = __ballot_sync(0xffffffffu, rec != nullptr);
                 entry[e] = next_entry[e];
@@ -418,17 +516,19 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         // candidate; the bytes of a chunk are under way while the block before it is
         // unpacked.
         const int row = threadIdx.x >> 2, hq = threadIdx.x & 3;
-        Quarter own, other;
-        auto fetch = [&](int i, int chunk, Quarter &q) {
+        Quarter<FMT> own, other;
+        auto fetch = [&](int i, int chunk, Quarter<FMT> &q) {
             q.load(s.rec[i % kPtrRing][chunk * kChunk + row], rank, hq);
         };
-        auto unpack = [&](int i, int chunk, const Quarter &q) {
+        auto unpack = [&](int i, int chunk, const Quarter<FMT> &q, auto rest) {
             const int r = chunk * kChunk + row, b = i & 1;
-            q.unpack(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
+            q.template unpack<decltype(rest)::value>(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
             ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&s.x_full[b]);
         };
+        using Whole = std::integral_constant<bool, false>;
+        using First = std::integral_constant<bool, kRests>;  // what a block's buffer holds first
         bool ok = true;
         if (u.n_blocks > 0) {
             ok = wait(&s.ptr_full[0], 0);
@@ -444,10 +544,16 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ok = !more || wait(&s.ptr_full[n % kPtrRing], n / kPtrRing & 1);
             ok = ok && wait(&s.x_empty[i & 1][0], (i >> 1 & 1) ^ 1);
             if (!ok) break;
-            unpack(i, 0, own);
+            unpack(i, 0, own, First{});
             ok = wait(&s.x_empty[i & 1][1], (i >> 1 & 1) ^ 1);
             if (!ok) break;
-            unpack(i, 1, other);
+            unpack(i, 1, other, First{});
+            if (kRests) {  // the rests are in the scores: the rounded values in their place
+                ok = wait(&s.rest_done[i & 1], i >> 1 & 1);
+                if (!ok) break;
+                unpack(i, 0, own, Whole{});
+                unpack(i, 1, other, Whole{});
+            }
             if (more) {
                 fetch(n, 0, own);
                 fetch(n, 1, other);
@@ -472,15 +578,30 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
             if (i < u.n_blocks) {  // QK(i)
-                ok = wait(&s.x_full[i & 1], i >> 1 & 1) && (i == 0 || wait(&s.s_free, (i & 1) ^ 1));
+                // (a buffer's phases: one a block, or two with rests)
+                ok = wait(&s.x_full[i & 1], kRests ? 0 : i >> 1 & 1) && (i == 0 || wait(&s.s_free, (i & 1) ^ 1));
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.x[i & 1]));
+                auto qk = [&](int k, bool add) {
+                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8,
+                                    xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, add);
+                };
+                if (kRests) {
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < kHalf / 16; ++k)
+                            if (k < 12 || rank == 0) qk(k, k > 0);  // (the last 64 dims of rank 1 are rope)
+                        ptx::mma_commit(&s.rest_done[i & 1]);
+                    }
+                    __syncwarp();
+                    ok = wait(&s.x_full[i & 1], 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                }
                 if (leader) {
 #pragma unroll
-                    for (int k = 0; k < kHalf / 16; ++k)
-                        ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8,
-                                        xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, k > 0);
+                    for (int k = 0; k < kHalf / 16; ++k) qk(k, kRests || k > 0);
                     ptx::mma_commit(&s.s_full);
                 }
                 __syncwarp();
@@ -729,7 +850,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::tc_fence_after();
         }
         // ---------------- epilogue: O half (and LSE) out
-        if (ok) {
+        if (ok && !(TREE && u.p < 0)) {  // (a tree's padding keeps its rows)
             const int r = u.r;
             float factor, lse_out = 0.f;
             const float2 ml = make_float2(m, l);
@@ -902,6 +1023,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ptx::griddep_wait();
     const int r = blockIdx.y;
+    if (P.parent && __ldg(P.q_pos + r) < 0) return;  // a tree's padding keeps its rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x * (8 / kWarps) + warp / kWarps, part = warp % kWarps;
     const size_t row0 = (size_t)r * P.n_split * kHeads + h, row_stride = kHeads;  // of the splits' rows
@@ -1062,12 +1184,16 @@ size_t attention_fp4_workspace_bytes(int B, int T, int max_selected, int W) {
 
 // `k` = the top-k row length (CSA) or the per-sequence capacity (HCA). The
 // workspace holds the splits' partials, their exponents and their (max, sum).
-cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, const csa_cache_desc &comp,
-                                 const void *ring, int R, int W, const int32_t *topk_idx, const int32_t *topk_cnt,
-                                 const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
-                                 void *out, float *lse, const csa_attention_epilogue *epi, void *ws, size_t ws_bytes,
-                                 int *err, cudaStream_t stream) {
+namespace {
+template <int FMT, bool TREE>
+cudaError_t launch_pairs(const void *q, const float *sink, float scale, const csa_cache_desc &comp, const void *ring,
+                         int R, int W, const csa_draft_tree &tree, const int32_t *topk_idx, const int32_t *topk_cnt,
+                         const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
+                         void *out, float *lse, const csa_attention_epilogue *epi, void *ws, size_t ws_bytes, int *err,
+                         cudaStream_t stream) {
     Params P = {};
+    P.draft = static_cast<const uint8_t *>(tree.records);
+    P.parent = tree.parent;
     P.q = static_cast<const __nv_bfloat16 *>(q);
     P.sink = sink;
     P.scale_log2 = scale * kLog2e;
@@ -1108,12 +1234,12 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
         P.part_ml = reinterpret_cast<float2 *>(P.part_ex + parts * 16);
     }
     constexpr size_t smem = sizeof(AttSmem) + 1024;
-    cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel), (int)smem);
+    cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel<FMT, TREE>), (int)smem);
     if (e != cudaSuccess) return e;
     PdlLaunch l(dim3(2 * rows * P.n_split), dim3(kThreads), stream);
     l.cfg.dynamicSmemBytes = smem;
     count_launch();
-    e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel, P);
+    e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel<FMT, TREE>, P);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || P.n_split == 1) return e;
     const bool spread = P.n_split > kCombineBatch;  // eight warps a head instead of one
@@ -1121,6 +1247,34 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
     count_launch();
     e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8>, P) : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1>, P);
     return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, const csa_cache_desc &comp,
+                                 const void *ring, int R, int W, const int32_t *topk_idx, const int32_t *topk_cnt,
+                                 const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
+                                 void *out, float *lse, const csa_attention_epilogue *epi, void *ws, size_t ws_bytes,
+                                 int *err, cudaStream_t stream) {
+    return launch_pairs<CSA_FORMAT_FP4, false>(q, sink, scale, comp, ring, R, W, csa_draft_tree{}, topk_idx, topk_cnt,
+                                               n_comp, m_hca, q_pos, B, T, k, hca, out, lse, epi, ws, ws_bytes, err,
+                                               stream);
+}
+
+size_t tree_attention_workspace_bytes(int B, int N, int max_selected, int W) {
+    return attention_fp4_workspace_bytes(B, N, max_selected, W);
+}
+
+// The tokens of a tree, over either record format.
+cudaError_t launch_tree_attention(const void *q, const float *sink, float scale, const csa_cache_desc &comp,
+                                  csa_format_t fmt, const void *ring, int R, int W, const csa_draft_tree &tree,
+                                  const int32_t *topk_idx, const int32_t *topk_cnt, const int32_t *n_comp, int m_hca,
+                                  const int32_t *q_pos, int B, int N, int k, bool hca, void *out, float *lse,
+                                  const csa_attention_epilogue *epi, void *ws, size_t ws_bytes, int *err,
+                                  cudaStream_t stream) {
+    const auto launch = fmt == CSA_FORMAT_FP4 ? launch_pairs<CSA_FORMAT_FP4, true> : launch_pairs<CSA_FORMAT_FP8, true>;
+    return launch(q, sink, scale, comp, ring, R, W, tree, topk_idx, topk_cnt, n_comp, m_hca, q_pos, B, N, k, hca, out,
+                  lse, epi, ws, ws_bytes, err, stream);
 }
 
 }  // namespace csa

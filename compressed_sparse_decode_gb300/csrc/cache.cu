@@ -365,6 +365,41 @@ read_kernel(const __grid_constant__ ReadParams P) {
     }
 }
 
+struct CommitParams {
+    Span span;
+    const uint4 *records;
+    const int32_t *select;
+    int N, words;  // records a sequence, 16-byte words a record
+    uint4 *base;
+    int *err;
+};
+
+// A warp a token: 24 or 37 words of 16 bytes, one or two a lane.
+__global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitParams P) {
+    ptx::griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (token >= P.span.B * P.span.T) return;
+    const int b = token / P.span.T, t = token - b * P.span.T;
+    // every lane looks the token up (the same addresses); one of them reports
+    int *const err = lane == 0 ? P.err : nullptr;
+    const Slot to = find_slot(P.span, b, t, err);
+    if (to.record < 0) return;
+    const int from = P.select ? __ldg(P.select + token) : t;
+    if (from < 0 || from >= P.N) {
+        report_error(err, CSA_ERR_BAD_INDEX);
+        return;
+    }
+    const uint4 *src = P.records + ((int64_t)b * P.N + from) * P.words;
+    uint4 *dst = P.base + to.record * P.words;
+    const bool more = lane + 32 < P.words;
+    uint4 v, w;
+    if (lane < P.words) v = __ldg(src + lane);
+    if (more) w = __ldg(src + lane + 32);
+    if (lane < P.words) dst[lane] = v;
+    if (more) dst[lane + 32] = w;
+}
+
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 // The checks that both calls share, and their span.
@@ -464,5 +499,26 @@ extern "C" CSA_API csa_status_t csa_cache_read(csa_cache_desc cache, csa_format_
     count_launch();
     const cudaError_t e = fmt == CSA_FORMAT_FP4 ? cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP4>, P)
                                                 : cudaLaunchKernelEx(&l.cfg, read_kernel<CSA_FORMAT_FP8>, P);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+extern "C" CSA_API csa_status_t csa_cache_commit(csa_cache_desc cache, csa_format_t fmt, int ring, const void *records,
+                                                 int N, const int32_t *select, const int32_t *first,
+                                                 const int32_t *count, int B, int T, int32_t *status,
+                                                 cudaStream_t stream) {
+    using namespace csa;
+    CommitParams P;
+    const csa_status_t a = make_span(cache, fmt, ring, first, count, B, T, status, &P.span);
+    if (a != CSA_OK) return a;
+    if (!records || misaligned(records) || misaligned(select) || N < 1 || (!select && T > N)) return CSA_ERR_INVALID_ARG;
+    P.records = static_cast<const uint4 *>(records);
+    P.select = select;
+    P.N = N;
+    P.words = (fmt == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes) / 16;
+    P.base = static_cast<uint4 *>(const_cast<void *>(cache.base));
+    P.err = status;
+    PdlLaunch l(dim3((B * T + kWarps - 1) / kWarps), dim3(kThreads), stream);
+    count_launch();
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, commit_kernel, P);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }

@@ -17,7 +17,10 @@
  * Beside the step: queries and latents are prepared by csa_head_norm_rope and
  * csa_head_norm_rope_e4m3, caches are filled by csa_cache_append and read back by
  * csa_cache_read, and the *_fp4 calls run the attention and the step over caches
- * of 4-bit records.
+ * of 4-bit records. Speculative decoding runs the attention and the step over a
+ * tree of drafted tokens (csa_tree_attention_decode, hca_tree_attention_decode,
+ * csa_tree_decode_step), accepts a path of it (csa_verify_drafts) and puts that
+ * path's records into the caches (csa_cache_commit).
  *
  * Conventions for every call
  *  - Pointers are DEVICE pointers unless stated; the caller owns all memory.
@@ -133,7 +136,11 @@ typedef enum {
     CSA_OP_TOPK = 1,
     CSA_OP_ATTENTION = 2,     /* csa_sink_attention_decode, `k` = top-k */
     CSA_OP_HCA_ATTENTION = 3, /* hca_sink_attention_decode, `k` ignored */
-    CSA_OP_DECODE_STEP = 4    /* csa_decode_step */
+    CSA_OP_DECODE_STEP = 4,   /* csa_decode_step */
+    CSA_OP_TREE_ATTENTION = 5,     /* csa_tree_attention_decode, T = N */
+    CSA_OP_HCA_TREE_ATTENTION = 6, /* hca_tree_attention_decode, T = N, `k` ignored */
+    CSA_OP_TREE_STEP = 7,          /* csa_tree_decode_step, T = N */
+    CSA_OP_VERIFY = 8              /* csa_verify_drafts, T = N, Ncap = V, `k` ignored */
 } csa_op_t;
 
 /* Workspace bytes that `op` needs for these sizes (0 if none). A workspace
@@ -480,6 +487,116 @@ CSA_API csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_id
                                          float *lse, int32_t *topk_idx, int32_t *topk_cnt,
                                          const csa_attention_epilogue *epilogue, void *workspace,
                                          size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/* ---- Speculative decoding: a tree of drafted tokens in one step.
+ *
+ * A tree of N tokens a sequence is an array of parents: parent[b,i] < i is the
+ * token that token i follows, -1 the last committed token (one that is in the
+ * sequence's window ring). Token i stands at position q_pos[b,i] = position of its
+ * parent + 1 (siblings share one); q_pos[b,i] < 0 marks padding: the token is not
+ * computed and its rows of the outputs are left as they were.
+ *   records  [B,N, record bytes] the drafted tokens' latents, records of the cache's
+ *            format (csa_cache_append with B sequences of N entries makes them)
+ *   parent   [B,N] int32. An entry outside [-1, i) is taken as -1
+ *            (CSA_ERR_BAD_INDEX) */
+typedef struct {
+    const void *records;
+    const int32_t *parent;
+} csa_draft_tree;
+
+/* The sink-merged attention of a tree's tokens: formulas, arguments, epilogue and
+ * error behaviour of csa_sink_attention_decode_ex, hca_sink_attention_decode_ex
+ * and csa_decode_step_ex, over caches of either format `fmt` (comp, swa_ring and
+ * tree->records hold records of it), but the window of token i at position p is
+ * itself, its ancestors a_1, a_2, .. in the tree and, before them, the
+ * committed tokens: the W positions p, p - 1, .. (none below 0), of which the
+ * first come from tree->records and, from the last committed token's on, from the
+ * ring. The ring has to hold the W - 1 committed positions before a root token
+ * (R >= W); no token of the tree is read from it. For every token the selected or
+ * visible compressed entries are those of its position q_pos, as without a tree.
+ * FP8 latents are rounded to BF16, 4-bit ones are exact; weights and partial outputs
+ * are rounded as in the *_fp4 calls, and as there, a NaN or infinite latent reaches
+ * the rows that select it and no others. Requires N <= CSA_MAX_TOKENS_PER_SEQ;
+ * workspaces: CSA_OP_TREE_ATTENTION, CSA_OP_HCA_TREE_ATTENTION, CSA_OP_TREE_STEP. */
+CSA_API csa_status_t csa_tree_attention_decode(const void *q, const float *sink, float softmax_scale,
+                                               csa_cache_desc comp, csa_format_t fmt, const void *swa_ring, int R,
+                                               int W, const csa_draft_tree *tree, const int32_t *topk_idx,
+                                               const int32_t *topk_cnt, const int32_t *q_pos, int B, int N, int k,
+                                               void *out, float *lse, const csa_attention_epilogue *epilogue,
+                                               void *workspace, size_t workspace_bytes, int32_t *status,
+                                               cudaStream_t stream);
+CSA_API csa_status_t hca_tree_attention_decode(const void *q, const float *sink, float softmax_scale,
+                                               csa_cache_desc comp, csa_format_t fmt, const int32_t *n_comp,
+                                               const void *swa_ring, int R, int W, const csa_draft_tree *tree,
+                                               const int32_t *q_pos, int B, int N, int m_hca, void *out, float *lse,
+                                               const csa_attention_epilogue *epilogue, void *workspace,
+                                               size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+CSA_API csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
+                                          const uint8_t *k_idx, const float *k_idx_scale, const void *q,
+                                          const float *sink, float softmax_scale, csa_cache_desc comp,
+                                          csa_format_t fmt, const void *swa_ring, int R, int W,
+                                          const csa_draft_tree *tree, const int32_t *q_pos, const int32_t *n_comp,
+                                          int B, int N, int Ncap, int m, int k, void *out, float *lse,
+                                          int32_t *topk_idx, int32_t *topk_cnt,
+                                          const csa_attention_epilogue *epilogue, void *workspace,
+                                          size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/* Verification of a tree's drafted tokens against the target's distribution, given
+ * the random numbers: what is emitted is distributed as if drawn from the target.
+ * Token 0 is the sequence's newest known token (the last one emitted), the others
+ * are drafts. With z = logits[b,j,.], t = temperature[b] and
+ *   p_j(v) = exp(z_v / t) / sum_w exp(z_w / t),   q_j(v) = draft_probs[b,j,v]
+ * the walk starts at j = 0 with r = p_0, R = 1 and goes through the children i of
+ * j (those with parent[b,i] = j) in ascending order. With x = token[b,i]:
+ *   accept  if uniform[b,i] * q_j(x) * R < r(x): j becomes i, r = p_i, R = 1;
+ *   reject  else: r = max(r - R q_j, 0) for every v, R = sum_v r(v).
+ * Without draft_probs (drafts that are no draws: the best tokens, looked-up text)
+ * q_j(x) is 1 and a rejection sets r(x) = 0 instead. When no child of j is left,
+ * next_token[b] = the v with the largest r(v) / noise[b,v] among r(v) > 0, the lowest
+ * on ties: for noise of exponential variates a draw from r. (If rounding left no
+ * r(v) > 0, r is p_j again.) t <= 0 or NaN is greedy: a child is accepted if its
+ * token is the largest logit's (the lowest on ties), which also is next_token.
+ *   logits       element (b, i, v) at logits[b*seq_stride + i*token_stride + v], of
+ *                type logits_dtype; strides in elements, >= 0. -inf masks a token. A
+ *                row whose largest logit is not finite (all are -inf, one is +inf or
+ *                NaN) has no distribution: if the walk reaches it, it ends there
+ *                and next_token is -1
+ *   draft_probs  NULL, or [B,N,V] of type draft_dtype, dense: row i is the
+ *                distribution that the children of i were drawn from (not read for
+ *                rows that the walk does not reach or that have no children)
+ *   token        [B,N] int32; parent [B,N] int32 (see csa_draft_tree; token 0's is not
+ *                read, and tokens that token 0 does not lead to, as those with
+ *                parent -1, are never reached). A draft outside [0,V) is never
+ *                accepted and takes nothing from r (CSA_ERR_BAD_INDEX if it is tried)
+ *   uniform      [B,N] fp32 in [0,1)      noise [B,V] fp32, > 0
+ *   temperature  [B] fp32, or NULL for 1
+ *   path         [B,N] int32: the accepted tokens' numbers from 0 on, -1 behind them
+ *   accepted     [B] int32 in [1,N]: how many these are
+ *   next_token   [B] int32
+ * Weights, sums and quotients are fp32. Requires B >= 1, 1 <= N <=
+ * CSA_MAX_TOKENS_PER_SEQ, B*N <= 65535, 1 <= V <= 2^24. Pointers need the alignment
+ * of their elements only (rows that all begin on 16 bytes are read in wider loads). */
+CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_t logits_dtype, int64_t seq_stride,
+                                       int64_t token_stride, const void *draft_probs, csa_dtype_t draft_dtype,
+                                       const int32_t *token, const int32_t *parent, const float *uniform,
+                                       const float *noise, const float *temperature, int B, int N, int V,
+                                       int32_t *path, int32_t *accepted, int32_t *next_token, void *workspace,
+                                       size_t workspace_bytes, int32_t *status, cudaStream_t stream);
+
+/* Puts records into a cache byte for byte: record select[b,t] of sequence b
+ * (t < count[b]) becomes entry first[b] + t of its sequence. After
+ * csa_verify_drafts, select is its path, count its accepted, first the number of
+ * committed tokens.
+ *   cache, fmt, ring, first, count   as in csa_cache_append (base is written; of more
+ *            than seq_capacity tokens only the last are kept in a ring)
+ *   records  [B,N, record bytes], not part of the cache
+ *   select   [B,T] int32 in [0,N) (entries behind count are not read), or NULL for t
+ * An entry outside the cache or a select outside [0,N) is not stored
+ * (CSA_ERR_BAD_INDEX); every other record of the cache is left as it was. Requires
+ * B, T, N >= 1, B*T <= 2^24, and T <= N without select. */
+CSA_API csa_status_t csa_cache_commit(csa_cache_desc cache, csa_format_t fmt, int ring, const void *records, int N,
+                                      const int32_t *select, const int32_t *first, const int32_t *count, int B,
+                                      int T, int32_t *status, cudaStream_t stream);
 
 /* Host-I/O decode pipeline (the pages have no counterpart; it serves callers
  * whose query-side inputs arrive in, and whose results go back to, host
