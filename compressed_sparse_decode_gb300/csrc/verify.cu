@@ -30,6 +30,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxNodes = CSA_MAX_TOKENS_PER_SEQ;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596303e-8f;  // log2(e) in two floats
 constexpr int kNoDraft = -1;  // draft type: none
 
 // What a pass over a row leaves: a value, its index and a sum.
@@ -57,17 +58,30 @@ __device__ __forceinline__ float element(const void *base, int64_t at) {
     return __bfloat162float(__ldg(static_cast<const __nv_bfloat16 *>(base) + at));
 }
 
-// W consecutive elements: 1, or 8 where rows begin on 16 bytes.
-template <int DT, int W>
-__device__ __forceinline__ void elements(const void *base, int64_t at, float (&f)[W]) {
-    if constexpr (W == 1) {
-        f[0] = element<DT>(base, at);
-    } else {
-        Octet<DT> o;
-        o.load(base, at);
-        o.floats(f);
+// A thread's U units of W consecutive elements, kThreads units apart, all loaded before any
+// is used. W is 8 where rows begin on 16 bytes, else 1.
+template <int DT, int W, int U>
+struct Units;
+template <int DT, int U>
+struct Units<DT, 8, U> {
+    Octet<DT> o[U];
+    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * kThreads * 8 < v1) o[u].load(base, row + v + u * kThreads * 8);
     }
-}
+    __device__ __forceinline__ void get(int u, float (&f)[8]) const { o[u].floats(f); }
+};
+template <int DT, int U>
+struct Units<DT, 1, U> {
+    float o[U];
+    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v + u * kThreads < v1) o[u] = element<DT>(base, row + v + u * kThreads);
+    }
+    __device__ __forceinline__ void get(int u, float (&f)[1]) const { f[0] = o[u]; }
+};
 
 __device__ __forceinline__ void store_remote(uint32_t addr, const Found &f) {
     asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(__float_as_uint(f.value)),
@@ -75,37 +89,37 @@ __device__ __forceinline__ void store_remote(uint32_t addr, const Found &f) {
                  : "memory");
 }
 
-__device__ __forceinline__ Found shuffled(const Found &f, int o) {
-    Found r;
-    r.value = __shfl_xor_sync(kAll, f.value, o);
-    r.index = __shfl_xor_sync(kAll, f.index, o);
-    r.sum = __shfl_xor_sync(kAll, f.sum, o);
-    r.unused = 0;
-    return r;
+// The larger value, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
 }
 
-// The larger value (the lower index on ties; a NaN stays).
-__device__ __forceinline__ bool before(const Found &a, const Found &b) {
-    return a.value > b.value || (a.value == b.value && a.index < b.index) || (a.value != a.value && b.value == b.value);
+// Order of the values: -0 is 0, a NaN (of any bits) above all.
+__device__ __forceinline__ uint32_t value_key(float v) {
+    return v != v ? 0xFFFFFFFFu : v == 0.f ? 0x80000000u : order_key(v);
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
-// Softmax statistics joined: sum is of 2^{(z - value) k}.
-struct JoinSoftmax {
-    float k;
-    __device__ __forceinline__ Found operator()(const Found &a, const Found &b) const {
-        Found r = before(b, a) ? b : a;
-        const float m = r.value;
-        // (a part whose largest is -inf has the sum 0, whatever the factor)
-        const float fa = a.value > -INFINITY ? exp2f((a.value - m) * k) : 0.f;
-        const float fb = b.value > -INFINITY ? exp2f((b.value - m) * k) : 0.f;
-        r.sum = a.sum * fa + b.sum * fb;
-        return r;
+// How the parts of a pass are joined: the largest value (a NaN is the largest of all) with
+// its lowest index, and the sum. Of a softmax the sums are of 2^{(z - value) k} and scaled
+// to the largest value (a part whose value is -inf has the sum 0).
+struct Join {
+    float k;  // 0: plain sums
+    __device__ __forceinline__ float factor(float value, float top) const {
+        return k == 0.f ? 1.f : value > -INFINITY ? exp2f((value - top) * k) : 0.f;
     }
-};
-struct JoinSum {
-    __device__ __forceinline__ Found operator()(const Found &a, const Found &b) const {
-        Found r = before(b, a) ? b : a;
-        r.sum = a.sum + b.sum;
+    // the parts of a warp's first `lanes` lanes (a power of two; the others hold them again)
+    __device__ __forceinline__ Found warp(const Found &f, int lanes) const {
+        Found r;
+        const uint32_t key = value_key(f.value), top = __reduce_max_sync(kAll, key);
+        r.value = key_value(top);
+        r.index = (int32_t)__reduce_min_sync(kAll, key == top ? (uint32_t)f.index : 0x7FFFFFFFu);
+        r.sum = f.sum * factor(f.value, r.value);
+        for (int o = lanes / 2; o; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
+        r.unused = 0;
         return r;
     }
 };
@@ -144,32 +158,21 @@ struct Smem {
 
 // Joins every thread's part over the cluster; the same result, bit for bit, in
 // all threads of it.
-template <class Join>
 __device__ __forceinline__ Found join_cluster(Smem &s, Found f, int ctas, int rank, int &pass, const Join &join) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const Found other = shuffled(f, o);
-        f = (lane & o) ? join(other, f) : join(f, other);  // in one order in both lanes
-    }
+    f = join.warp(f, 32);
     if (lane == 0) s.warps[warp] = f;
     __syncthreads();
     if (warp == 0) {
-        f = s.warps[lane % kWarps];
-#pragma unroll
-        for (int o = kWarps / 2; o; o >>= 1) {
-            const Found other = shuffled(f, o);
-            f = (lane & o) ? join(other, f) : join(f, other);
-        }
+        f = join.warp(s.warps[lane % kWarps], kWarps);
         if (lane < ctas) store_remote(ptx::mapa(ptx::smem_u32(&s.ctas[pass & 1][rank]), lane), f);
     }
     // (A slot is written again two passes later, behind the next pass's barrier,
     // which every thread enters after it has read this pass's slots.)
     ptx::cluster_sync();
-    f = s.ctas[pass & 1][0];
-    for (int c = 1; c < ctas; ++c) f = join(f, s.ctas[pass & 1][c]);
+    const Found r = join.warp(s.ctas[pass & 1][lane & (ctas - 1)], ctas);
     ++pass;
-    return f;
+    return r;
 }
 
 template <int DT, int QT, int W>
@@ -180,6 +183,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31;
     constexpr bool kDraft = QT != kNoDraft;
     constexpr int kQ = kDraft ? QT : CSA_FP32;
+    constexpr int kRow = W == 1 ? 16 : DT == CSA_FP32 ? 2 : 4;              // units of a row in flight
+    constexpr int kRows = W == 1 ? 8 : DT == CSA_FP32 || kDraft ? 1 : 2;  // of two or three rows
     if (tid < P.N) {
         const int64_t at = (int64_t)b * P.N + tid;
         s.parent[tid] = __ldg(P.parent + at);
@@ -188,12 +193,20 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     }
     const float t = P.temperature ? __ldg(P.temperature + b) : 1.f;
     const bool greedy = !(t > 0.f);
-    // 1 / t in units of log2; in (0, inf) for any t, so that a largest logit's weight
-    // stays 1 and a masked token's 0
-    const double kd = greedy ? 1.4426950408889634 : fmin(fmax(1.4426950408889634 / (double)t, 1e-30), 1e38);
-    const float k = (float)kd, k_rest = (float)(kd - (double)k);
+    // 1 / t in units of log2, in two floats; in (0, inf) for any t, so that a largest
+    // logit's weight stays 1 and a masked token's 0
+    float k = kLog2e, k_rest = kLog2eRest;
+    if (!greedy) {
+        k = fminf(fmaxf(kLog2e / t, 1e-30f), 1e38f);
+        const float rest = (fmaf(-k, t, kLog2e) + kLog2eRest) / t;
+        k_rest = fabsf(rest) < k ? rest : 0.f;  // (where k was clamped it has none)
+    }
     const int v0 = rank * P.slice, v1 = min(P.V, v0 + P.slice);  // this CTA's tokens
-    const float *noise = P.noise + (int64_t)b * P.V;
+    const int mine = v0 + tid * W;                               // this thread's first
+    const int64_t noise_row = (int64_t)b * P.V;
+    if (!greedy)  // (read at the end of the walk)
+        for (int v = v0 + tid * 32; v < v1; v += kThreads * 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(P.noise + noise_row + v));
     // every CTA has started before anything is stored into it
     ptx::cluster_sync();
 
@@ -204,35 +217,67 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         ++n;
         const int64_t row = b * P.seq_stride + cur * P.token_stride;
         const int64_t qrow = ((int64_t)b * P.N + cur) * P.V;
-        if (tid < P.N && tid > cur && s.parent[tid] == cur) {  // what the children's tests will ask for
+        // what the children's tests will ask for, under way with the row
+        const bool child_here = tid < P.N && tid > cur && s.parent[tid] == cur;
+        float child_logit = 0.f, child_q = 1.f;
+        if (child_here) {
             const int x = s.token[tid];
-            const bool in = x >= 0 && x < P.V;
-            s.logit[tid] = in ? element<DT>(P.logits, row + x) : 0.f;
-            s.draft[tid] = kDraft && in ? element<kQ>(P.draft, qrow + x) : 1.f;
+            if (x >= 0 && x < P.V) {
+                child_logit = element<DT>(P.logits, row + x);
+                if (kDraft) child_q = element<kQ>(P.draft, qrow + x);
+            }
         }
         // ---- the row's largest logit and softmax sum
         Found f = {-INFINITY, INT32_MAX, 0.f, 0u};
-        for (int v = v0 + tid * W; v < v1; v += kThreads * W) {
-            float z[W];
-            elements<DT, W>(P.logits, row + v, z);
-            float m = z[0];
-            int at = 0;
+        for (int v = mine; v < v1; v += kThreads * W * kRow) {
+            Units<DT, W, kRow> z;
+            z.load(P.logits, row, v, v1);
+            float m = f.value;
 #pragma unroll
-            for (int e = 1; e < W; ++e)
-                if (z[e] > m || (z[e] != z[e] && m == m)) m = z[e], at = e;
-            if (m > f.value || (m != m && f.value == f.value)) {
-                f.sum = f.value > -INFINITY ? f.sum * exp2f((f.value - m) * k) : 0.f;
+            for (int u = 0; u < kRow; ++u)
+                if (v + u * kThreads * W < v1) {
+                    float x[W];
+                    z.get(u, x);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) m = max_nan(m, x[e]);
+                }
+            if (greedy) {
+                if (m != f.value) {  // (its first place; no sum is needed)
+                    f.value = m;
+#pragma unroll
+                    for (int u = kRow - 1; u >= 0; --u)
+                        if (v + u * kThreads * W < v1) {
+                            float x[W];
+                            z.get(u, x);
+#pragma unroll
+                            for (int e = W - 1; e >= 0; --e)
+                                if (x[e] == m) f.index = v + u * kThreads * W + e;
+                        }
+                }
+                continue;
+            }
+            if (!(m > -INFINITY)) {  // (nothing yet, or a NaN)
                 f.value = m;
-                f.index = v + at;
+                continue;
             }
-            if (f.value > -INFINITY) {
-                float part = 0.f;
+            f.sum = f.value > -INFINITY ? f.sum * exp2f((f.value - m) * k) : 0.f;
+            f.value = m;
+            float part[2] = {0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < W; ++e) part += exp2f((z[e] - f.value) * k);
-                f.sum += part;
-            }
+            for (int u = 0; u < kRow; ++u)
+                if (v + u * kThreads * W < v1) {
+                    float x[W];
+                    z.get(u, x);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) part[(u * W + e) & 1] += ptx::ex2_approx((x[e] - m) * k);
+                }
+            f.sum += part[0] + part[1];
         }
-        f = join_cluster(s, f, ctas, rank, pass, JoinSoftmax{k});
+        if (child_here) {
+            s.logit[tid] = child_logit;
+            s.draft[tid] = child_q;
+        }
+        f = join_cluster(s, f, ctas, rank, pass, Join{k});
         const float top = f.value;
         const int best = f.index;
         if (!(fabsf(top) < INFINITY)) break;  // no distribution
@@ -243,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         int gone = 0;        // rejected tokens in s.out
         int last = cur, taken = -1;
         auto weight = [&](float z, float q) {  // of a token in the residual, rejected tokens aside
-            const float p = exp2f((z - top) * k);
+            const float p = ptx::ex2_approx((z - top) * k);
             return kDraft ? p - S * q : p;
         };
         while (taken < 0) {
@@ -266,14 +311,22 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             }
             if (kDraft && stale) {  // the sum of what is left
                 Found g = {0.f, 0, 0.f, 0u};
-                for (int v = v0 + tid * W; v < v1; v += kThreads * W) {
-                    float z[W], q[W];
-                    elements<DT, W>(P.logits, row + v, z);
-                    elements<kQ, W>(P.draft, qrow + v, q);
+                for (int v = mine; v < v1; v += kThreads * W * kRows) {
+                    Units<DT, W, kRows> z;
+                    Units<kQ, W, kRows> q;
+                    z.load(P.logits, row, v, v1);
+                    q.load(P.draft, qrow, v, v1);
 #pragma unroll
-                    for (int e = 0; e < W; ++e) g.sum += fmaxf(weight(z[e], q[e]), 0.f);
+                    for (int u = 0; u < kRows; ++u)
+                        if (v + u * kThreads * W < v1) {
+                            float x[W], y[W];
+                            z.get(u, x);
+                            q.get(u, y);
+#pragma unroll
+                            for (int e = 0; e < W; ++e) g.sum += fmaxf(weight(x[e], y[e]), 0.f);
+                        }
                 }
-                R = {join_cluster(s, g, ctas, rank, pass, JoinSum{}).sum, 0.f};
+                R = {join_cluster(s, g, ctas, rank, pass, Join{0.f}).sum, 0.f};
                 stale = false;
             }
             const float p = weight_of(s.logit[child] - top, k, k_rest);
@@ -311,23 +364,38 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         for (int from_p = 0; from_p < 2; ++from_p) {  // the second time from p itself
             if (from_p) S = 0.f, gone = 0;
             Found g = {-1.f, INT32_MAX, 0.f, 0u};
-            for (int v = v0 + tid * W; v < v1; v += kThreads * W) {
-                float z[W], q[W], e[W];
-                elements<DT, W>(P.logits, row + v, z);
-                if (kDraft) elements<kQ, W>(P.draft, qrow + v, q);
-                elements<CSA_FP32, W>(noise, v, e);
+            for (int v = mine; v < v1; v += kThreads * W * kRows) {
+                Units<DT, W, kRows> z;
+                Units<kQ, W, kRows> q;
+                Units<CSA_FP32, W, kRows> e;
+                z.load(P.logits, row, v, v1);
+                if (kDraft) q.load(P.draft, qrow, v, v1);
+                e.load(P.noise, noise_row, v, v1);
+                uint32_t out = 0;  // which of these tokens were rejected
+                if (!kDraft)
+                    for (int o = 0; o < gone; ++o) {
+                        const int at = s.out[o] - v;
 #pragma unroll
-                for (int i = 0; i < W; ++i) {
-                    const float r = weight(z[i], kDraft ? q[i] : 0.f);
-                    if (!(r > 0.f)) continue;
-                    const float ratio = r / e[i];
-                    if (!(ratio > g.value)) continue;
-                    bool out = false;
-                    for (int o = 0; o < gone; ++o) out |= s.out[o] == v + i;
-                    if (!out) g.value = ratio, g.index = v + i;
-                }
+                        for (int u = 0; u < kRows; ++u)
+                            if ((uint32_t)(at - u * kThreads * W) < (uint32_t)W) out |= 1u << (u * W + at - u * kThreads * W);
+                    }
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    if (v + u * kThreads * W < v1) {
+                        float x[W], y[W], d[W];
+                        z.get(u, x);
+                        if (kDraft) q.get(u, y);
+                        e.get(u, d);
+#pragma unroll
+                        for (int i = 0; i < W; ++i) {
+                            const float r = weight(x[i], kDraft ? y[i] : 0.f);
+                            const bool in = r > 0.f && (kDraft || !(out >> (u * W + i) & 1u));
+                            const float ratio = in ? __fdividef(r, d[i]) : -1.f;
+                            if (ratio > g.value) g.value = ratio, g.index = v + u * kThreads * W + i;
+                        }
+                    }
             }
-            g = join_cluster(s, g, ctas, rank, pass, JoinSum{});
+            g = join_cluster(s, g, ctas, rank, pass, Join{0.f});
             if (g.value >= 0.f) {
                 next_token = g.index;
                 break;
@@ -347,11 +415,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 struct Plan {
     int ctas, slice;
 };
-// CTAs a sequence: as many as have 4096 tokens each, a power of two up to eight.
-Plan make_plan(int V) {
+// CTAs a sequence, a power of two up to eight: as many as have 2048 tokens each, while all
+// sequences' fit on the SMs at once (two an SM).
+Plan make_plan(int B, int V) {
     Plan p;
     p.ctas = 1;
-    while (p.ctas < kMaxCluster && V > p.ctas * 4096) p.ctas *= 2;
+    while (p.ctas < kMaxCluster && V > p.ctas * 2048 && B * p.ctas * 2 <= 2 * cached_sm_count()) p.ctas *= 2;
     p.slice = ((V + p.ctas - 1) / p.ctas + 7) / 8 * 8;
     return p;
 }
@@ -416,7 +485,7 @@ extern "C" CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_
     P.accepted = accepted;
     P.next = next_token;
     P.err = status;
-    const Plan plan = make_plan(V);
+    const Plan plan = make_plan(B, V);
     P.slice = plan.slice;
     // eight elements a load where every row that is read begins on 16 bytes
     const bool wide = V % 8 == 0 && seq_stride % 8 == 0 && token_stride % 8 == 0 && !off(logits, 16) &&
