@@ -200,12 +200,6 @@ __device__ __forceinline__ void store_to_peer(uint32_t addr, float v, uint32_t b
                  "r"(__float_as_uint(v)), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void store4_to_peer(uint32_t addr, const uint32_t *v, uint32_t bar) {
-    asm volatile(
-        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
-        : "memory");
-}
 // Copy into the other CTA, counted on a barrier there.
 __device__ __forceinline__ void copy_to_peer(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile(
@@ -214,24 +208,12 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, const void *src, uint
         : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // Bounded wait of a whole warp: true when the phase is complete for every lane,
 // and what the other CTA stored before it arrived is visible. One (suspending)
 // try is in line, the rest out of it (in line at every wait, the roles' loops take
 // more of the instruction cache: 203 us instead of 198 for the longest calls).
 __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, limit_ns) && try_wait_cluster(bar, parity)) != 0;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, limit_ns) && ptx::try_wait_cluster(bar, parity)) != 0;
 }
 
 // ---------------------------------------------------------------- unpacking
@@ -407,7 +389,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
     };
     auto wait_peer = [&](uint64_t *bar, uint32_t parity) {
-        const bool now = !poll && try_wait_cluster(bar, parity);
+        const bool now = !poll && ptx::try_wait_cluster(bar, parity);
         return __all_sync(0xffffffffu, now) || wait_slow(bar, parity, abort, P.wait_ns);
     };
     if (warp == kPtrWarp) {
@@ -712,7 +694,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::tmem_ld_wait();
 #pragma unroll
             for (int c = 0; c < kSoftCols / 4; ++c)
-                store4_to_peer(peer_part + c * (kHeads * 16), v + 4 * c, peer_part_full);
+                ptx::store4_to_peer(peer_part + c * (kHeads * 16), v + 4 * c, peer_part_full);
             __syncwarp();
             // (each warp expects the bytes of the other CTA's warp like it)
             if (lane == 0) ptx::mbar_arrive_expect_tx(&s.part_full, 32 * 4 * kSoftCols);

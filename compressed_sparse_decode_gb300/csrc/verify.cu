@@ -14,10 +14,10 @@
 //
 // One cluster of up to eight CTAs a sequence, each with a slice of the vocabulary;
 // only rows on the accepted path are read. All CTAs take every decision from the
-// same numbers in the same order, so they walk together without a leader; partial
-// results go to every CTA of the cluster through distributed shared memory, one
-// cluster barrier a pass.
+// same numbers in the same order, so they walk together without a leader; every warp's
+// part of a pass goes to every CTA of the cluster through distributed shared memory.
 #include <cmath>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -38,7 +38,7 @@ struct alignas(16) Found {
     float value;  // the largest (NaN if one is)
     int32_t index;
     float sum;
-    uint32_t unused;
+    uint32_t ok;  // (of the joined parts: they have all come)
 };
 
 struct VerifyParams {
@@ -49,6 +49,7 @@ struct VerifyParams {
     int N, V, slice;  // slice: tokens a CTA, a multiple of 8
     int32_t *path, *accepted, *next;
     int *err;
+    uint64_t wait_ns;  // limit of each bounded wait
 };
 
 template <int DT>
@@ -59,40 +60,122 @@ __device__ __forceinline__ float element(const void *base, int64_t at) {
 }
 
 // A thread's U units of W consecutive elements, kThreads units apart, all loaded before any
-// is used. W is 8 where rows begin on 16 bytes, else 1.
+// is used (behind v1: `fill`). W is 8 where rows begin on 16 bytes, else 1.
+template <int DT>
+constexpr uint32_t kMinusInf = DT == CSA_FP32 ? 0xFF800000u : DT == CSA_FP16 ? 0xFC00FC00u : 0xFF80FF80u;
 template <int DT, int W, int U>
 struct Units;
 template <int DT, int U>
 struct Units<DT, 8, U> {
     Octet<DT> o[U];
-    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1) {
+    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1, uint32_t fill) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            o[u].v = make_uint4(fill, fill, fill, fill);
+            if constexpr (DT == CSA_FP32) o[u].u = o[u].v;
             if (v + u * kThreads * 8 < v1) o[u].load(base, row + v + u * kThreads * 8);
+        }
     }
     __device__ __forceinline__ void get(int u, float (&f)[8]) const { o[u].floats(f); }
 };
 template <int DT, int U>
 struct Units<DT, 1, U> {
     float o[U];
-    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1) {
+    __device__ __forceinline__ void load(const void *base, int64_t row, int v, int v1, uint32_t fill) {
+        const float f = DT == CSA_FP32 ? __uint_as_float(fill) : fill ? -INFINITY : 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (v + u * kThreads < v1) o[u] = element<DT>(base, row + v + u * kThreads);
+        for (int u = 0; u < U; ++u) o[u] = v + u * kThreads < v1 ? element<DT>(base, row + v + u * kThreads) : f;
     }
     __device__ __forceinline__ void get(int u, float (&f)[1]) const { f[0] = o[u]; }
 };
-
-__device__ __forceinline__ void store_remote(uint32_t addr, const Found &f) {
-    asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(__float_as_uint(f.value)),
-                 "r"((uint32_t)f.index), "r"(__float_as_uint(f.sum)), "r"(0u)
-                 : "memory");
-}
 
 // The larger value, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
     return a;
+}
+
+// The largest element of the units, NaN if one is (16-bit elements two at a time).
+template <int DT, int W, int U>
+__device__ __forceinline__ float largest(const Units<DT, W, U> &z) {
+    if constexpr (W == 8 && DT != CSA_FP32) {
+        using Two = std::conditional_t<DT == CSA_BF16, __nv_bfloat162, __half2>;
+        Two m[2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4] = {z.o[u].v.x, z.o[u].v.y, z.o[u].v.z, z.o[u].v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Two x = *reinterpret_cast<const Two *>(&w[i]);
+                m[i & 1] = u == 0 && i < 2 ? x : __hmax2_nan(m[i & 1], x);
+            }
+        }
+        const Two t = __hmax2_nan(m[0], m[1]);
+        return max_nan((float)t.x, (float)t.y);
+    } else {
+        float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[W];
+            z.get(u, x);
+#pragma unroll
+            for (int e = 0; e < W; ++e) m[(u * W + e) & 1] = max_nan(m[(u * W + e) & 1], x[e]);
+        }
+        return max_nan(m[0], m[1]);
+    }
+}
+
+// A thread's part of the pass over tokens [mine, v1) of a row: the largest logit and the
+// softmax sum, or, greedy, the largest logit and its first place.
+template <int DT, int W>
+__device__ __forceinline__ Found scan_row(const void *logits, int64_t row, int mine, int v1, float k, bool greedy) {
+    constexpr int U = W == 1 ? 16 : DT == CSA_FP32 ? 2 : 4;  // units in flight
+    Found f = {-INFINITY, INT32_MAX, 0.f, 1u};
+    for (int v = mine; v < v1; v += kThreads * W * U) {
+        Units<DT, W, U> z;
+        z.load(logits, row, v, v1, kMinusInf<DT>);
+        const float m = max_nan(f.value, largest(z));
+        if (greedy) {
+            if (m == f.value) continue;
+            f.value = m;
+#pragma unroll
+            for (int u = U - 1; u >= 0; --u) {
+                float x[W];
+                z.get(u, x);
+#pragma unroll
+                for (int e = W - 1; e >= 0; --e)
+                    if (x[e] == m) f.index = v + u * kThreads * W + e;
+            }
+            continue;
+        }
+        if (!(m > -INFINITY)) {  // (nothing yet, or a NaN)
+            f.value = m;
+            continue;
+        }
+        f.sum = f.value > -INFINITY ? f.sum * exp2f((f.value - m) * k) : 0.f;
+        f.value = m;
+        if constexpr (W == 1) {
+            float part[2] = {0.f, 0.f};
+#pragma unroll
+            for (int u = 0; u < U; ++u) part[u & 1] += ptx::ex2_approx((z.o[u] - m) * k);
+            f.sum += part[0] + part[1];
+        } else {
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float x[W];
+                z.get(u, x);
+#pragma unroll
+                for (int e = 0; e < W / 2; ++e) {
+                    float2 d = __fadd2_rn(make_float2(x[2 * e], x[2 * e + 1]), make_float2(-m, -m));
+                    d = __fmul2_rn(d, make_float2(k, k));
+                    part[e & 1] = __fadd2_rn(part[e & 1], make_float2(ptx::ex2_approx(d.x), ptx::ex2_approx(d.y)));
+                }
+            }
+            f.sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+        }
+    }
+    return f;
 }
 
 // Order of the values: -0 is 0, a NaN (of any bits) above all.
@@ -119,7 +202,7 @@ struct Join {
         r.index = (int32_t)__reduce_min_sync(kAll, key == top ? (uint32_t)f.index : 0x7FFFFFFFu);
         r.sum = f.sum * factor(f.value, r.value);
         for (int o = lanes / 2; o; o >>= 1) r.sum += __shfl_xor_sync(kAll, r.sum, o);
-        r.unused = 0;
+        r.ok = 1;
         return r;
     }
 };
@@ -147,137 +230,138 @@ __device__ __forceinline__ Pair less(const Pair &a, float v) {
     return r;
 }
 
+// A sequence's 1 / temperature in units of log2, in two floats; in (0, inf) for any
+// temperature, so that a largest logit's weight stays 1 and a masked token's 0.
+struct Scale {
+    bool greedy;
+    float k, k_rest;
+    __device__ __forceinline__ Scale(const VerifyParams &P, int b) {
+        const float t = P.temperature ? __ldg(P.temperature + b) : 1.f;
+        greedy = !(t > 0.f);
+        k = kLog2e;
+        k_rest = kLog2eRest;
+        if (greedy) return;
+        k = fminf(fmaxf(kLog2e / t, 1e-30f), 1e38f);
+        const float rest = (fmaf(-k, t, kLog2e) + kLog2eRest) / t;
+        k_rest = fabsf(rest) < k ? rest : 0.f;  // (where k was clamped it has none)
+    }
+};
+
 struct Smem {
     Found warps[kWarps];
     Found ctas[2][kMaxCluster];  // by the parity of the pass
+    Found all;
+    uint64_t full[2];
     int32_t parent[kMaxNodes], token[kMaxNodes];
     float uniform[kMaxNodes];
-    float logit[kMaxNodes], draft[kMaxNodes];  // of the children of the current token
-    int32_t out[kMaxNodes];                    // rejected tokens of the current token (no draft probabilities)
+    float logit[kMaxNodes], draft[kMaxNodes];  // of the drafts: their logit and probability, in their parents' rows
+    uint8_t out[kWarps][kMaxNodes];            // a warp's list of the current token's rejected children (no draft)
+    int abort_flag;
 };
 
 // Joins every thread's part over the cluster; the same result, bit for bit, in
-// all threads of it.
-__device__ __forceinline__ Found join_cluster(Smem &s, Found f, int ctas, int rank, int &pass, const Join &join) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// all threads of it. The first warp of each CTA sends the CTA's part to all of them,
+// counted on a barrier there. (Slots and barriers are two by turns: those of pass p are
+// sent to again in pass p + 2, after a wait for pass p + 1, to which every CTA sends after
+// it has read pass p's.) False, for the whole CTA, after a wait that expired.
+__device__ __forceinline__ bool join_cluster(Smem &s, Found &f, int ctas, int rank, int &pass, const Join &join,
+                                             uint64_t wait_ns) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, now = pass & 1;
     f = join.warp(f, 32);
     if (lane == 0) s.warps[warp] = f;
     __syncthreads();
     if (warp == 0) {
         f = join.warp(s.warps[lane % kWarps], kWarps);
-        if (lane < ctas) store_remote(ptx::mapa(ptx::smem_u32(&s.ctas[pass & 1][rank]), lane), f);
+        uint64_t *full = &s.full[now];
+        if (lane < ctas) {
+            const uint32_t v[4] = {__float_as_uint(f.value), (uint32_t)f.index, __float_as_uint(f.sum), 0u};
+            ptx::store4_to_peer(ptx::mapa(ptx::smem_u32(&s.ctas[now][rank]), lane), v,
+                                ptx::mapa(ptx::smem_u32(full), lane));
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, ctas * sizeof(Found));
+        const uint32_t parity = (pass >> 1) & 1;
+        const bool here = ptx::try_wait_cluster(full, parity) ||
+                          (ptx::mbar_wait(full, parity, &s.abort_flag, wait_ns) && ptx::try_wait_cluster(full, parity));
+        const bool all = __all_sync(kAll, here);
+        f = join.warp(s.ctas[now][lane & (ctas - 1)], ctas);
+        f.ok = all;
+        if (lane == 0) s.all = f;
     }
-    // (A slot is written again two passes later, behind the next pass's barrier,
-    // which every thread enters after it has read this pass's slots.)
-    ptx::cluster_sync();
-    const Found r = join.warp(s.ctas[pass & 1][lane & (ctas - 1)], ctas);
+    __syncthreads();
+    f = s.all;
     ++pass;
-    return r;
+    return f.ok;
 }
 
 template <int DT, int QT, int W>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams P, int ctas) {
     __shared__ Smem s;
-    ptx::griddep_wait();
     const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
     const int tid = threadIdx.x, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.full[i], 1);  // (and all CTAs' bytes)
+        s.abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    // every CTA's barriers exist before anything is sent to it (waited for behind the
+    // first row's loads)
+    ptx::cluster_arrive();
+    ptx::griddep_wait();
     constexpr bool kDraft = QT != kNoDraft;
     constexpr int kQ = kDraft ? QT : CSA_FP32;
-    constexpr int kRow = W == 1 ? 16 : DT == CSA_FP32 ? 2 : 4;              // units of a row in flight
-    constexpr int kRows = W == 1 ? 8 : DT == CSA_FP32 || kDraft ? 1 : 2;  // of two or three rows
+    constexpr int kRows = W == 1 ? 8 : DT == CSA_FP32 || kDraft ? 1 : 2;  // units of two or three rows in flight
     if (tid < P.N) {
         const int64_t at = (int64_t)b * P.N + tid;
-        s.parent[tid] = __ldg(P.parent + at);
-        s.token[tid] = __ldg(P.token + at);
+        const int parent = __ldg(P.parent + at), x = __ldg(P.token + at);
+        s.parent[tid] = parent;
+        s.token[tid] = x;
         s.uniform[tid] = __ldg(P.uniform + at);
+        float logit = 0.f, q = 1.f;
+        if (parent >= 0 && parent < tid && x >= 0 && x < P.V) {
+            logit = element<DT>(P.logits, b * P.seq_stride + parent * P.token_stride + x);
+            if (kDraft) q = element<kQ>(P.draft, (at - tid + parent) * P.V + x);
+        }
+        s.logit[tid] = logit;
+        s.draft[tid] = q;
     }
-    const float t = P.temperature ? __ldg(P.temperature + b) : 1.f;
-    const bool greedy = !(t > 0.f);
-    // 1 / t in units of log2, in two floats; in (0, inf) for any t, so that a largest
-    // logit's weight stays 1 and a masked token's 0
-    float k = kLog2e, k_rest = kLog2eRest;
-    if (!greedy) {
-        k = fminf(fmaxf(kLog2e / t, 1e-30f), 1e38f);
-        const float rest = (fmaf(-k, t, kLog2e) + kLog2eRest) / t;
-        k_rest = fabsf(rest) < k ? rest : 0.f;  // (where k was clamped it has none)
-    }
+    const Scale scale(P, b);
+    const bool greedy = scale.greedy;
+    const float k = scale.k;
     const int v0 = rank * P.slice, v1 = min(P.V, v0 + P.slice);  // this CTA's tokens
     const int mine = v0 + tid * W;                               // this thread's first
     const int64_t noise_row = (int64_t)b * P.V;
-    if (!greedy)  // (read at the end of the walk)
-        for (int v = v0 + tid * 32; v < v1; v += kThreads * 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(P.noise + noise_row + v));
-    // every CTA has started before anything is stored into it
-    ptx::cluster_sync();
+    uint8_t *out_list = s.out[tid >> 5];
+    __syncthreads();
 
     int cur = 0, n = 0, pass = 0;
+    bool ok = true;
     if (rank == 0 && tid == 0) P.path[(int64_t)b * P.N] = 0;
     int next_token = -1;
+    // the current token's next child behind token `last` (kMaxNodes: none)
+    auto next_child = [&](int last) {
+        for (int i0 = last & ~31; i0 < P.N; i0 += 32) {
+            const int i = i0 + lane;
+            const uint32_t hit = __ballot_sync(kAll, i < P.N && i > last && s.parent[i] == cur);
+            if (hit) return i0 + __ffs(hit) - 1;
+        }
+        return kMaxNodes;
+    };
     while (true) {
         ++n;
         const int64_t row = b * P.seq_stride + cur * P.token_stride;
         const int64_t qrow = ((int64_t)b * P.N + cur) * P.V;
-        // what the children's tests will ask for, under way with the row
-        const bool child_here = tid < P.N && tid > cur && s.parent[tid] == cur;
-        float child_logit = 0.f, child_q = 1.f;
-        if (child_here) {
-            const int x = s.token[tid];
-            if (x >= 0 && x < P.V) {
-                child_logit = element<DT>(P.logits, row + x);
-                if (kDraft) child_q = element<kQ>(P.draft, qrow + x);
-            }
-        }
         // ---- the row's largest logit and softmax sum
-        Found f = {-INFINITY, INT32_MAX, 0.f, 0u};
-        for (int v = mine; v < v1; v += kThreads * W * kRow) {
-            Units<DT, W, kRow> z;
-            z.load(P.logits, row, v, v1);
-            float m = f.value;
-#pragma unroll
-            for (int u = 0; u < kRow; ++u)
-                if (v + u * kThreads * W < v1) {
-                    float x[W];
-                    z.get(u, x);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) m = max_nan(m, x[e]);
-                }
-            if (greedy) {
-                if (m != f.value) {  // (its first place; no sum is needed)
-                    f.value = m;
-#pragma unroll
-                    for (int u = kRow - 1; u >= 0; --u)
-                        if (v + u * kThreads * W < v1) {
-                            float x[W];
-                            z.get(u, x);
-#pragma unroll
-                            for (int e = W - 1; e >= 0; --e)
-                                if (x[e] == m) f.index = v + u * kThreads * W + e;
-                        }
-                }
-                continue;
-            }
-            if (!(m > -INFINITY)) {  // (nothing yet, or a NaN)
-                f.value = m;
-                continue;
-            }
-            f.sum = f.value > -INFINITY ? f.sum * exp2f((f.value - m) * k) : 0.f;
-            f.value = m;
-            float part[2] = {0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < kRow; ++u)
-                if (v + u * kThreads * W < v1) {
-                    float x[W];
-                    z.get(u, x);
-#pragma unroll
-                    for (int e = 0; e < W; ++e) part[(u * W + e) & 1] += ptx::ex2_approx((x[e] - m) * k);
-                }
-            f.sum += part[0] + part[1];
+        Found f = scan_row<DT, W>(P.logits, row, mine, v1, k, greedy);
+        if (n == 1) {
+            // the noise, read at the end of the walk, comes into L2 behind the first row
+            if (!greedy)
+                for (int v = v0 + tid * 32; v < v1; v += kThreads * 32)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(P.noise + noise_row + v));
+            ptx::cluster_wait();
         }
-        if (child_here) {
-            s.logit[tid] = child_logit;
-            s.draft[tid] = child_q;
-        }
-        f = join_cluster(s, f, ctas, rank, pass, Join{k});
+        ok = join_cluster(s, f, ctas, rank, pass, Join{k}, P.wait_ns);
+        if (!ok) break;
         const float top = f.value;
         const int best = f.index;
         if (!(fabsf(top) < INFINITY)) break;  // no distribution
@@ -285,19 +369,14 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         float S = 0.f;
         Pair R = {f.sum, 0.f};
         bool stale = false;  // R is that of the rejections before the last
-        int gone = 0;        // rejected tokens in s.out
+        int gone = 0;        // children in out_list
         int last = cur, taken = -1;
         auto weight = [&](float z, float q) {  // of a token in the residual, rejected tokens aside
             const float p = ptx::ex2_approx((z - top) * k);
             return kDraft ? p - S * q : p;
         };
         while (taken < 0) {
-            int child = kMaxNodes;
-            for (int i0 = 0; i0 < P.N && child == kMaxNodes; i0 += 32) {
-                const int i = i0 + lane;
-                const uint32_t hit = __ballot_sync(kAll, i < P.N && i > last && s.parent[i] == cur);
-                if (hit) child = i0 + __ffs(hit) - 1;
-            }
+            const int child = next_child(last);
             if (child == kMaxNodes) break;
             last = child;
             const int x = s.token[child];
@@ -314,29 +393,30 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 for (int v = mine; v < v1; v += kThreads * W * kRows) {
                     Units<DT, W, kRows> z;
                     Units<kQ, W, kRows> q;
-                    z.load(P.logits, row, v, v1);
-                    q.load(P.draft, qrow, v, v1);
+                    z.load(P.logits, row, v, v1, kMinusInf<DT>);
+                    q.load(P.draft, qrow, v, v1, 0u);
 #pragma unroll
-                    for (int u = 0; u < kRows; ++u)
-                        if (v + u * kThreads * W < v1) {
-                            float x[W], y[W];
-                            z.get(u, x);
-                            q.get(u, y);
+                    for (int u = 0; u < kRows; ++u) {
+                        float x[W], y[W];
+                        z.get(u, x);
+                        q.get(u, y);
 #pragma unroll
-                            for (int e = 0; e < W; ++e) g.sum += fmaxf(weight(x[e], y[e]), 0.f);
-                        }
+                        for (int e = 0; e < W; ++e) g.sum += fmaxf(weight(x[e], y[e]), 0.f);
+                    }
                 }
-                R = {join_cluster(s, g, ctas, rank, pass, Join{0.f}).sum, 0.f};
+                ok = join_cluster(s, g, ctas, rank, pass, Join{0.f}, P.wait_ns);
+                if (!ok) break;
+                R = {g.sum, 0.f};
                 stale = false;
             }
-            const float p = weight_of(s.logit[child] - top, k, k_rest);
+            const float p = weight_of(s.logit[child] - top, k, scale.k_rest);
             const float q = s.draft[child];
             float r = p;
             if (kDraft) {
                 r = fmaxf(fmaf(-S, q, p), 0.f);
             } else {
                 for (int i = 0; i < gone; ++i)
-                    if (s.out[i] == x) r = 0.f;
+                    if (s.token[out_list[i]] == x) r = 0.f;
             }
             if (s.uniform[child] * q * R.hi < r) {
                 taken = child;
@@ -345,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 stale = true;
             } else if (r > 0.f) {
                 R = less(R, p);
-                __syncthreads();
-                if (tid == 0) s.out[gone] = x;
+                if (lane == 0) out_list[gone] = (uint8_t)child;
                 ++gone;
-                __syncthreads();
+                __syncwarp();
             }
         }
+        if (!ok) break;
         if (taken >= 0) {
             if (rank == 0 && tid == 0) P.path[(int64_t)b * P.N + n] = taken;
             cur = taken;
@@ -368,40 +448,44 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 Units<DT, W, kRows> z;
                 Units<kQ, W, kRows> q;
                 Units<CSA_FP32, W, kRows> e;
-                z.load(P.logits, row, v, v1);
-                if (kDraft) q.load(P.draft, qrow, v, v1);
-                e.load(P.noise, noise_row, v, v1);
+                z.load(P.logits, row, v, v1, kMinusInf<DT>);
+                if (kDraft) q.load(P.draft, qrow, v, v1, 0u);
+                e.load(P.noise, noise_row, v, v1, 0x3F800000u);
                 uint32_t out = 0;  // which of these tokens were rejected
                 if (!kDraft)
                     for (int o = 0; o < gone; ++o) {
-                        const int at = s.out[o] - v;
+                        const int at = s.token[out_list[o]] - v;
 #pragma unroll
                         for (int u = 0; u < kRows; ++u)
                             if ((uint32_t)(at - u * kThreads * W) < (uint32_t)W) out |= 1u << (u * W + at - u * kThreads * W);
                     }
 #pragma unroll
-                for (int u = 0; u < kRows; ++u)
-                    if (v + u * kThreads * W < v1) {
-                        float x[W], y[W], d[W];
-                        z.get(u, x);
-                        if (kDraft) q.get(u, y);
-                        e.get(u, d);
+                for (int u = 0; u < kRows; ++u) {
+                    float x[W], y[W], d[W];
+                    z.get(u, x);
+                    if (kDraft) q.get(u, y);
+                    e.get(u, d);
 #pragma unroll
-                        for (int i = 0; i < W; ++i) {
-                            const float r = weight(x[i], kDraft ? y[i] : 0.f);
-                            const bool in = r > 0.f && (kDraft || !(out >> (u * W + i) & 1u));
-                            const float ratio = in ? __fdividef(r, d[i]) : -1.f;
-                            if (ratio > g.value) g.value = ratio, g.index = v + u * kThreads * W + i;
-                        }
+                    for (int i = 0; i < W; ++i) {
+                        const float r = weight(x[i], kDraft ? y[i] : 0.f);
+                        const bool in = r > 0.f && (kDraft || !(out >> (u * W + i) & 1u));
+                        const float ratio = in ? __fdividef(r, d[i]) : -1.f;
+                        if (ratio > g.value) g.value = ratio, g.index = v + u * kThreads * W + i;
                     }
+                }
             }
-            g = join_cluster(s, g, ctas, rank, pass, Join{0.f});
+            ok = join_cluster(s, g, ctas, rank, pass, Join{0.f}, P.wait_ns);
+            if (!ok) break;
             if (g.value >= 0.f) {
                 next_token = g.index;
                 break;
             }
         }
         break;
+    }
+    if (!ok) {  // given up: nothing is on its way to a CTA that has left
+        if (tid == 0) report_error(P.err, CSA_ERR_TIMEOUT);
+        ptx::cluster_sync();
     }
     if (rank == 0) {
         if (tid == 0) {
@@ -456,7 +540,7 @@ extern "C" CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_
                                                   int32_t *accepted, int32_t *next_token, void *workspace,
                                                   size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
     using namespace csa;
-    (void)workspace;
+    (void)workspace;  // (none is needed)
     (void)workspace_bytes;
     if (!logits || !token || !parent || !uniform || !noise || !path || !accepted || !next_token)
         return CSA_ERR_INVALID_ARG;
@@ -485,6 +569,7 @@ extern "C" CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_
     P.accepted = accepted;
     P.next = next_token;
     P.err = status;
+    P.wait_ns = wait_limit_ns();
     const Plan plan = make_plan(B, V);
     P.slice = plan.slice;
     // eight elements a load where every row that is read begins on 16 bytes
