@@ -45,7 +45,6 @@
 // unpacking, took 222 us; more warps for the unpacking, the softmax or the exchange
 // cost registers, and all were slower.)
 #include <cuda_fp4.h>
-#include <type_traits>
 
 #include "rows.cuh"
 
@@ -78,6 +77,7 @@ constexpr uint32_t kTmemCols = 512;
 
 struct AttSmem {
     alignas(1024) uint8_t x[2][kBlockBytes];
+    alignas(1024) uint8_t rest[kAtom];         // FP8: what rounding left of 64 dims of a block
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
     float4 part[2][kSoftCols / 4][kHeads];     // the other CTA's part of the own scores
@@ -85,7 +85,7 @@ struct AttSmem {
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
     uint64_t x_full[2], x_empty[2][2];         // of a buffer; of its chunks
-    uint64_t rest_done[2];                     // of a buffer: the scores have its latents' rests
+    uint64_t dims_full, rest_empty;            // FP8: of 64 dims and their rests; of the rests' buffer
     uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, part_full, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint8_t chain[CSA_MAX_TOKENS_PER_SEQ];  // a tree's token and its ancestors, the youngest first
@@ -262,7 +262,6 @@ struct Quarter<CSA_FORMAT_FP4> {
         }
     }
     // to column block i of a row at lo / hi (16-byte chunks 2 hq and 2 hq + 1)
-    template <bool REST>
     __device__ __forceinline__ void unpack(int rank, int hq, uint4 *lo, uint4 *hi) const {
         constexpr int kStep = kAtom / 16;
         const float pw = fp4_power(power & 0xFFu);
@@ -281,21 +280,20 @@ struct Quarter<CSA_FORMAT_FP4> {
     }
 };
 
-// 8 E4M3 codes times a multiplier as BF16 (rounded once), or, with `rest`, what that
-// rounding left, as BF16.
-template <bool REST>
-__device__ __forceinline__ uint4 unpack8_e4m3(uint32_t w0, uint32_t w1, float s) {
+// 8 E4M3 codes times a multiplier: as BF16 (rounded once), and what that rounding left, as
+// BF16.
+__device__ __forceinline__ void unpack8_e4m3(uint32_t w0, uint32_t w1, float s, uint4 &whole, uint4 &rest) {
     const uint32_t w[2] = {w0, w1};
-    uint32_t o[4];
+    uint32_t o[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
         const float2 a = __fmul2_rn(e4m3x2_to_float2(two), make_float2(s, s));
         o[i] = pack_bf16(a.x, a.y);
-        if (REST)
-            o[i] = pack_bf16(a.x - __uint_as_float(o[i] << 16), a.y - __uint_as_float(o[i] & 0xFFFF0000u));
+        l[i] = pack_bf16(a.x - __uint_as_float(o[i] << 16), a.y - __uint_as_float(o[i] & 0xFFFF0000u));
     }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    whole = make_uint4(o[0], o[1], o[2], o[3]);
+    rest = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
 template <>
@@ -315,22 +313,20 @@ struct Quarter<CSA_FORMAT_FP8> {
         if (rank == 1) piece[4] = __ldcs(last + 1);
         mult = __ldcs(reinterpret_cast<const float2 *>(rec + kScaleOffset) + rank);
     }
-    template <bool REST>
-    __device__ __forceinline__ void unpack(int rank, int hq, uint4 *lo, uint4 *hi) const {
-        constexpr int kStep = kAtom / 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (i == 3 && rank == 1) {
-                if (!REST) {  // (rope dims are BF16: no rest)
-                    lo[i * kStep] = piece[3];
-                    hi[i * kStep] = piece[4];
-                }
-                break;
-            }
-            const float s = i < 2 ? mult.x : mult.y;
-            lo[i * kStep] = unpack8_e4m3<REST>(piece[i].x, piece[i].y, s);
-            hi[i * kStep] = unpack8_e4m3<REST>(piece[i].z, piece[i].w, s);
+    // unit i's two 16-byte chunks, to lo and hi, and their rests (rope dims are BF16:
+    // none)
+    __device__ __forceinline__ void unpack(int i, int rank, uint4 *lo, uint4 *hi, uint4 (&rest)[2]) const {
+        if (i == 3 && rank == 1) {
+            *lo = piece[3];
+            *hi = piece[4];
+            return;
         }
+        const float s = i < 2 ? mult.x : mult.y;
+        uint4 whole[2];
+        unpack8_e4m3(piece[i].x, piece[i].y, s, whole[0], rest[0]);
+        unpack8_e4m3(piece[i].z, piece[i].w, s, whole[1], rest[1]);
+        *lo = whole[0];
+        *hi = whole[1];
     }
 };
 
@@ -351,12 +347,13 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s.x_full[i], 2 * kConvWarps);  // both chunks of a block
             for (int c = 0; c < 2; ++c) ptx::mbar_init(&s.x_empty[i][c], 1);
-            ptx::mbar_init(&s.rest_done[i], 1);
         }
         for (int i = 0; i < kPtrRing; ++i) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
             ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
         }
+        ptx::mbar_init(&s.dims_full, kConvWarps);
+        ptx::mbar_init(&s.rest_empty, 1);
         ptx::mbar_init(&s.s_full, 1);
         ptx::mbar_init(&s.s_free, kSoftWarps);
         ptx::mbar_init(&s.part_full, kSoftWarps);  // (and the other CTA's bytes)
@@ -502,15 +499,37 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         auto fetch = [&](int i, int chunk, Quarter<FMT> &q) {
             q.load(s.rec[i % kPtrRing][chunk * kChunk + row], rank, hq);
         };
-        auto unpack = [&](int i, int chunk, const Quarter<FMT> &q, auto rest) {
-            const int r = chunk * kChunk + row, b = i & 1;
-            q.template unpack<decltype(rest)::value>(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
-            ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s.x_full[b]);
+        auto unpack = [&](int i, int chunk, const Quarter<FMT> &q) {
+            if constexpr (!kRests) {
+                const int r = chunk * kChunk + row, b = i & 1;
+                q.unpack(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
+                ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.x_full[b]);
+            }
         };
-        using Whole = std::integral_constant<bool, false>;
-        using First = std::integral_constant<bool, kRests>;  // what a block's buffer holds first
+        // FP8: 64 dims of the whole block at a time, with their rests, which go into the
+        // scores before the next 64 dims' come into their buffer
+        auto unpack_dims = [&](int i, int a) {
+            if constexpr (kRests) {
+                uint8_t *x = s.x[i & 1] + a * kAtom;
+                uint4 rest[2][2];
+                own.unpack(a, rank, sw128(x, row, 2 * hq), sw128(x, row, 2 * hq + 1), rest[0]);
+                other.unpack(a, rank, sw128(x, kChunk + row, 2 * hq), sw128(x, kChunk + row, 2 * hq + 1), rest[1]);
+                if (!wait(&s.rest_empty, (a & 1) ^ 1)) return false;
+                if (a < 3 || rank == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        *sw128(s.rest, c * kChunk + row, 2 * hq) = rest[c][0];
+                        *sw128(s.rest, c * kChunk + row, 2 * hq + 1) = rest[c][1];
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s.dims_full);
+            }
+            return true;
+        };
         bool ok = true;
         if (u.n_blocks > 0) {
             ok = wait(&s.ptr_full[0], 0);
@@ -526,15 +545,14 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ok = !more || wait(&s.ptr_full[n % kPtrRing], n / kPtrRing & 1);
             ok = ok && wait(&s.x_empty[i & 1][0], (i >> 1 & 1) ^ 1);
             if (!ok) break;
-            unpack(i, 0, own, First{});
+            unpack(i, 0, own);
             ok = wait(&s.x_empty[i & 1][1], (i >> 1 & 1) ^ 1);
             if (!ok) break;
-            unpack(i, 1, other, First{});
-            if (kRests) {  // the rests are in the scores: the rounded values in their place
-                ok = wait(&s.rest_done[i & 1], i >> 1 & 1);
+            unpack(i, 1, other);
+            if (kRests) {
+#pragma unroll
+                for (int a = 0; a < 4; ++a) ok = ok && unpack_dims(i, a);
                 if (!ok) break;
-                unpack(i, 0, own, Whole{});
-                unpack(i, 1, other, Whole{});
             }
             if (more) {
                 fetch(n, 0, own);
@@ -560,33 +578,42 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
             if (i < u.n_blocks) {  // QK(i)
-                // (a buffer's phases: one a block, or two with rests)
-                ok = wait(&s.x_full[i & 1], kRests ? 0 : i >> 1 & 1) && (i == 0 || wait(&s.s_free, (i & 1) ^ 1));
-                if (!ok) break;
-                ptx::tc_fence_after();
                 const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.x[i & 1]));
-                auto qk = [&](int k, bool add) {
-                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8,
-                                    xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, add);
+                auto qk = [&](int k, uint64_t d, bool add) {  // dims [16 k, 16 k + 16)
+                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8, d, kIdescQK, add);
                 };
+                auto at = [](int k) { return (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4); };
                 if (kRests) {
-                    if (leader) {
+                    const uint64_t rd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.rest));
 #pragma unroll
-                        for (int k = 0; k < kHalf / 16; ++k)
-                            if (k < 12 || rank == 0) qk(k, k > 0);  // (the last 64 dims of rank 1 are rope)
-                        ptx::mma_commit(&s.rest_done[i & 1]);
+                    for (int a = 0; a < 4; ++a) {
+                        ok = ok && wait(&s.dims_full, a & 1) && (a > 0 || i == 0 || wait(&s.s_free, (i & 1) ^ 1));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        if (leader) {
+                            if (a < 3 || rank == 0) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) qk(4 * a + k, rd + at(k), a > 0 || k > 0);
+                            }
+                            ptx::mma_commit(&s.rest_empty);
+#pragma unroll
+                            for (int k = 4 * a; k < 4 * a + 4; ++k) qk(k, xd + at(k), true);
+                            if (a == 3) ptx::mma_commit(&s.s_full);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    ok = wait(&s.x_full[i & 1], 1);
+                    if (!ok) break;
+                } else {
+                    ok = wait(&s.x_full[i & 1], i >> 1 & 1) && (i == 0 || wait(&s.s_free, (i & 1) ^ 1));
                     if (!ok) break;
                     ptx::tc_fence_after();
-                }
-                if (leader) {
+                    if (leader) {
 #pragma unroll
-                    for (int k = 0; k < kHalf / 16; ++k) qk(k, kRests || k > 0);
-                    ptx::mma_commit(&s.s_full);
+                        for (int k = 0; k < kHalf / 16; ++k) qk(k, xd + at(k), k > 0);
+                        ptx::mma_commit(&s.s_full);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (i > 0) {  // PV(i - 1): the own, then the other CTA's candidates
                 const uint32_t ph = (i & 1) ^ 1;
