@@ -1,6 +1,7 @@
 // attention_fp4.cu -- sink-merged attention over caches of 4-bit records
-// (csa_sink_attention_decode_fp4, hca_sink_attention_decode_fp4) on the tensor
-// cores.
+// (csa_sink_attention_decode_fp4, hca_sink_attention_decode_fp4), and of a tree's
+// drafted tokens over 4-bit or FP8 records (csa_tree_attention_decode,
+// hca_tree_attention_decode), on the tensor cores.
 //
 // For head h over candidates j (x_j the dequantised latent):
 //   z_j = scale * q_h . x_j,  o_h = sum_j e^{z_j-M} x_j / (e^{sink_h-M} + sum_j e^{z_j-M}),
@@ -44,6 +45,21 @@
 // which need no partial sums but 64-column MMAs and one and a half times the
 // unpacking, took 222 us; more warps for the unpacking, the softmax or the exchange
 // cost registers, and all were slower.)
+//
+// A tree's token differs in its window alone: the pointer warp walks up its ancestors
+// and takes their records from the drafts. 8 x 8 tokens of 2176 candidates take 62 us,
+// 4 x 32 of 8320 382.
+//
+// FP8 latents (a code times an fp32 multiplier of 128 dims) do not fit BF16. Rounded
+// once, they move each score by 10^-3 and the log-sums by 4 10^-5 of their value, so the
+// scores take them as two BF16 numbers, the rounded value and the rest (2^-17 of it is
+// lost): q . x = q . bf16(x) + q . bf16(x - bf16(x)). PV takes the rounded ones, whose
+// error there is of the size of the weights'. The rests, 64 candidates x 64 dims at a time,
+// pass through a ring of three 8 KB buffers, all that fits. That makes a block 9000
+// cycles: 7 x 4 ragged chains over 2048 entries 48.2 us (with rounded latents 38.7). The
+// rests of a whole block before its rounded values in the same buffer, unpacked twice,
+// took 61.2 us, one buffer of 64 dims of the block 50.8; issuing PV as soon as
+// its weights are there, between the pieces of QK, changed nothing.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -64,6 +80,7 @@ constexpr int kSoftCols = kChunk / 2;      // scores per softmax thread
 constexpr int kAtom = kBlock * 128;        // 128 candidates x 64 dims, 128-byte swizzled rows
 constexpr int kBlockBytes = 4 * kAtom;     // 128 candidates x 256 dims, 64 KB
 constexpr int kPtrRing = 4;                // blocks of resolved record pointers
+constexpr int kRests = 3;                  // buffers of rests (FP8)
 constexpr int kPieces = kHalf / 32 / 2;    // 32-column pieces of the output per softmax thread
 constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
 constexpr float kLog2e = 1.4426950408889634f;
@@ -77,7 +94,7 @@ constexpr uint32_t kTmemCols = 512;
 
 struct AttSmem {
     alignas(1024) uint8_t x[2][kBlockBytes];
-    alignas(1024) uint8_t rest[kAtom];         // FP8: what rounding left of 64 dims of a block
+    alignas(1024) uint8_t rest[kRests][kAtom / 2];  // FP8: what rounding left of 64 candidates x 64 dims
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
     float4 part[2][kSoftCols / 4][kHeads];     // the other CTA's part of the own scores
@@ -85,7 +102,7 @@ struct AttSmem {
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
     uint32_t vmask[kPtrRing][2];               // which own candidates exist
     uint64_t x_full[2], x_empty[2][2];         // of a buffer; of its chunks
-    uint64_t dims_full, rest_empty;            // FP8: of 64 dims and their rests; of the rests' buffer
+    uint64_t rest_full[kRests], rest_empty[kRests];
     uint64_t ptr_full[kPtrRing], ptr_empty[kPtrRing];
     uint64_t s_full, s_free, part_full, p_full, pp_full, max_full[2], o_done, q_ready, mma_done, pair[4];
     uint8_t chain[CSA_MAX_TOKENS_PER_SEQ];  // a tree's token and its ancestors, the youngest first
@@ -336,7 +353,7 @@ template <int FMT, bool TREE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
     constexpr int kRecordBytes = FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes;
-    constexpr bool kRests = FMT == CSA_FORMAT_FP8;  // BF16 does not hold the latents
+    constexpr bool kFp8 = FMT == CSA_FORMAT_FP8;  // (whose latents BF16 does not hold)
     extern __shared__ uint8_t smem_raw[];
     AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -352,8 +369,10 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
             ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
         }
-        ptx::mbar_init(&s.dims_full, kConvWarps);
-        ptx::mbar_init(&s.rest_empty, 1);
+        for (int i = 0; i < kRests; ++i) {
+            ptx::mbar_init(&s.rest_full[i], kConvWarps);
+            ptx::mbar_init(&s.rest_empty[i], 1);
+        }
         ptx::mbar_init(&s.s_full, 1);
         ptx::mbar_init(&s.s_free, kSoftWarps);
         ptx::mbar_init(&s.part_full, kSoftWarps);  // (and the other CTA's bytes)
@@ -395,32 +414,14 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         // three stages, one block apart, so that no stage waits for the load it
         // started: entry (top-k list), page (block table), record.
         // Of a tree's window the last `own` positions are its token and the token's
-        // ancestors, found by walking up from it: lane L holds the parents of
-        // tokens L, L + 32, ..
+        // ancestors, found by walking up from it while the first entries and pages are
+        // under way: lane L holds the parents of tokens L, L + 32, ..
         int own = 0;
-        if (TREE && u.ce > u.n_sel) {
-            int up[CSA_MAX_TOKENS_PER_SEQ / 32];
+        const bool walk = TREE && u.ce > u.n_sel;
+        int up[CSA_MAX_TOKENS_PER_SEQ / 32];
 #pragma unroll
-            for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j)
-                up[j] = 32 * j + lane < P.T ? __ldg(P.parent + (int64_t)u.b * P.T + 32 * j + lane) : -1;
-            const int most = min(min(P.W, u.p + 1), P.T);
-#pragma unroll 1
-            for (int node = u.r - u.b * P.T; node >= 0 && own < most; ++own) {
-                if (lane == 0) s.chain[own] = (uint8_t)node;
-                int next = -1;
-#pragma unroll
-                for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j) {
-                    const int v = __shfl_sync(0xffffffffu, up[j], node & 31);
-                    if (node >> 5 == j) next = v;
-                }
-                if (next >= node || next < -1) {  // (a parent comes before its children: the walk ends)
-                    if (rank == 0 && lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
-                    next = -1;
-                }
-                node = next;
-            }
-            __syncwarp();
-        }
+        for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j)
+            up[j] = walk && 32 * j + lane < P.T ? __ldg(P.parent + (int64_t)u.b * P.T + 32 * j + lane) : -1;
         auto cand = [&](int i, int e) {
             return u.cb + i * kBlock + (e < 2 ? rank : rank ^ 1) * kChunk + (e & 1) * 32 + lane;
         };
@@ -460,6 +461,25 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         for (int e = 0; e < 4; ++e) next_entry[e] = u.n_blocks > 1 ? load_entry(1, e) : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) page[e] = u.n_blocks > 0 ? load_page(0, e, entry[e]) : 0;
+        if (walk) {
+            const int most = min(min(P.W, u.p + 1), P.T);
+#pragma unroll 1
+            for (int node = u.r - u.b * P.T; node >= 0 && own < most; ++own) {
+                if (lane == 0) s.chain[own] = (uint8_t)node;
+                int next = -1;
+#pragma unroll
+                for (int j = 0; j < CSA_MAX_TOKENS_PER_SEQ / 32; ++j) {
+                    const int v = __shfl_sync(0xffffffffu, up[j], node & 31);
+                    if (node >> 5 == j) next = v;
+                }
+                if (next >= node || next < -1) {  // (a parent comes before its children: the walk ends)
+                    if (rank == 0 && lane == 0) report_error(P.err, CSA_ERR_BAD_INDEX);
+                    next = -1;
+                }
+                node = next;
+            }
+            __syncwarp();
+        }
 #pragma unroll 1
         for (int i = 0; i < u.n_blocks; ++i) {
             const int pr = i % kPtrRing;
@@ -500,7 +520,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             q.load(s.rec[i % kPtrRing][chunk * kChunk + row], rank, hq);
         };
         auto unpack = [&](int i, int chunk, const Quarter<FMT> &q) {
-            if constexpr (!kRests) {
+            if constexpr (!kFp8) {
                 const int r = chunk * kChunk + row, b = i & 1;
                 q.unpack(rank, hq, sw128(s.x[b], r, 2 * hq), sw128(s.x[b], r, 2 * hq + 1));
                 ptx::fence_proxy_async_smem();  // generic-proxy stores -> MMA (async proxy) reads
@@ -508,25 +528,24 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (lane == 0) ptx::mbar_arrive(&s.x_full[b]);
             }
         };
-        // FP8: 64 dims of the whole block at a time, with their rests, which go into the
-        // scores before the next 64 dims' come into their buffer
-        auto unpack_dims = [&](int i, int a) {
-            if constexpr (kRests) {
+        // FP8: 64 dims of a chunk at a time, and their rests, which go into the scores from
+        // a ring of buffers
+        int slot = 0;
+        uint32_t turn = 1;  // parity of the ring's last turn
+        auto unpack_dims = [&](int i, int a, int chunk, const Quarter<FMT> &q) {
+            if constexpr (kFp8) {
                 uint8_t *x = s.x[i & 1] + a * kAtom;
-                uint4 rest[2][2];
-                own.unpack(a, rank, sw128(x, row, 2 * hq), sw128(x, row, 2 * hq + 1), rest[0]);
-                other.unpack(a, rank, sw128(x, kChunk + row, 2 * hq), sw128(x, kChunk + row, 2 * hq + 1), rest[1]);
-                if (!wait(&s.rest_empty, (a & 1) ^ 1)) return false;
+                uint4 rest[2];
+                q.unpack(a, rank, sw128(x, chunk * kChunk + row, 2 * hq), sw128(x, chunk * kChunk + row, 2 * hq + 1), rest);
+                if (!wait(&s.rest_empty[slot], turn)) return false;
                 if (a < 3 || rank == 0) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        *sw128(s.rest, c * kChunk + row, 2 * hq) = rest[c][0];
-                        *sw128(s.rest, c * kChunk + row, 2 * hq + 1) = rest[c][1];
-                    }
+                    *sw128(s.rest[slot], row, 2 * hq) = rest[0];
+                    *sw128(s.rest[slot], row, 2 * hq + 1) = rest[1];
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&s.dims_full);
+                if (lane == 0) ptx::mbar_arrive(&s.rest_full[slot]);
+                if (++slot == kRests) slot = 0, turn ^= 1;
             }
             return true;
         };
@@ -549,9 +568,9 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ok = wait(&s.x_empty[i & 1][1], (i >> 1 & 1) ^ 1);
             if (!ok) break;
             unpack(i, 1, other);
-            if (kRests) {
+            if (kFp8) {
 #pragma unroll
-                for (int a = 0; a < 4; ++a) ok = ok && unpack_dims(i, a);
+                for (int a = 0; a < 4; ++a) ok = ok && unpack_dims(i, a, 0, own) && unpack_dims(i, a, 1, other);
                 if (!ok) break;
             }
             if (more) {
@@ -575,32 +594,45 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 ptx::mma_f16(tmem + kColO, ad + (uint64_t)(k * 32 >> 4), bd + (uint64_t)(k * 2048 >> 4), kIdescPV,
                              !(first && k == 0));
         };
+        int slot = 0;       // of the rests' ring (FP8), and
+        uint32_t turn = 0;  // the parity of its turn
 #pragma unroll 1
         for (int i = 0; i <= u.n_blocks && ok; ++i) {
             if (i < u.n_blocks) {  // QK(i)
                 const uint64_t xd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.x[i & 1]));
-                auto qk = [&](int k, uint64_t d, bool add) {  // dims [16 k, 16 k + 16)
-                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8, d, kIdescQK, add);
+                auto qk = [&](int k) {  // dims [16 k, 16 k + 16)
+                    ptx::mma_f16_ts(tmem + kColS, tmem + kColQ + k * 8,
+                                    xd + (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4), kIdescQK, kFp8 || k > 0);
                 };
-                auto at = [](int k) { return (uint64_t)(((k >> 2) * kAtom + (k & 3) * 32) >> 4); };
-                if (kRests) {
-                    const uint64_t rd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.rest));
+                if (kFp8) {
+                    // the rests of a chunk's 64 dims into its half of the scores, then, both
+                    // chunks' being there, the 64 dims themselves
+                    constexpr uint32_t kIdescRest = ptx::idesc_f32acc(1, 1, 128, kChunk);
+#pragma unroll 1
+                    for (int dims = 0; dims < 4 && ok; ++dims) {
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        ok = ok && wait(&s.dims_full, a & 1) && (a > 0 || i == 0 || wait(&s.s_free, (i & 1) ^ 1));
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        if (leader) {
-                            if (a < 3 || rank == 0) {
+                        for (int chunk = 0; chunk < 2; ++chunk) {
+                            ok = ok && wait(&s.rest_full[slot], turn) &&
+                                 (dims + chunk > 0 || i == 0 || wait(&s.s_free, (i & 1) ^ 1));
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            if (leader) {
+                                if (dims < 3 || rank == 0) {  // (the last 64 dims of rank 1 are rope: no rests)
+                                    const uint64_t rd = ptx::desc_kmajor_sw128(ptx::smem_u32(s.rest[slot]));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) qk(4 * a + k, rd + at(k), a > 0 || k > 0);
+                                    for (int k = 0; k < 4; ++k)
+                                        ptx::mma_f16_ts(tmem + kColS + chunk * kChunk, tmem + kColQ + (4 * dims + k) * 8,
+                                                        rd + k * 2, kIdescRest, dims > 0 || k > 0);
+                                }
+                                ptx::mma_commit(&s.rest_empty[slot]);
+                                if (chunk == 1) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) qk(4 * dims + k);
+                                }
                             }
-                            ptx::mma_commit(&s.rest_empty);
-#pragma unroll
-                            for (int k = 4 * a; k < 4 * a + 4; ++k) qk(k, xd + at(k), true);
-                            if (a == 3) ptx::mma_commit(&s.s_full);
+                            __syncwarp();
+                            if (++slot == kRests) slot = 0, turn ^= 1;
                         }
-                        __syncwarp();
                     }
                     if (!ok) break;
                 } else {
@@ -609,11 +641,11 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                     ptx::tc_fence_after();
                     if (leader) {
 #pragma unroll
-                        for (int k = 0; k < kHalf / 16; ++k) qk(k, xd + at(k), k > 0);
-                        ptx::mma_commit(&s.s_full);
+                        for (int k = 0; k < kHalf / 16; ++k) qk(k);
                     }
-                    __syncwarp();
                 }
+                if (leader) ptx::mma_commit(&s.s_full);
+                __syncwarp();
             }
             if (i > 0) {  // PV(i - 1): the own, then the other CTA's candidates
                 const uint32_t ph = (i & 1) ^ 1;
