@@ -52,6 +52,9 @@ def parse():
                     help="time the attention with its output epilogues (inverse RoPE, E2M1 output)")
     ap.add_argument("--prefill", type=int, default=0, metavar="T",
                     help="time T tokens of one 128K sequence as one step against T single-token steps")
+    ap.add_argument("--speculative", type=int, default=0, metavar="N",
+                    help="time a step of speculative decoding: a tree of N drafted tokens for each of 8 sequences of "
+                         "128K tokens through the decode step, verified and committed, in both record formats")
     ap.add_argument("--graph-replay", type=int, default=0, metavar="LAYERS",
                     help="time LAYERS decode steps (one per layer, each with its own paged cache) as direct calls "
                          "and as one replayed CUDA graph, on --workload (default: the 1K-context one)")
@@ -852,6 +855,121 @@ def prefill(args):
                                   "clock": "CUDA events, median of 20 after 3 warm-ups"}}), flush=True)
 
 
+def speculative(args):
+    """A step of speculative decoding of one layer and the verification behind
+    the last: a tree of N drafted tokens for each of 8 sequences of 128K tokens
+    (top-2048) through csa_tree_decode_step, csa_verify_drafts over a vocabulary
+    of 131072 and csa_cache_commit of the accepted path, each and all three
+    replayed from a CUDA graph, with FP8 and with 4-bit records; beside it the
+    step of one token each. CUDA events on the replay stream, median of 20 after
+    3 warm-ups, the same inputs every time."""
+    import torch
+
+    import compressed_sparse_decode_gb300 as csd
+    import synth
+    csd.build()
+    csd.load()
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    N, B, V = args.speculative, 8, 131072
+    wl = synth.custom("csa", B=B, T=N, ncap=32768, k=2048, ctx=131072, name=f"csa_b{B}_tree{N}_ctx128k_k2048")
+    x = synth.generate(wl, seed=0, device=dev)
+    g = torch.Generator(device=dev).manual_seed(1)
+    # a random tree under token 0, every token after one of the four before it
+    i = torch.arange(N, device=dev, dtype=torch.int32)
+    parent = i - 1 - (torch.rand((B, N), generator=g, device=dev) * torch.clamp(i, max=4)).int()
+    parent = torch.where(i > 0, parent.clamp(min=0), -1).to(torch.int32).contiguous()
+    depth = torch.zeros((B, N), dtype=torch.int32, device=dev)
+    for j in range(1, N):
+        depth[:, j] = depth.gather(1, parent[:, j:j + 1].long())[:, 0] + 1
+    pos = (x.q_pos[:, :1] + depth).to(torch.int32).contiguous()
+    first = x.q_pos[:, 0].contiguous()
+    logits = torch.randn((B, N, V), generator=g, device=dev) * 3
+    token = logits.argmax(-1).gather(1, parent.clamp(min=0).long()).int()
+    logits = (logits + 8.0 * torch.nn.functional.one_hot(logits.argmax(-1), V)).to(torch.bfloat16)
+    uniform = torch.rand((B, N), generator=g, device=dev)
+    noise = torch.empty((B, V), device=dev).exponential_(generator=g)
+    stream = torch.cuda.Stream(device=dev)
+
+    def timed(fn):
+        with torch.cuda.stream(stream):
+            for _ in range(3):
+                fn()
+        torch.cuda.synchronize(dev)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            fn()
+        ts = []
+        with torch.cuda.stream(stream):
+            for n in range(23):
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                a.record(stream)
+                graph.replay()
+                b.record(stream)
+                b.synchronize()
+                if n >= 3:
+                    ts.append(a.elapsed_time(b) * 1e3)
+        return round(float(statistics.median(ts)), 2)
+
+    res, accepted = {}, 0.0
+    for name, fmt in (("fp8", csd.FORMAT_FP8), ("fp4", csd.FORMAT_FP4)):
+        size = csd.FORMAT_BYTES[fmt]
+
+        def records(n):
+            rec = torch.zeros((n, size), dtype=torch.uint8, device=dev)
+            cache = csd.cache_desc(rec, n, seq_stride=n, fmt=fmt)
+            for s in range(0, n, 1 << 16):
+                t = min(n - s, 1 << 16)
+                csd.csa_cache_append(cache, torch.randn((1, t, 512), generator=g, device=dev).to(torch.bfloat16),
+                                     torch.tensor([s], dtype=torch.int32, device=dev), rope_theta=None)
+            return rec
+
+        pool = records(B * wl.ncap)
+        comp = csd.cache_desc(pool, wl.ncap, seq_stride=wl.ncap, fmt=fmt)
+        R = wl.W + N
+        ring, draft = records(B * R).view(B, R, size), records(B * N).view(B, N, size)
+        ring_cache = csd.cache_desc(ring, R, seq_stride=R, fmt=fmt)
+        out = torch.empty_like(x.q)
+        lse = torch.empty((B, N, 128), dtype=torch.float32, device=dev)
+        ws = csd.workspace(csd.OP_TREE_STEP, B, N, wl.ncap, wl.k, dev)
+        path = torch.empty((B, N), dtype=torch.int32, device=dev)
+        acc, nxt = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
+
+        def step():
+            csd.csa_tree_decode_step(x.q_idx, x.q_idx_scale, x.w_idx, x.k_idx, x.k_idx_scale, x.q, x.sink, SCALE, comp,
+                                     ring, wl.W, draft, parent, pos, x.n_comp, wl.m, wl.k, out=out, lse=lse, ws=ws,
+                                     inverse_rope=True)
+
+        def verify():
+            csd.csa_verify_drafts(logits, token, parent, uniform, noise, path=path, accepted=acc, next_token=nxt)
+
+        def commit():
+            csd.csa_cache_commit(ring_cache, draft, path, acc, first, ring=True)
+
+        def everything():
+            step()
+            verify()
+            commit()
+
+        one = [t[:, :1].contiguous() for t in (x.q_idx, x.q_idx_scale, x.w_idx, x.q, pos)]
+        single = csd.csa_decode_step if fmt == csd.FORMAT_FP8 else csd.csa_decode_step_fp4
+        out1, lse1 = torch.empty_like(one[3]), torch.empty((B, 1, 128), dtype=torch.float32, device=dev)
+        ws1 = csd.workspace(csd.OP_DECODE_STEP, B, 1, wl.ncap, wl.k, dev)
+
+        def token_step():
+            single(one[0], one[1], one[2], x.k_idx, x.k_idx_scale, one[3], x.sink, SCALE, comp, ring, wl.W, one[4],
+                   x.n_comp, wl.m, wl.k, out=out1, lse=lse1, ws=ws1, inverse_rope=True)
+
+        res[name] = {"tree_step_us": timed(step), "verify_us": timed(verify), "commit_us": timed(commit),
+                     "all_us": timed(everything), "one_token_step_us": timed(token_step)}
+        accepted = float(acc.float().mean())
+        if csd.csa_read_device_error():
+            raise RuntimeError("device error word set")
+    print(json.dumps({"speculative": {"workload": wl.name, "tokens": N, "vocabulary": V,
+                                      "mean_accepted": round(accepted, 2), **res,
+                                      "clock": "CUDA events, median of 20 after 3 warm-ups"}}), flush=True)
+
+
 def epilogue_timing(args):
     """The attention's output epilogue ("DSV4 Audit" section A4, "ROADMAP --
     Stage E" section E6) on the 128K and HCA workloads: the attention call
@@ -925,6 +1043,10 @@ def main():
     if args.prefill:
         if rank == 0:
             prefill(args)
+        return
+    if args.speculative:
+        if rank == 0:
+            speculative(args)
         return
     if args.graph_replay:
         if rank == 0:
