@@ -56,10 +56,10 @@
 // lost): q . x = q . bf16(x) + q . bf16(x - bf16(x)). PV takes the rounded ones, whose
 // error there is of the size of the weights'. The rests, 64 candidates x 64 dims at a time,
 // pass through a ring of three 8 KB buffers, all that fits. That makes a block 9000
-// cycles: 7 x 4 ragged chains over 2048 entries 48.2 us (with rounded latents 38.7). The
-// rests of a whole block before its rounded values in the same buffer, unpacked twice,
-// took 61.2 us, one buffer of 64 dims of the block 50.8; issuing PV as soon as
-// its weights are there, between the pieces of QK, changed nothing.
+// cycles: 7 x 4 ragged chains over 2048 entries, two parts each, 48.2 us (with rounded
+// latents 38.7). The rests of a whole block before its rounded values in the same buffer,
+// unpacked twice, took 61.2 us, one buffer of 64 dims of the block 50.8; issuing PV as soon
+// as its weights are there, between the pieces of QK, changed nothing.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"
@@ -81,6 +81,7 @@ constexpr int kAtom = kBlock * 128;        // 128 candidates x 64 dims, 128-byte
 constexpr int kBlockBytes = 4 * kAtom;     // 128 candidates x 256 dims, 64 KB
 constexpr int kPtrRing = 4;                // blocks of resolved record pointers
 constexpr int kRests = 3;                  // buffers of rests (FP8)
+constexpr int kDealtRows = 64;             // the most queries that are dealt out
 constexpr int kPieces = kHalf / 32 / 2;    // 32-column pieces of the output per softmax thread
 constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
 constexpr float kLog2e = 1.4426950408889634f;
@@ -122,45 +123,119 @@ struct Params {
     int m_hca, hca, T, k, n_split;
     __nv_bfloat16 *out;
     float *lse;
-    __half *part_o;         // [rows, n_split, 128, 512] FP16 (n_split > 1), each 32 dims to a power of two:
-    uint8_t *part_ex;       // [rows, n_split, 128, 16] their exponents (see part_unit)
-    float2 *part_ml;        // [rows, n_split, 128] (max, sum) in log2 units
+    __half *part_o;         // [units, 128, 512] FP16 of split queries, each 32 dims to a power of two:
+    uint8_t *part_ex;       // [units, 128, 16] their exponents (see part_unit)
+    float2 *part_ml;        // [units, 128] (max, sum) in log2 units
     uint8_t *out_fp4;       // null: BF16 output
     float *out_fp4_scale;
     int inv_rope;
     uint64_t turn[kRope / 2];
     const uint8_t *draft;   // [B, T] records of a tree's tokens, and their parents (null: no tree)
     const int32_t *parent;
+    int4 *dealt;            // [pairs] units as deal_units_kernel makes them (query, split, splits of the
+    int2 *row_units;        // query, blocks), [rows] a query's first unit and how many it has; else null
+    int rows, pairs;
     int *err;
     uint64_t wait_ns;  // limit of each bounded wait (drains keep kDrainWaitNs)
+};
+
+// Queries of an ordinary call, and a tree's, split in equal parts or as dealt out.
+enum Plan { kNoTree, kTree, kTreeDealt };
+
+// Selected entries of query r, and its candidates with the window's.
+struct Candidates {
+    int p, n_sel, n;
+    __device__ __forceinline__ Candidates(const Params &P, int r) {
+        p = __ldg(P.q_pos + r);
+        if (P.hca) {
+            n_sel = visible_entries(p, P.m_hca, __ldg(P.n_comp + r / P.T), P.comp.seq_capacity);
+        } else {
+            const int c = __ldg(P.topk_cnt + r);
+            n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
+        }
+        n = n_sel + (p >= 0 ? p - max(0, p - P.W + 1) + 1 : 0);
+    }
 };
 
 // The candidates of a work unit: [cb, ce) of the row's selected entries
 // followed by its window.
 struct Unit {
-    int r, b, split, p, n_sel, j0, cb, ce, n_blocks;
+    int r, b, p, n_sel, j0, cb, ce, n_blocks;
 };
 
+template <Plan PLAN>
 __device__ __forceinline__ Unit make_unit(const Params &P) {
     Unit u;
     const int pair = blockIdx.x >> 1;
-    u.r = pair / P.n_split;
-    u.split = pair % P.n_split;
-    u.b = u.r / P.T;
-    u.p = __ldg(P.q_pos + u.r);
-    if (P.hca) {
-        u.n_sel = visible_entries(u.p, P.m_hca, __ldg(P.n_comp + u.b), P.comp.seq_capacity);
+    int split, per;
+    if (PLAN == kTreeDealt) {
+        const int4 d = P.dealt[pair];
+        u.r = max(d.x, 0);
+        split = d.x < 0 ? -1 : d.y;
+        per = d.w * kBlock;
     } else {
-        const int c = __ldg(P.topk_cnt + u.r);
-        u.n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
+        u.r = pair / P.n_split;
+        split = pair % P.n_split;
     }
+    u.b = u.r / P.T;
+    const Candidates c(P, u.r);
+    u.p = c.p;
+    u.n_sel = c.n_sel;
     u.j0 = max(0, u.p - P.W + 1);
-    const int n = u.n_sel + (u.p >= 0 ? u.p - u.j0 + 1 : 0);
-    const int per = ((n + P.n_split - 1) / P.n_split + kBlock - 1) / kBlock * kBlock;
-    u.cb = min(n, u.split * per);
-    u.ce = min(n, u.cb + per);
+    if (PLAN != kTreeDealt) per = ((c.n + P.n_split - 1) / P.n_split + kBlock - 1) / kBlock * kBlock;
+    if (PLAN == kTreeDealt && split < 0) u.p = -1, split = 0, per = 0;  // a pair without a unit: as padding
+    u.cb = min(c.n, split * per);
+    u.ce = min(c.n, u.cb + per);
     u.n_blocks = (u.ce - u.cb + kBlock - 1) / kBlock;
     return u;
+}
+
+// Deals out the queries of a small tree step, whose lengths differ (positions, selections,
+// padding), to all pairs: units of up to c blocks, the smallest c with which they are no more
+// than the pairs. (Equal parts, pairs / queries rounded down a query, leave up to half
+// of the pairs idle: 7 x 4 ragged chains took 48.2 us with two parts each, 38.1 so.
+// Done at the start of each CTA instead, the registers that it takes made every block 12 %
+// longer.) One warp.
+__global__ void __launch_bounds__(32) deal_units_kernel(const __grid_constant__ Params P) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the attention sets up meanwhile)
+    ptx::griddep_wait();
+    const int lane = threadIdx.x;
+    int blocks[kDealtRows / 32], most = 1;
+#pragma unroll
+    for (int j = 0; j < kDealtRows / 32; ++j) {
+        blocks[j] = 0;
+        if (32 * j + lane < P.rows) {
+            const Candidates c(P, 32 * j + lane);
+            if (c.p >= 0) blocks[j] = max(1, (c.n + kBlock - 1) / kBlock);  // (one without candidates has its output)
+        }
+        most = max(most, blocks[j]);
+    }
+    int lo = 1, hi = __reduce_max_sync(0xffffffffu, most);
+    while (lo < hi) {
+        const int c = (lo + hi) >> 1;
+        int units = 0;
+#pragma unroll
+        for (int j = 0; j < kDealtRows / 32; ++j) units += (blocks[j] + c - 1) / c;
+        if ((int)__reduce_add_sync(0xffffffffu, units) <= P.pairs) hi = c;
+        else lo = c + 1;
+    }
+    int next = 0;
+#pragma unroll
+    for (int j = 0; j < kDealtRows / 32; ++j) {
+        const int n = (blocks[j] + lo - 1) / lo;
+        int end = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += v;
+        }
+        end += next;
+        const int r = 32 * j + lane;
+        if (r < P.rows) P.row_units[r] = make_int2(end - n, n);
+        for (int i = 0; i < n; ++i) P.dealt[end - n + i] = make_int4(r, i, n, lo);
+        next = __shfl_sync(0xffffffffu, end, 31);
+    }
+    for (int i = next + lane; i < P.pairs; i += 32) P.dealt[i] = make_int4(-1, 0, 1, 0);
 }
 
 // The larger magnitude, NaN if one is (a plain maximum would drop it).
@@ -349,11 +424,12 @@ struct Quarter<CSA_FORMAT_FP8> {
 
 // ---------------------------------------------------------------- the kernel
 
-template <int FMT, bool TREE>
+template <int FMT, Plan PLAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 attention_fp4_kernel(const __grid_constant__ Params P) {
     constexpr int kRecordBytes = FMT == CSA_FORMAT_FP4 ? kFp4Bytes : kRecBytes;
     constexpr bool kFp8 = FMT == CSA_FORMAT_FP8;  // (whose latents BF16 does not hold)
+    constexpr bool TREE = PLAN != kNoTree;
     extern __shared__ uint8_t smem_raw[];
     AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -393,7 +469,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     ptx::tc_fence_after();
     const uint32_t tmem = s.tmem_base;
     ptx::griddep_wait();
-    const Unit u = make_unit(P);
+    const Unit u = make_unit<PLAN>(P);
 
     auto fail = [&]() {
         report_error(P.err, CSA_ERR_TIMEOUT);
@@ -697,6 +773,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
         const uint32_t peer_part_full = ptx::mapa(ptx::smem_u32(&s.part_full), rank ^ 1);
         const uint32_t peer_pp = ptx::mapa(ptx::smem_u32(s.pp), rank ^ 1);
         const uint32_t peer_pp_full = ptx::mapa(ptx::smem_u32(&s.pp_full), rank ^ 1);
+        const bool final_out = PLAN == kTreeDealt ? P.dealt[blockIdx.x >> 1].z == 1 : P.n_split == 1;
         // this thread's maximum of block i (or, at the end, its sum) to the other
         // three threads of the head
         auto send = [&](int i, float v) {
@@ -895,7 +972,6 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             const int r = u.r;
             float factor, lse_out = 0.f;
             const float2 ml = make_float2(m, l);
-            const bool final_out = P.n_split == 1;
             if (final_out) {
                 const float sk = __ldg(P.sink + h) * kLog2e;
                 const float M = fmaxf(sk, m);
@@ -940,7 +1016,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             uint8_t *ostage = s.x[0];
             if (!(final_out && P.out_fp4)) {
                 uint8_t *srow = ostage + h * (kHalf * 2);
-                const size_t part = ((size_t)r * P.n_split + u.split) * kHeads;
+                const size_t part = (size_t)(blockIdx.x >> 1) * kHeads;  // (units are numbered in the order of their queries)
                 uint32_t exponents = 0;
 #pragma unroll 1
                 for (int piece = half * kPieces; piece < half * kPieces + kPieces; ++piece) {
@@ -1031,7 +1107,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
                 if (final_out)
                     P.lse[(size_t)r * kHeads + h] = lse_out;
                 else
-                    P.part_ml[((size_t)r * P.n_split + u.split) * kHeads + h] = ml;
+                    P.part_ml[(size_t)(blockIdx.x >> 1) * kHeads + h] = ml;
             }
         }
     }
@@ -1067,7 +1143,15 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     if (P.parent && __ldg(P.q_pos + r) < 0) return;  // a tree's padding keeps its rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x * (8 / kWarps) + warp / kWarps, part = warp % kWarps;
-    const size_t row0 = (size_t)r * P.n_split * kHeads + h, row_stride = kHeads;  // of the splits' rows
+    int n_split = P.n_split;
+    int64_t unit = (int64_t)r * n_split;
+    if (P.row_units) {
+        const int2 mine = P.row_units[r];
+        unit = mine.x;
+        n_split = mine.y;
+        if (n_split == 1) return;  // (written by its unit)
+    }
+    const size_t row0 = (size_t)unit * kHeads + h, row_stride = kHeads;  // of the splits' rows
     const uint64_t policy = ptx::l2_policy_evict_first();
     const float sk = __ldg(P.sink + h) * kLog2e;
     // four splits' rows (all splits have written theirs)
@@ -1080,7 +1164,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
             ex[q] = 32;
             v[q][0].clear();
             v[q][1].clear();
-            if (s >= P.n_split) continue;
+            if (s >= n_split) continue;
             const size_t at = row0 + s * row_stride;
             const uint4 *o = reinterpret_cast<const uint4 *>(P.part_o + at * kDim) + lane * 2;
             ex[q] = P.part_ex[at * 16 + (lane >> 1)];
@@ -1092,7 +1176,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll
     for (int j = 0; j < kMaxSplits / 32; ++j) {
         ml[j] = make_float2(-INFINITY, 0.f);
-        if (32 * j + lane < P.n_split) ml[j] = P.part_ml[row0 + (32 * j + lane) * row_stride];
+        if (32 * j + lane < n_split) ml[j] = P.part_ml[row0 + (32 * j + lane) * row_stride];
     }
     load(part);  // (while the weights are computed)
     float w[kMaxSplits / 32], M = sk, den = 0.f;
@@ -1132,7 +1216,7 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
             }
         }
         s0 += kCombineBatch * kWarps;
-        if (s0 >= P.n_split) break;
+        if (s0 >= n_split) break;
         load(s0);
     }
     if (kWarps > 1) {
@@ -1217,16 +1301,30 @@ int choose_splits(int rows, int64_t max_candidates) {
 
 }  // namespace
 
+namespace {
+// The partials of this many units: values, exponents, (max, sum).
+size_t part_bytes(int units) { return (size_t)units * kHeads * (kDim * sizeof(__half) + 16 + sizeof(float2)); }
+
+// Pairs that a tree's queries are dealt out to: all, if there are two at least for each
+// query but not one for each block; else 0, they are not dealt out. (More queries than half
+// of the pairs cannot all be split, so the longest decides as it would in any case; with a
+// pair a block, equal parts are as good, and the dealing, 2 us, is saved.)
+int dealt_units(int rows, int64_t max_candidates) {
+    const int64_t pairs = cached_sm_count() / 2, all = rows * ((max_candidates + kBlock - 1) / kBlock);
+    return rows <= kDealtRows && rows <= pairs / 2 && all > pairs ? (int)pairs : 0;
+}
+size_t dealt_bytes(int rows, int units) { return (size_t)units * sizeof(int4) + (size_t)rows * sizeof(int2); }
+}  // namespace
+
 size_t attention_fp4_workspace_bytes(int B, int T, int max_selected, int W) {
     const int n = choose_splits(B * T, (int64_t)max_selected + W);
-    const size_t parts = (size_t)B * T * n * kHeads;
-    return n == 1 ? 0 : parts * (kDim * sizeof(__half) + 16 + sizeof(float2));
+    return n == 1 ? 0 : part_bytes(B * T * n);
 }
 
 // `k` = the top-k row length (CSA) or the per-sequence capacity (HCA). The
 // workspace holds the splits' partials, their exponents and their (max, sum).
 namespace {
-template <int FMT, bool TREE>
+template <int FMT, Plan PLAN>
 cudaError_t launch_pairs(const void *q, const float *sink, float scale, const csa_cache_desc &comp, const void *ring,
                          int R, int W, const csa_draft_tree &tree, const int32_t *topk_idx, const int32_t *topk_cnt,
                          const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
@@ -1265,26 +1363,38 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
             for (int i = 0; i < kRope / 2; ++i) P.turn[i] = o.turn[i];
         }
     }
-    const int rows = B * T;
-    P.n_split = choose_splits(rows, (int64_t)k + W);
+    P.rows = B * T;
+    P.n_split = choose_splits(P.rows, (int64_t)k + W);
+    P.pairs = PLAN == kTreeDealt ? dealt_units(P.rows, (int64_t)k + W) : P.rows * P.n_split;
     if (P.n_split > 1) {
-        if (!ws || ws_bytes < attention_fp4_workspace_bytes(B, T, k, W)) return cudaErrorInvalidValue;
-        const size_t parts = (size_t)rows * P.n_split * kHeads;
+        if (!ws || ws_bytes < part_bytes(P.pairs) + (PLAN == kTreeDealt ? dealt_bytes(P.rows, P.pairs) : 0))
+            return cudaErrorInvalidValue;
+        const size_t parts = (size_t)P.pairs * kHeads;
         P.part_o = static_cast<__half *>(ws);
         P.part_ex = static_cast<uint8_t *>(ws) + parts * kDim * sizeof(__half);
         P.part_ml = reinterpret_cast<float2 *>(P.part_ex + parts * 16);
+        if (PLAN == kTreeDealt) {
+            P.dealt = reinterpret_cast<int4 *>(P.part_ml + parts);
+            P.row_units = reinterpret_cast<int2 *>(P.dealt + P.pairs);
+        }
     }
     constexpr size_t smem = sizeof(AttSmem) + 1024;
-    cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel<FMT, TREE>), (int)smem);
+    cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel<FMT, PLAN>), (int)smem);
     if (e != cudaSuccess) return e;
-    PdlLaunch l(dim3(2 * rows * P.n_split), dim3(kThreads), stream);
+    if (PLAN == kTreeDealt) {
+        PdlLaunch d(dim3(1), dim3(32), stream);
+        count_launch();
+        e = cudaLaunchKernelEx(&d.cfg, deal_units_kernel, P);
+        if (e != cudaSuccess) return e;
+    }
+    PdlLaunch l(dim3(2 * P.pairs), dim3(kThreads), stream);
     l.cfg.dynamicSmemBytes = smem;
     count_launch();
-    e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel<FMT, TREE>, P);
+    e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel<FMT, PLAN>, P);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || P.n_split == 1) return e;
     const bool spread = P.n_split > kCombineBatch;  // eight warps a head instead of one
-    PdlLaunch c(dim3(spread ? kHeads : kHeads / 8, rows), dim3(256), stream);
+    PdlLaunch c(dim3(spread ? kHeads : kHeads / 8, P.rows), dim3(256), stream);
     count_launch();
     e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8>, P) : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1>, P);
     return e == cudaSuccess ? cudaGetLastError() : e;
@@ -1297,13 +1407,14 @@ cudaError_t launch_attention_fp4(const void *q, const float *sink, float scale, 
                                  const int32_t *n_comp, int m_hca, const int32_t *q_pos, int B, int T, int k, bool hca,
                                  void *out, float *lse, const csa_attention_epilogue *epi, void *ws, size_t ws_bytes,
                                  int *err, cudaStream_t stream) {
-    return launch_pairs<CSA_FORMAT_FP4, false>(q, sink, scale, comp, ring, R, W, csa_draft_tree{}, topk_idx, topk_cnt,
+    return launch_pairs<CSA_FORMAT_FP4, kNoTree>(q, sink, scale, comp, ring, R, W, csa_draft_tree{}, topk_idx, topk_cnt,
                                                n_comp, m_hca, q_pos, B, T, k, hca, out, lse, epi, ws, ws_bytes, err,
                                                stream);
 }
 
 size_t tree_attention_workspace_bytes(int B, int N, int max_selected, int W) {
-    return attention_fp4_workspace_bytes(B, N, max_selected, W);
+    const int units = dealt_units(B * N, (int64_t)max_selected + W);
+    return units ? part_bytes(units) + dealt_bytes(B * N, units) : attention_fp4_workspace_bytes(B, N, max_selected, W);
 }
 
 // The tokens of a tree, over either record format.
@@ -1313,7 +1424,10 @@ cudaError_t launch_tree_attention(const void *q, const float *sink, float scale,
                                   const int32_t *q_pos, int B, int N, int k, bool hca, void *out, float *lse,
                                   const csa_attention_epilogue *epi, void *ws, size_t ws_bytes, int *err,
                                   cudaStream_t stream) {
-    const auto launch = fmt == CSA_FORMAT_FP4 ? launch_pairs<CSA_FORMAT_FP4, true> : launch_pairs<CSA_FORMAT_FP8, true>;
+    const bool dealt = dealt_units(B * N, (int64_t)k + W) > 0;
+    const auto launch = fmt == CSA_FORMAT_FP4
+                            ? (dealt ? launch_pairs<CSA_FORMAT_FP4, kTreeDealt> : launch_pairs<CSA_FORMAT_FP4, kTree>)
+                            : (dealt ? launch_pairs<CSA_FORMAT_FP8, kTreeDealt> : launch_pairs<CSA_FORMAT_FP8, kTree>);
     return launch(q, sink, scale, comp, ring, R, W, tree, topk_idx, topk_cnt, n_comp, m_hca, q_pos, B, N, k, hca, out,
                   lse, epi, ws, ws_bytes, err, stream);
 }

@@ -196,12 +196,12 @@ def test_a_batch_of_padding_alone(cuda_lib):
         assert bool((out == 7).all()) and bool((lse == 7).all()) and cuda_lib.csa_read_device_error() == 0
 
 
-@pytest.mark.parametrize("B", [1, 20])
-def test_a_chain_is_the_same_step_without_a_tree(cuda_lib, B):
-    """Bit for bit the ordinary call whose ring holds the drafts (4-bit records)."""
-    csd, N = cuda_lib, 4
-    c = Tree(csd, B, N, 500, "chain", 1, R=140, seed=5)
-    idx, cnt = c.select(300)
+def test_a_chain_is_the_same_step_without_a_tree(cuda_lib):
+    """Bit for bit the ordinary call whose ring holds the drafts (4-bit records; of so many queries that neither call
+    splits one)."""
+    csd, B, N = cuda_lib, 80, 4
+    c = Tree(csd, B, N, 60, "chain", 1, R=140, seed=5)
+    idx, cnt = c.select(50)
     got = c.csa(idx, cnt, inverse_rope=True)
     ring = c.ring.clone()
     for b in range(B):
@@ -209,8 +209,28 @@ def test_a_chain_is_the_same_step_without_a_tree(cuda_lib, B):
             ring[b, int(c.pos[b, i]) % 140] = c.draft[b, i]
     want = csd.csa_sink_attention_decode_fp4(c.q.cuda(), c.sink.cuda(), S.SCALE, c.cache(), ring.cuda(), c.W, idx.cuda(),
                                              cnt.cuda(), c.pos.cuda(), inverse_rope=True)
-    # (a workspace of its own size: both calls split a query alike)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("B, N, live", [(19, 2, 2), (13, 3, 1), (1, 2, 1), (4, 9, 8), (3, 13, 13), (19, 4, 4), (11, 7, 5), (38, 4, 2), (3, 100, 9)])
+def test_queries_of_very_different_lengths(cuda_lib, fmt, B, N, live):
+    """One long query among short ones and padding: fewer and more queries than half of the CTA pairs, than all
+    and twice as many."""
+    c = Tree(cuda_lib, B, N, 2200, "random", fmt, seed=B, padded=False)
+    c.pos[:, live:] = -1
+    idx, cnt = c.select(2000)
+    cnt[:, :] = torch.randint(0, 40, cnt.shape, generator=c.gen).to(torch.int32)
+    cnt[0, 0], cnt[B // 2, 0] = 2000, 700
+    for b in range(B):
+        for i in range(N):
+            idx[b, i, :int(cnt[b, i])] = torch.arange(int(cnt[b, i]), dtype=torch.int32) + b % 7
+    out, lse = outputs(B, N)
+    got = c.csa(idx, cnt, out=out, lse=lse, inverse_rope=True)
+    rows = {(0, 0), (B // 2, 0), (B - 1, live - 1)} | {(b, (b * 3) % live) for b in range(0, B, 5)}
+    c.check(got, lambda b, i: idx[b, i, :int(cnt[b, i])].numpy(), 10000.0, rows=rows)
+    assert bool((got[0].cpu()[c.pos < 0] == 7).all()) and bool(torch.isfinite(got[0].float()).all())
+    assert cuda_lib.csa_read_device_error() == 0
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
