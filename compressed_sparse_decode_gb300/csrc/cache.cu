@@ -1,6 +1,6 @@
 // cache.cu -- writing latents into a cache and reading them back
-// (csa_cache_append, csa_cache_read): FP8 and 4-bit records, contiguous, paged
-// or ring.
+// (csa_cache_append, csa_cache_read), and whole records into it (csa_cache_commit): FP8 and
+// 4-bit records, contiguous, paged or ring.
 //
 // One warp a token (several, one after the other, in large calls); lane l holds
 // dims [16 l, 16 l + 16): lanes 0..27 the nope dims (one 4-bit scale block each,
@@ -374,7 +374,9 @@ struct CommitParams {
     int *err;
 };
 
-// A warp a token: 24 or 37 words of 16 bytes, one or two a lane.
+// A warp a token: 24 or 37 words of 16 bytes, one or two a lane. Bound by its three trips
+// to memory in a row (count and first; page and number; the record): 64 x up to 128 FP8
+// records 2.8 us, a launch of nothing 2.
 __global__ void __launch_bounds__(kThreads) commit_kernel(const __grid_constant__ CommitParams P) {
     ptx::griddep_wait();
     const int lane = threadIdx.x & 31;
