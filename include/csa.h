@@ -592,7 +592,8 @@ CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_t logits_dt
  *   records  [B,N, record bytes], not part of the cache
  *   select   [B,T] int32 in [0,N) (entries behind count are not read), or NULL for t
  * An entry outside the cache or a select outside [0,N) is not stored
- * (CSA_ERR_BAD_INDEX); every other record of the cache is left as it was. Requires
+ * (CSA_ERR_BAD_INDEX); every other record of the cache is left as it was. Sequences of one
+ * call must not share a page that it writes. Requires
  * B, T, N >= 1, B*T <= 2^24, and T <= N without select. */
 CSA_API csa_status_t csa_cache_commit(csa_cache_desc cache, csa_format_t fmt, int ring, const void *records, int N,
                                       const int32_t *select, const int32_t *first, const int32_t *count, int B,
