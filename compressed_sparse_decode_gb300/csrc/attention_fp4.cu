@@ -1306,12 +1306,14 @@ namespace {
 size_t part_bytes(int units) { return (size_t)units * kHeads * (kDim * sizeof(__half) + 16 + sizeof(float2)); }
 
 // Pairs that a tree's queries are dealt out to: all, if there are two at least for each
-// query but not one for each block; else 0, they are not dealt out. (More queries than half
-// of the pairs cannot all be split, so the longest decides as it would in any case; with a
-// pair a block, equal parts are as good, and the dealing, 2 us, is saved.)
+// query and equal parts would have more than four blocks; else 0, they are not dealt out.
+// (More queries than half of the pairs cannot all be split, so the longest decides as it
+// would in any case; dealing costs 3 us, half a block's time: six queries of 17 blocks,
+// twelve parts each, 22.2 us without and 24.7 with it.)
 int dealt_units(int rows, int64_t max_candidates) {
-    const int64_t pairs = cached_sm_count() / 2, all = rows * ((max_candidates + kBlock - 1) / kBlock);
-    return rows <= kDealtRows && rows <= pairs / 2 && all > pairs ? (int)pairs : 0;
+    const int pairs = cached_sm_count() / 2, parts = choose_splits(rows, max_candidates);
+    const int64_t blocks = (max_candidates + kBlock - 1) / kBlock;
+    return rows <= kDealtRows && rows <= pairs / 2 && blocks > 4 * parts ? pairs : 0;
 }
 size_t dealt_bytes(int rows, int units) { return (size_t)units * sizeof(int4) + (size_t)rows * sizeof(int2); }
 }  // namespace
@@ -1393,7 +1395,10 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
     e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel<FMT, PLAN>, P);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || P.n_split == 1) return e;
-    const bool spread = P.n_split > kCombineBatch;  // eight warps a head instead of one
+    // Eight warps a head instead of one. For trees' queries up to three alone: one of 17
+    // splits takes 17.2 us a call with eight and 19.4 with one, three 18.7 and 19.6, four 21.6
+    // and 20.1, eight of nine splits 30.6 and 24.9.
+    const bool spread = P.n_split > kCombineBatch && (PLAN == kNoTree || P.rows <= 3);
     PdlLaunch c(dim3(spread ? kHeads : kHeads / 8, P.rows), dim3(256), stream);
     count_launch();
     e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8>, P) : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1>, P);
