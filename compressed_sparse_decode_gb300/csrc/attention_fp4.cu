@@ -81,7 +81,9 @@ constexpr int kAtom = kBlock * 128;        // 128 candidates x 64 dims, 128-byte
 constexpr int kBlockBytes = 4 * kAtom;     // 128 candidates x 256 dims, 64 KB
 constexpr int kPtrRing = 4;                // blocks of resolved record pointers
 constexpr int kRests = 3;                  // buffers of rests (FP8)
-constexpr int kDealtRows = 64;             // the most queries that are dealt out
+constexpr int kDealtRows = 304;            // the most queries that are dealt out
+constexpr int kMaxSplits = 96;             // the most units of a query
+constexpr uint32_t kWarp = 0xffffffffu;
 constexpr int kPieces = kHalf / 32 / 2;    // 32-column pieces of the output per softmax thread
 constexpr int kFp4RowBytes = kDim / 2;     // E2M1 output bytes per head
 constexpr float kLog2e = 1.4426950408889634f;
@@ -134,7 +136,7 @@ struct Params {
     const int32_t *parent;
     int4 *dealt;            // [pairs] units as deal_units_kernel makes them (query, split, splits of the
     int2 *row_units;        // query, blocks), [rows] a query's first unit and how many it has; else null
-    int rows, pairs;
+    int rows, pairs, round;  // queries, pairs launched, pairs that run at once
     int *err;
     uint64_t wait_ns;  // limit of each bounded wait (drains keep kDrainWaitNs)
 };
@@ -190,50 +192,70 @@ __device__ __forceinline__ Unit make_unit(const Params &P) {
     return u;
 }
 
-// Deals out the queries of a small tree step, whose lengths differ (positions, selections,
-// padding), to all pairs: units of up to c blocks, the smallest c with which they are no more
-// than the pairs. (Equal parts, pairs / queries rounded down a query, leave up to half
-// of the pairs idle: 7 x 4 ragged chains took 48.2 us with two parts each, 38.1 so.
-// Done at the start of each CTA instead, the registers that it takes made every block 12 %
-// longer.) One warp.
+// Deals out the queries of a tree step, whose lengths differ (positions, selections, padding),
+// to the pairs: units of up to c blocks, the smallest c with which they fill w rounds of all
+// pairs, w and c for the least w (c + kUnitCost), a unit costing that many blocks besides
+// its own, and the combine of what is split. (Equal parts, pairs / queries rounded down
+// a query, leave pairs idle: 7 x 4 ragged HCA chains took 48.2 us with two parts each, 38.2
+// dealt out; 5 x 8 of 65 blocks 190 whole and 156 dealt out, ragged ones 177 and 90. Done at the
+// start of each CTA instead, the registers that it takes made every block 12 % longer.)
+// One warp, kEach queries a lane.
+constexpr float kUnitCost = 2.5f, kPartCost = 0.015f;
+template <int kEach>
 __global__ void __launch_bounds__(32) deal_units_kernel(const __grid_constant__ Params P) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the attention sets up meanwhile)
     ptx::griddep_wait();
     const int lane = threadIdx.x;
-    int blocks[kDealtRows / 32], most = 1;
+    int blocks[kEach], most = 1, live = 0;
 #pragma unroll
-    for (int j = 0; j < kDealtRows / 32; ++j) {
+    for (int j = 0; j < kEach; ++j) {
         blocks[j] = 0;
         if (32 * j + lane < P.rows) {
             const Candidates c(P, 32 * j + lane);
             if (c.p >= 0) blocks[j] = max(1, (c.n + kBlock - 1) / kBlock);  // (one without candidates has its output)
         }
         most = max(most, blocks[j]);
+        live += blocks[j] > 0;
     }
-    int lo = 1, hi = __reduce_max_sync(0xffffffffu, most);
-    while (lo < hi) {
-        const int c = (lo + hi) >> 1;
-        int units = 0;
+    most = __reduce_max_sync(kWarp, most);
+    live = __reduce_add_sync(kWarp, live);
+    auto parts = [](int b, float of_c, int c) { return (int)(((float)(b + c - 1) + 0.5f) * of_c); };  // ceil(b / c)
+    auto units = [&](int c) {
+        const float of_c = 1.f / (float)c;
+        int n = 0;
 #pragma unroll
-        for (int j = 0; j < kDealtRows / 32; ++j) units += (blocks[j] + c - 1) / c;
-        if ((int)__reduce_add_sync(0xffffffffu, units) <= P.pairs) hi = c;
-        else lo = c + 1;
+        for (int j = 0; j < kEach; ++j) n += parts(blocks[j], of_c, c);
+        return (int)__reduce_add_sync(kWarp, n);
+    };
+    int best = most;
+    float least = INFINITY;
+    for (int w = max(1, (live + P.round - 1) / P.round); w * P.round <= P.pairs; ++w) {
+        int lo = (most + kMaxSplits - 1) / kMaxSplits, hi = most;
+        while (lo < hi) {
+            const int c = (lo + hi) >> 1;
+            if (units(c) <= w * P.round) hi = c;
+            else lo = c + 1;
+        }
+        const int n = units(lo);
+        const float time = w * (lo + kUnitCost) + (n > live ? kPartCost * n : 0.f);
+        if (time < least) least = time, best = lo;
     }
     int next = 0;
+    const float of_best = 1.f / (float)best;
 #pragma unroll
-    for (int j = 0; j < kDealtRows / 32; ++j) {
-        const int n = (blocks[j] + lo - 1) / lo;
+    for (int j = 0; j < kEach; ++j) {
+        const int n = parts(blocks[j], of_best, best);
         int end = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, end, o);
+            const int v = __shfl_up_sync(kWarp, end, o);
             if (lane >= o) end += v;
         }
         end += next;
         const int r = 32 * j + lane;
         if (r < P.rows) P.row_units[r] = make_int2(end - n, n);
-        for (int i = 0; i < n; ++i) P.dealt[end - n + i] = make_int4(r, i, n, lo);
-        next = __shfl_sync(0xffffffffu, end, 31);
+        for (int i = 0; i < n; ++i) P.dealt[end - n + i] = make_int4(r, i, n, best);
+        next = __shfl_sync(kWarp, end, 31);
     }
     for (int i = next + lane; i < P.pairs; i += 32) P.dealt[i] = make_int4(-1, 0, 1, 0);
 }
@@ -1129,7 +1151,6 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 // 18.8 us a call, and with one warp 16.9, 18.2 and 28.7; two splits of 32 queries
 // took 46 us with one warp, with eight 68.
 constexpr int kCombineBatch = 4;
-constexpr int kMaxSplits = 96;
 template <int kWarps>
 __global__ void __launch_bounds__(256, 3)
 combine_fp4_kernel(const __grid_constant__ Params P) {
@@ -1305,15 +1326,18 @@ namespace {
 // The partials of this many units: values, exponents, (max, sum).
 size_t part_bytes(int units) { return (size_t)units * kHeads * (kDim * sizeof(__half) + 16 + sizeof(float2)); }
 
-// Pairs that a tree's queries are dealt out to: all, if there are two at least for each
-// query and equal parts would have more than four blocks; else 0, they are not dealt out.
-// (More queries than half of the pairs cannot all be split, so the longest decides as it
-// would in any case; dealing costs 3 us, half a block's time: six queries of 17 blocks,
-// twelve parts each, 22.2 us without and 24.7 with it.)
+// Pairs launched for a tree's queries that are dealt out: as many times all pairs as the
+// queries fill them, and once more where that leaves a choice; 0 where they are not dealt
+// out. Dealing costs 3 us, half a block's time, and pairs that get no unit 1 us a round: six
+// queries of 17 blocks, twelve parts each, take 22.2 us without and 24.7 with it. So it is
+// done where equal parts have more than four blocks and, of more queries than half of the
+// pairs, which would go unsplit, more than 24.
 int dealt_units(int rows, int64_t max_candidates) {
     const int pairs = cached_sm_count() / 2, parts = choose_splits(rows, max_candidates);
     const int64_t blocks = (max_candidates + kBlock - 1) / kBlock;
-    return rows <= kDealtRows && rows <= pairs / 2 && blocks > 4 * parts ? pairs : 0;
+    if (rows > kDealtRows || pairs < 1) return 0;
+    if (2 * rows <= pairs) return blocks > 4 * parts ? pairs : 0;
+    return blocks > 24 ? pairs * ((rows + pairs - 1) / pairs + 1) : 0;
 }
 size_t dealt_bytes(int rows, int units) { return (size_t)units * sizeof(int4) + (size_t)rows * sizeof(int2); }
 }  // namespace
@@ -1368,7 +1392,8 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
     P.rows = B * T;
     P.n_split = choose_splits(P.rows, (int64_t)k + W);
     P.pairs = PLAN == kTreeDealt ? dealt_units(P.rows, (int64_t)k + W) : P.rows * P.n_split;
-    if (P.n_split > 1) {
+    P.round = cached_sm_count() / 2;
+    if (P.n_split > 1 || PLAN == kTreeDealt) {
         if (!ws || ws_bytes < part_bytes(P.pairs) + (PLAN == kTreeDealt ? dealt_bytes(P.rows, P.pairs) : 0))
             return cudaErrorInvalidValue;
         const size_t parts = (size_t)P.pairs * kHeads;
@@ -1386,7 +1411,8 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
     if (PLAN == kTreeDealt) {
         PdlLaunch d(dim3(1), dim3(32), stream);
         count_launch();
-        e = cudaLaunchKernelEx(&d.cfg, deal_units_kernel, P);
+        e = P.rows <= 64 ? cudaLaunchKernelEx(&d.cfg, deal_units_kernel<2>, P)
+                         : cudaLaunchKernelEx(&d.cfg, deal_units_kernel<(kDealtRows + 31) / 32>, P);
         if (e != cudaSuccess) return e;
     }
     PdlLaunch l(dim3(2 * P.pairs), dim3(kThreads), stream);
@@ -1394,7 +1420,7 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
     count_launch();
     e = cudaLaunchKernelEx(&l.cfg, attention_fp4_kernel<FMT, PLAN>, P);
     if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess || P.n_split == 1) return e;
+    if (e != cudaSuccess || (P.n_split == 1 && PLAN != kTreeDealt)) return e;
     // Eight warps a head instead of one. For trees' queries up to three alone: one of 17
     // splits takes 17.2 us a call with eight and 19.4 with one, three 18.7 and 19.6, four 21.6
     // and 20.1, eight of nine splits 30.6 and 24.9.

@@ -234,6 +234,25 @@ def test_queries_of_very_different_lengths(cuda_lib, fmt, B, N, live):
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("B, N, long", [(100, 1, 16400), (40, 1, 9000), (150, 2, 4000), (304, 1, 4000), (305, 1, 4000)])
+def test_hca_queries_of_very_different_lengths(cuda_lib, fmt, B, N, long):
+    """A query of up to 130 blocks among short ones, more queries than half of the pairs up to the most that are dealt
+    out, and one more; all sequences' tables lead to the same pages."""
+    cap, page = long + 100, 32
+    c = Tree(cuda_lib, B, N, 32, "chain", fmt, seed=B, page=page)
+    pages = -(-cap // page)
+    c.cap, c.pool = cap, S.random_records(pages * page, fmt, 77)
+    c.table = torch.randperm(pages, generator=c.gen).to(torch.int32).repeat(B, 1).contiguous()
+    n_comp = torch.randint(0, 6, (B,), generator=c.gen).to(torch.int32)
+    n_comp[B // 3], n_comp[B - 1] = long, long // 2
+    c.pos += long - int(c.pos.min())
+    got = c.hca(n_comp, 1, inverse_rope=True)
+    assert cuda_lib.csa_read_device_error() == 0 and bool(torch.isfinite(got[0].float()).all())
+    rows = {(b, N - 1) for b in (0, B // 3, B // 2, B - 1)}
+    c.check(got, lambda b, i: np.arange(int(n_comp[b])), 10000.0, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_only_ancestors_and_committed_tokens_are_read(cuda_lib, fmt):
     """Latents that are NaN in every place that no token may look at."""
     csd, B, N, W = cuda_lib, 2, 10, 16
