@@ -219,7 +219,11 @@ __global__ void __launch_bounds__(32) deal_units_kernel(const __grid_constant__ 
     }
     most = __reduce_max_sync(kWarp, most);
     live = __reduce_add_sync(kWarp, live);
-    auto parts = [](int b, float of_c, int c) { return (int)(((float)(b + c - 1) + 0.5f) * of_c); };  // ceil(b / c)
+    auto parts = [](int b, float of_c, int c) {  // ceil(b / c): within one by floats (b <= 2^24), then as whole numbers
+        int q = (int)((float)(b + c - 1) * of_c);
+        q += q * c < b ? 1 : 0;
+        return q - ((q - 1) * c >= b ? 1 : 0);
+    };
     auto units = [&](int c) {
         const float of_c = 1.f / (float)c;
         int n = 0;

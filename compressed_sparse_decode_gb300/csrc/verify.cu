@@ -262,7 +262,7 @@ struct Smem {
     float uniform[kMaxNodes];
     float logit[kMaxNodes], draft[kMaxNodes];  // of the drafts: their logit and probability, in their parents' rows
     uint8_t out[kWarps][kMaxNodes];            // a warp's list of the current token's rejected children (no draft)
-    int abort_flag;
+    int abort_flag;                            // (never raised: one warp of the CTA waits)
 };
 
 // Joins every thread's part over the cluster; the same result, bit for bit, in
@@ -489,8 +489,12 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         }
         break;
     }
-    if (!ok) {  // given up: nothing is on its way to a CTA that has left
+    if (!ok) {
+        // given up: what was sent to another CTA (16 bytes a pass) lands long before this
+        // bounded pause ends, and none has left before the others' has
         if (tid == 0) report_error(P.err, CSA_ERR_TIMEOUT);
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ptx::globaltimer_ns() - t0 < 100000ull) {}
         ptx::cluster_sync();
     }
     if (rank == 0) {

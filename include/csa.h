@@ -562,8 +562,9 @@ CSA_API csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_i
  *                NaN) has no distribution: if the walk reaches it, it ends there
  *                and next_token is -1
  *   draft_probs  NULL, or [B,N,V] of type draft_dtype, dense: row i is the
- *                distribution that the children of i were drawn from (not read for
- *                rows that the walk does not reach or that have no children)
+ *                distribution that the children of i were drawn from (of rows that the
+ *                walk does not reach no more than the children's own elements is read,
+ *                of rows without children nothing counts)
  *   token        [B,N] int32; parent [B,N] int32 (see csa_draft_tree; token 0's is not
  *                read, and tokens that token 0 does not lead to, as those with
  *                parent -1, are never reached). A draft outside [0,V) is never

@@ -356,6 +356,70 @@ def test_offsets_past_32_bits(cuda_lib, fmt):
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("B, N, cap", [(1, 1, 200), (2, 12, 2000)])  # many splits; two
+def test_a_selected_nan_record_reaches_its_row_only(cuda_lib, fmt, B, N, cap):
+    c = Tree(cuda_lib, B, N, cap, "random", fmt, seed=21)
+    c.sink[3], c.sink[4] = -float("inf"), 80.0
+    idx, cnt = c.select(min(cap, 1500))
+    cnt[:, :] = idx.shape[2]
+    for b in range(B):
+        for i in range(N):
+            idx[b, i] = torch.arange(idx.shape[2], dtype=torch.int32) + 1
+    if idx.shape[2] >= cap:
+        idx, cnt = idx[:, :, :cap - 1].contiguous(), cnt.clamp(max=cap - 1)
+    clean = c.csa(idx, cnt)
+    c.check(clean, lambda b, i: idx[b, i, :int(cnt[b, i])].numpy(), rows={(0, 0), (B - 1, N - 1)})
+    rec = c.pool[int(c.where(B - 1, [0])[0])]
+    rec[:] = 0xFF  # entry 0 of the last sequence: NaN in every place
+    idx[B - 1, N - 1, 0] = 0
+    got = c.csa(idx, cnt)
+    assert bool(torch.isnan(got[0][B - 1, N - 1]).all()) and bool(torch.isnan(got[1][B - 1, N - 1]).all())
+    keep = torch.ones((B, N), dtype=torch.bool)
+    keep[B - 1, N - 1] = False
+    keep = keep.cuda()
+    assert torch.equal(got[0][keep], clean[0][keep]) and torch.equal(got[1][keep], clean[1][keep])
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+def test_dealt_out_queries_captured_and_replayed(cuda_lib, fmt):
+    """Lengths that change between replays deal the queries out anew; two calls in one graph share a workspace."""
+    csd, B, N, cap = cuda_lib, 4, 11, 4000
+    c = Tree(csd, B, N, cap, "random", fmt, seed=22, page=1)
+    c.pos = (4000 + S.depths(c.parent)).to(torch.int32)
+    q, sink, ring, draft, parent, pos = (t.cuda() for t in (c.q, c.sink, c.ring, c.draft, c.parent, c.pos))
+    comp = c.cache()
+    n_comp = torch.tensor([4000, 10, 0, 2500], dtype=torch.int32, device="cuda")
+    ws = csd.workspace(csd.OP_HCA_TREE_ATTENTION, B, N, cap, 0, "cuda")
+    a, b = outputs(B, N), outputs(B, N)
+
+    def calls(x, y):
+        for o, l in (x, y):
+            csd.hca_tree_attention_decode(q, sink, S.SCALE, comp, n_comp, ring, c.W, draft, parent, pos, 1, out=o, lse=l,
+                                          ws=ws)
+
+    calls(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(a, b)
+    for lengths, pad in (([4000, 10, 0, 2500], 0), ([3, 3999, 1200, 1], 5), ([0, 0, 0, 0], 0), ([4000] * 4, 11)):
+        n_comp.copy_(torch.tensor(lengths, dtype=torch.int32))
+        p = c.pos.clone()
+        p[1, N - pad:] = -1
+        pos.copy_(p)
+        for t in (*a, *b):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        assert bool((a[0].cpu()[p < 0] == 7).all()) and bool((a[1].cpu()[p < 0] == 7).all())
+        keep, c.pos = c.pos, p
+        c.check(a, lambda b_, i: np.arange(lengths[b_]), rows={(0, 0), (1, 0), (1, N - 1), (2, 5), (3, N - 1)})
+        c.pos = keep
+    assert csd.csa_read_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
 def test_capture_replay_and_other_stream(cuda_lib, fmt):
     csd = cuda_lib
     c = Tree(csd, 2, 5, 400, "random", fmt, seed=14)

@@ -231,6 +231,22 @@ def test_buffers_streams_and_replay(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(run([torch.empty_like(t) for t in out]), want))
 
 
+def test_expired_waits_end_and_the_next_call_is_right(cuda_lib):
+    """A wait limit of one nanosecond: a cluster's CTAs give up, or were in time; either way the call ends."""
+    csd = cuda_lib
+    x = make(20, 5, 40000, "chain", "bf16", "bf16", seed=11)
+    want = call(csd, x)
+    csd.csa_debug_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            call(csd, x)
+    finally:
+        csd.csa_debug_set_wait_limit_ns(0)
+    assert csd.csa_read_device_error() in (0, csd.ERR_TIMEOUT)
+    assert all(np.array_equal(a, b) for a, b in zip(call(csd, x), want))
+    assert csd.csa_read_device_error() == 0
+
+
 @pytest.mark.parametrize("q", [False, True])
 def test_what_is_emitted_is_drawn_from_the_target(cuda_lib, q):
     """The first emitted token of 16000 sequences with one target: each token's share within five standard
