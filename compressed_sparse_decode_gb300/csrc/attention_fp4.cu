@@ -48,7 +48,7 @@
 //
 // A tree's token differs in its window alone: the pointer warp walks up its ancestors
 // and takes their records from the drafts. 8 x 8 tokens of 2176 candidates take 62 us,
-// 4 x 32 of 8320 382.
+// 4 x 32 of 8320 382 in equal parts and 389 dealt out (see deal_units_kernel).
 //
 // FP8 latents (a code times an fp32 multiplier of 128 dims) do not fit BF16. Rounded
 // once, they move each score by 10^-3 and the log-sums by 4 10^-5 of their value, so the
@@ -57,9 +57,11 @@
 // error there is of the size of the weights'. The rests, 64 candidates x 64 dims at a time,
 // pass through a ring of three 8 KB buffers, all that fits. That makes a block 9000
 // cycles: 7 x 4 ragged chains over 2048 entries, two parts each, 48.2 us (with rounded
-// latents 38.7). The rests of a whole block before its rounded values in the same buffer,
-// unpacked twice, took 61.2 us, one buffer of 64 dims of the block 50.8; issuing PV as soon
-// as its weights are there, between the pieces of QK, changed nothing.
+// latents 38.7; dealt out 38.3). Tried on the two parts: the rests of a whole block before
+// its rounded values in the same buffer, unpacked twice, 61.2 us; one buffer of 64 dims of
+// the block 50.8; issuing PV as soon as its weights are there, between the pieces of QK, no
+// change. Tried on the dealt ones: both chunks' pieces behind one fence 38.9; buffers of 32
+// dims of both chunks, whose MMAs are 128 columns wide, 40.2.
 #include <cuda_fp4.h>
 
 #include "rows.cuh"

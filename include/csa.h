@@ -514,9 +514,10 @@ typedef struct {
  * ring. The ring has to hold the W - 1 committed positions before a root token
  * (R >= W); no token of the tree is read from it. For every token the selected or
  * visible compressed entries are those of its position q_pos, as without a tree.
- * FP8 latents are rounded to BF16, 4-bit ones are exact; weights and partial outputs
- * are rounded as in the *_fp4 calls, and as there, a NaN or infinite latent reaches
- * the rows that select it and no others. Requires N <= CSA_MAX_TOKENS_PER_SEQ;
+ * FP8 latents enter the scores as two BF16 numbers (2^-17 of a latent is lost) and the
+ * output rounded to BF16, 4-bit ones are exact; weights and partial outputs are
+ * rounded as in the *_fp4 calls, and as there, a NaN or infinite latent reaches the
+ * rows that select it and no others. Requires N <= CSA_MAX_TOKENS_PER_SEQ;
  * workspaces: CSA_OP_TREE_ATTENTION, CSA_OP_HCA_TREE_ATTENTION, CSA_OP_TREE_STEP. */
 CSA_API csa_status_t csa_tree_attention_decode(const void *q, const float *sink, float softmax_scale,
                                                csa_cache_desc comp, csa_format_t fmt, const void *swa_ring, int R,
