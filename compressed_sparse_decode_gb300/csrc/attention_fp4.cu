@@ -146,7 +146,8 @@ struct Params {
 // Queries of an ordinary call, and a tree's, split in equal parts or as dealt out.
 enum Plan { kNoTree, kTree, kTreeDealt };
 
-// Selected entries of query r, and its candidates with the window's.
+// Selected entries of query r, and its candidates with the window's. (A tree's padding has
+// none, whatever the caller's selection left in its rows.)
 struct Candidates {
     int p, n_sel, n;
     __device__ __forceinline__ Candidates(const Params &P, int r) {
@@ -154,7 +155,7 @@ struct Candidates {
         if (P.hca) {
             n_sel = visible_entries(p, P.m_hca, __ldg(P.n_comp + r / P.T), P.comp.seq_capacity);
         } else {
-            const int c = __ldg(P.topk_cnt + r);
+            const int c = P.parent && p < 0 ? 0 : __ldg(P.topk_cnt + r);
             n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
         }
         n = n_sel + (p >= 0 ? p - max(0, p - P.W + 1) + 1 : 0);
