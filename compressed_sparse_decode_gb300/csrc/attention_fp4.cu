@@ -567,7 +567,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) page[e] = u.n_blocks > 0 ? load_page(0, e, entry[e]) : 0;
         if (walk) {
-            const int most = min(min(P.W, u.p + 1), P.T);
+            const int most = min(min(P.W - 1, u.p) + 1, P.T);  // (position 2^31 - 1 has a window too)
 #pragma unroll 1
             for (int node = u.r - u.b * P.T; node >= 0 && own < most; ++own) {
                 if (lane == 0) s.chain[own] = (uint8_t)node;
