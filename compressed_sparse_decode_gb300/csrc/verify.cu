@@ -7,7 +7,8 @@
 // since max(max(a - b, 0) - c, 0) = max(a - b - c, 0) for c >= 0, all residuals of a
 // token are r_k = max(p - S_k q, 0) with S_k = R_1 + .. + R_k-1: a rejection
 // changes one number, and only R_k+1, where another child asks for it, takes a pass
-// over the row. (Without q: r_k is p without the tokens rejected so far.) At the end
+// over the row. (Without q: r_k is p without the tokens rejected so far, and R_k+1 is
+// R_k - r_k(x_k), with a pass where that is little of R_k.) At the end
 // of the walk the next token is argmax r(v) / noise(v), one more pass. Everything is
 // kept without the softmax's denominator: p stands for e^{(z - max) / t}, R_1 for its
 // sum.
@@ -222,8 +223,12 @@ __device__ __forceinline__ float weight_of(float d, float k, float k_rest) {
     return fabsf(rest) < 1.f ? fmaf(e, rest * 0.69314718f, e) : e;  // (d = -inf has no rest)
 }
 
-// A sum that tokens are taken from, in two floats: what is left after most of it
-// has gone keeps its bits.
+// A sum that tokens are taken from, in two floats: taking them off adds no rounding to the
+// sum's own error. What is left carries that error whole, so when less than kLeast of the last
+// sum is left, and another child asks for it, it is summed anew (R off by up to 1e-6 / kLeast
+// of itself; with one token of 1 - 1e-5 refused it would be off by a hundredth, and below
+// 1e-7 nothing would be left of it).
+constexpr float kLeast = 0.25f;
 struct Pair {
     float hi, lo;
 };
@@ -374,12 +379,24 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         // ---- its children
         float S = 0.f;
         Pair R = {f.sum, 0.f};
-        bool stale = false;  // R is that of the rejections before the last
-        int gone = 0;        // children in out_list
+        float whole = f.sum;  // the sum that R comes from
+        bool stale = false;   // R is to be summed: it is that of the rejections before the last, or too little of `whole`
+        int gone = 0;         // children in out_list
         int last = cur, taken = -1;
         auto weight = [&](float z, float q) {  // of a token in the residual, rejected tokens aside
             const float p = ptx::ex2_approx((z - top) * k);
             return kDraft ? p - S * q : p;
+        };
+        auto rejected = [&](int v) {  // which of a thread's tokens from v on, bit u W + e (no draft)
+            uint32_t out = 0;
+            if (!kDraft)
+                for (int o = 0; o < gone; ++o) {
+                    const int at = s.token[out_list[o]] - v;
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u)
+                        if ((uint32_t)(at - u * kThreads * W) < (uint32_t)W) out |= 1u << (u * W + at - u * kThreads * W);
+                }
+            return out;
         };
         while (taken < 0) {
             const int child = next_child(last);
@@ -394,25 +411,28 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 if (x == best) taken = child;
                 continue;
             }
-            if (kDraft && stale) {  // the sum of what is left
+            if (stale) {  // the sum of what is left
                 Found g = {0.f, 0, 0.f, 0u};
                 for (int v = mine; v < v1; v += kThreads * W * kRows) {
                     Units<DT, W, kRows> z;
                     Units<kQ, W, kRows> q;
                     z.load(P.logits, row, v, v1, kMinusInf<DT>);
-                    q.load(P.draft, qrow, v, v1, 0u);
+                    if (kDraft) q.load(P.draft, qrow, v, v1, 0u);
+                    const uint32_t out = rejected(v);
 #pragma unroll
                     for (int u = 0; u < kRows; ++u) {
                         float x[W], y[W];
                         z.get(u, x);
-                        q.get(u, y);
+                        if (kDraft) q.get(u, y);
 #pragma unroll
-                        for (int e = 0; e < W; ++e) g.sum += fmaxf(weight(x[e], y[e]), 0.f);
+                        for (int e = 0; e < W; ++e)
+                            if (kDraft || !(out >> (u * W + e) & 1u)) g.sum += fmaxf(weight(x[e], kDraft ? y[e] : 0.f), 0.f);
                     }
                 }
                 ok = join_cluster(s, g, ctas, rank, pass, Join{0.f}, P.wait_ns);
                 if (!ok) break;
                 R = {g.sum, 0.f};
+                whole = g.sum;
                 stale = false;
             }
             const float p = weight_of(s.logit[child] - top, k, scale.k_rest);
@@ -431,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 stale = true;
             } else if (r > 0.f) {
                 R = less(R, p);
+                stale = R.hi < kLeast * whole;
                 if (lane == 0) out_list[gone] = (uint8_t)child;
                 ++gone;
                 __syncwarp();
@@ -457,14 +478,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 z.load(P.logits, row, v, v1, kMinusInf<DT>);
                 if (kDraft) q.load(P.draft, qrow, v, v1, 0u);
                 e.load(P.noise, noise_row, v, v1, 0x3F800000u);
-                uint32_t out = 0;  // which of these tokens were rejected
-                if (!kDraft)
-                    for (int o = 0; o < gone; ++o) {
-                        const int at = s.token[out_list[o]] - v;
-#pragma unroll
-                        for (int u = 0; u < kRows; ++u)
-                            if ((uint32_t)(at - u * kThreads * W) < (uint32_t)W) out |= 1u << (u * W + at - u * kThreads * W);
-                    }
+                const uint32_t out = rejected(v);
 #pragma unroll
                 for (int u = 0; u < kRows; ++u) {
                     float x[W], y[W], d[W];
