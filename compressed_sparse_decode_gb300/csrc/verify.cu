@@ -291,7 +291,8 @@ __device__ __forceinline__ bool join_cluster(Smem &s, Found &f, int ctas, int ra
         }
         if (lane == 0) ptx::mbar_arrive_expect_tx(full, ctas * sizeof(Found));
         const uint32_t parity = (pass >> 1) & 1;
-        const bool here = ptx::try_wait_cluster(full, parity) ||
+        // (the first try is suspended for longer than a diagnostic limit)
+        const bool here = (wait_ns >= ptx::kPollOnlyBelowNs && ptx::try_wait_cluster(full, parity)) ||
                           (ptx::mbar_wait(full, parity, &s.abort_flag, wait_ns) && ptx::try_wait_cluster(full, parity));
         const bool all = __all_sync(kAll, here);
         f = join.warp(s.ctas[now][lane & (ctas - 1)], ctas);

@@ -575,7 +575,8 @@ CSA_API csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_i
  *   path         [B,N] int32: the accepted tokens' numbers from 0 on, -1 behind them
  *   accepted     [B] int32 in [1,N]: how many these are
  *   next_token   [B] int32
- * Weights, sums and quotients are fp32. Requires B >= 1, 1 <= N <=
+ * After CSA_ERR_TIMEOUT every sequence has its result, or the part of its path that had
+ * been walked and next_token -1. Weights, sums and quotients are fp32. Requires B >= 1, 1 <= N <=
  * CSA_MAX_TOKENS_PER_SEQ, B*N <= 65535, 1 <= V <= 2^24. Pointers need the alignment
  * of their elements only (rows that all begin on 16 bytes are read in wider loads). */
 CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_t logits_dtype, int64_t seq_stride,
@@ -687,7 +688,7 @@ CSA_API csa_status_t csa_check_device_status(int32_t *status, int32_t *host_stat
 CSA_API csa_status_t csa_read_device_error(int32_t *status, int32_t *host_code, cudaStream_t stream);
 
 /* Diagnostic: sets the time limit of the bounded waits inside the tensor-core
- * kernels (indexer and attention) for launches made after this call, in
+ * kernels (indexer and attention) and the verification for launches made after this call, in
  * nanoseconds of GPU global time; 0 restores the default of one second. A
  * wait that reaches the limit records CSA_ERR_TIMEOUT in the status word and
  * the kernel winds down: it drains its own copies and MMAs already in flight
