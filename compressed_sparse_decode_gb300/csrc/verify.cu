@@ -370,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             if (!greedy)
                 for (int v = v0 + tid * 32; v < v1; v += kThreads * 32)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(P.noise + noise_row + v));
+            __syncwarp();  // (the loops' trips differ between lanes, and the wait takes a converged warp)
             ptx::cluster_wait();
         }
         ok = join_cluster(s, f, ctas, rank, pass, Join{k}, P.wait_ns);
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         if (tid == 0) report_error(P.err, CSA_ERR_TIMEOUT);
         const uint64_t t0 = ptx::globaltimer_ns();
         while (ptx::globaltimer_ns() - t0 < 100000ull) {}
+        __syncwarp();
         ptx::cluster_sync();
     }
     if (rank == 0) {
