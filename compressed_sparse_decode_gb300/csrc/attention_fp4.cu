@@ -97,11 +97,15 @@ constexpr uint32_t kColS = 128;  // 128 columns: scores, own candidates first
 constexpr uint32_t kColO = 256;  // 256 columns: O half, fp32
 constexpr uint32_t kTmemCols = 512;
 
+// (The rests take their 24 KB with FP8 records alone: the longest 4-bit calls took 198.6 us
+// instead of 198.0 with them.)
+template <int FMT>
 struct AttSmem {
     alignas(1024) uint8_t x[2][kBlockBytes];
-    alignas(1024) uint8_t rest[kRests][kAtom / 2];  // FP8: what rounding left of 64 candidates x 64 dims
     alignas(1024) uint8_t p[kHeads * 128];     // own weights (K-major 128-byte rows)
     alignas(1024) uint8_t pp[kHeads * 128];    // the other CTA's weights
+    alignas(1024) uint8_t rest[FMT == CSA_FORMAT_FP8 ? kRests : 1][FMT == CSA_FORMAT_FP8 ? kAtom / 2 : 1024];
+                                               // what rounding left of 64 candidates x 64 dims
     float4 part[2][kSoftCols / 4][kHeads];     // the other CTA's part of the own scores
     float pmax[2][4][kHeads];                  // maxima: own CTA's halves, the other CTA's halves
     const uint8_t *rec[kPtrRing][kBlock];      // records: the own chunk's, then the other CTA's (nullptr: none)
@@ -114,7 +118,7 @@ struct AttSmem {
     uint32_t tmem_base;
     int abort_flag;
 };
-static_assert(sizeof(AttSmem) + 1024 <= 232448, "shared memory plan exceeds the per-CTA limit");
+static_assert(sizeof(AttSmem<CSA_FORMAT_FP8>) + 1024 <= 232448, "shared memory plan exceeds the per-CTA limit");
 
 struct Params {
     const __nv_bfloat16 *q;
@@ -146,16 +150,17 @@ struct Params {
 // Queries of an ordinary call, and a tree's, split in equal parts or as dealt out.
 enum Plan { kNoTree, kTree, kTreeDealt };
 
-// Selected entries of query r, and its candidates with the window's. (A tree's padding has
-// none, whatever the caller's selection left in its rows.)
+// Selected entries of query r (of sequence b), and its candidates with the window's. (A tree's
+// padding has none, whatever the caller's selection left in its rows. The attention passes the
+// b that it has: a second division ahead of these loads made its calls 0.2 us longer.)
 struct Candidates {
     int p, n_sel, n;
-    __device__ __forceinline__ Candidates(const Params &P, int r) {
+    __device__ __forceinline__ Candidates(const Params &P, int r, int b, bool tree) {
         p = __ldg(P.q_pos + r);
         if (P.hca) {
-            n_sel = visible_entries(p, P.m_hca, __ldg(P.n_comp + r / P.T), P.comp.seq_capacity);
+            n_sel = visible_entries(p, P.m_hca, __ldg(P.n_comp + b), P.comp.seq_capacity);
         } else {
-            const int c = P.parent && p < 0 ? 0 : __ldg(P.topk_cnt + r);
+            const int c = tree && p < 0 ? 0 : __ldg(P.topk_cnt + r);
             n_sel = c < 0 ? 0 : (c > P.k ? P.k : c);
         }
         n = n_sel + (p >= 0 ? p - max(0, p - P.W + 1) + 1 : 0);
@@ -183,7 +188,7 @@ __device__ __forceinline__ Unit make_unit(const Params &P) {
         split = pair % P.n_split;
     }
     u.b = u.r / P.T;
-    const Candidates c(P, u.r);
+    const Candidates c(P, u.r, u.b, PLAN != kNoTree);
     u.p = c.p;
     u.n_sel = c.n_sel;
     u.j0 = max(0, u.p - P.W + 1);
@@ -214,7 +219,8 @@ __global__ void __launch_bounds__(32) deal_units_kernel(const __grid_constant__ 
     for (int j = 0; j < kEach; ++j) {
         blocks[j] = 0;
         if (32 * j + lane < P.rows) {
-            const Candidates c(P, 32 * j + lane);
+            const int r = 32 * j + lane;
+            const Candidates c(P, r, r / P.T, true);
             if (c.p >= 0) blocks[j] = max(1, (c.n + kBlock - 1) / kBlock);  // (one without candidates has its output)
         }
         most = max(most, blocks[j]);
@@ -460,7 +466,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
     constexpr bool kFp8 = FMT == CSA_FORMAT_FP8;  // (whose latents BF16 does not hold)
     constexpr bool TREE = PLAN != kNoTree;
     extern __shared__ uint8_t smem_raw[];
-    AttSmem &s = *reinterpret_cast<AttSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    AttSmem<FMT> &s = *reinterpret_cast<AttSmem<FMT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x & 1;  // = the CTA's rank in its cluster
     volatile int *abort = &s.abort_flag;
@@ -474,7 +480,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
             ptx::mbar_init(&s.ptr_full[i], 32);  // every lane of the pointer warp
             ptx::mbar_init(&s.ptr_empty[i], kConvWarps + kSoftWarps);
         }
-        for (int i = 0; i < kRests; ++i) {
+        for (int i = 0; kFp8 && i < kRests; ++i) {
             ptx::mbar_init(&s.rest_full[i], kConvWarps);
             ptx::mbar_init(&s.rest_empty[i], 1);
         }
@@ -1158,7 +1164,7 @@ attention_fp4_kernel(const __grid_constant__ Params P) {
 // 18.8 us a call, and with one warp 16.9, 18.2 and 28.7; two splits of 32 queries
 // took 46 us with one warp, with eight 68.
 constexpr int kCombineBatch = 4;
-template <int kWarps>
+template <int kWarps, Plan PLAN>
 __global__ void __launch_bounds__(256, 3)
 combine_fp4_kernel(const __grid_constant__ Params P) {
     static_assert(kWarps == 1 || kWarps == 8, "one head a warp, or one a block");
@@ -1168,12 +1174,12 @@ combine_fp4_kernel(const __grid_constant__ Params P) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     ptx::griddep_wait();
     const int r = blockIdx.y;
-    if (P.parent && __ldg(P.q_pos + r) < 0) return;  // a tree's padding keeps its rows
+    if (PLAN != kNoTree && __ldg(P.q_pos + r) < 0) return;  // a tree's padding keeps its rows
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.x * (8 / kWarps) + warp / kWarps, part = warp % kWarps;
     int n_split = P.n_split;
     int64_t unit = (int64_t)r * n_split;
-    if (P.row_units) {
+    if (PLAN == kTreeDealt) {
         const int2 mine = P.row_units[r];
         unit = mine.x;
         n_split = mine.y;
@@ -1412,7 +1418,7 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
             P.row_units = reinterpret_cast<int2 *>(P.dealt + P.pairs);
         }
     }
-    constexpr size_t smem = sizeof(AttSmem) + 1024;
+    constexpr size_t smem = sizeof(AttSmem<FMT>) + 1024;
     cudaError_t e = set_max_dynamic_smem_once(reinterpret_cast<const void *>(attention_fp4_kernel<FMT, PLAN>), (int)smem);
     if (e != cudaSuccess) return e;
     if (PLAN == kTreeDealt) {
@@ -1434,7 +1440,8 @@ cudaError_t launch_pairs(const void *q, const float *sink, float scale, const cs
     const bool spread = P.n_split > kCombineBatch && (PLAN == kNoTree || P.rows <= 3);
     PdlLaunch c(dim3(spread ? kHeads : kHeads / 8, P.rows), dim3(256), stream);
     count_launch();
-    e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8>, P) : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1>, P);
+    e = spread ? cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<8, PLAN>, P)
+               : cudaLaunchKernelEx(&c.cfg, combine_fp4_kernel<1, PLAN>, P);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
