@@ -267,7 +267,6 @@ struct Smem {
     float uniform[kMaxNodes];
     float logit[kMaxNodes], draft[kMaxNodes];  // of the drafts: their logit and probability, in their parents' rows
     uint8_t out[kWarps][kMaxNodes];            // a warp's list of the current token's rejected children (no draft)
-    int abort_flag;                            // (never raised: one warp of the CTA waits)
 };
 
 // Joins every thread's part over the cluster; the same result, bit for bit, in
@@ -291,9 +290,11 @@ __device__ __forceinline__ bool join_cluster(Smem &s, Found &f, int ctas, int ra
         }
         if (lane == 0) ptx::mbar_arrive_expect_tx(full, ctas * sizeof(Found));
         const uint32_t parity = (pass >> 1) & 1;
-        // (the first try is suspended for longer than a diagnostic limit)
-        const bool here = (wait_ns >= ptx::kPollOnlyBelowNs && ptx::try_wait_cluster(full, parity)) ||
-                          (ptx::mbar_wait(full, parity, &s.abort_flag, wait_ns) && ptx::try_wait_cluster(full, parity));
+        const bool poll = wait_ns < ptx::kPollOnlyBelowNs;  // (a diagnostic limit: no suspension outlasts it)
+        const uint64_t t0 = ptx::globaltimer_ns();
+        bool here;
+        do here = (!poll || ptx::mbar_test_wait(full, parity)) && ptx::try_wait_cluster(full, parity);
+        while (!here && ptx::globaltimer_ns() - t0 <= wait_ns);
         const bool all = __all_sync(kAll, here);
         f = join.warp(s.ctas[now][lane & (ctas - 1)], ctas);
         f.ok = all;
@@ -312,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&s.full[i], 1);  // (and all CTAs' bytes)
-        s.abort_flag = 0;
         ptx::fence_mbar_init();
     }
     __syncthreads();
