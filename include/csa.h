@@ -567,8 +567,9 @@ CSA_API csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_i
  *                walk does not reach no more than the children's own elements is read,
  *                of rows without children nothing counts)
  *   token        [B,N] int32; parent [B,N] int32 (see csa_draft_tree; token 0's is not
- *                read, and tokens that token 0 does not lead to, as those with
- *                parent -1, are never reached). A draft outside [0,V) is never
+ *                used, and tokens that token 0 does not lead to are never reached:
+ *                padding has parent -1, and any entry outside [-1,i) is taken as -1 here
+ *                without being reported). A draft outside [0,V) is never
  *                accepted and takes nothing from r (CSA_ERR_BAD_INDEX if it is tried)
  *   uniform      [B,N] fp32 in [0,1)      noise [B,V] fp32, > 0
  *   temperature  [B] fp32, or NULL for 1
