@@ -779,8 +779,9 @@ def csa_tree_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_des
     """csa_sink_attention_decode for a tree of N drafted tokens a sequence (q [B, N, 128, 512]): token i follows
     token ``parent[b, i]`` < i (-1: the last committed token) and attends, beside its selected entries, to itself, to
     its ancestors among ``draft`` [B, N, record bytes] and to the committed tokens of its window in ``swa_ring``.
-    ``comp``, ring and drafts hold records of the cache's format, FP8 or 4-bit. Tokens with q_pos < 0 are padding:
-    their rows are left as they were (pass outputs of your own). Returns (out, lse); with fp4_out,
+    ``comp``, ring and drafts hold records of the cache's format, FP8 or 4-bit. Entries that the tree's own tokens
+    complete are not among the compressed ones (see include/csa.h). Tokens with q_pos < 0 are padding: what their rows
+    of the selection hold does not matter, and their rows are left as they were (pass outputs of your own). Returns (out, lse); with fp4_out,
     ((out_fp4, out_fp4_scale), lse)."""
     B, N, k = topk_idx.shape
     dev = _dev(q, "q")
@@ -906,7 +907,8 @@ def csa_cache_commit(cache: csa_cache_desc, records, select, count, first, ring:
     """Put record ``select[b, t]`` of ``records`` [B, N, record bytes] (of the cache's format) into the cache as entry
     ``first[b] + t`` of sequence b, for t < ``count[b]``, byte for byte: after csa_verify_drafts, ``select`` and
     ``count`` are its path and its accepted. ``select`` None: record t; ``count`` None: all of them. ``ring``: entry
-    modulo the cache's capacity. ``records`` must not be part of the cache."""
+    modulo the cache's capacity. ``records`` must not be part of the cache. ``select``, ``count`` and ``first`` begin on
+    16 bytes (a path that is a slice of a larger tensor may not)."""
     B, N, size = records.shape
     dev = _dev(records, "records")
     if cache._copied:

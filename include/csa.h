@@ -513,7 +513,14 @@ typedef struct {
  * first come from tree->records and, from the last committed token's on, from the
  * ring. The ring has to hold the W - 1 committed positions before a root token
  * (R >= W); no token of the tree is read from it. For every token the selected or
- * visible compressed entries are those of its position q_pos, as without a tree.
+ * visible compressed entries are those of its position q_pos among the stored ones, as
+ * without a tree (csa_indexer_logits' n_vis). An entry that the tree's own tokens complete
+ * is not among them: tokens behind a compression boundary have it in their window, token by
+ * token, but not also as an entry, which decoding one token at a time would give them, and
+ * their logits differ by that. The caller of a chain can append such entries (and their
+ * keys, and raise n_comp) before the call; branches of a tree would need different entries
+ * at one index, which these calls do not have. After the commit the entries that the accepted
+ * tokens complete are appended as always (csa_cache_append).
  * FP8 latents enter the scores as two BF16 numbers (2^-17 of a latent is lost) and the
  * output rounded to BF16, 4-bit ones are exact; weights and partial outputs are
  * rounded as in the *_fp4 calls, and as there, a NaN or infinite latent reaches the
@@ -543,7 +550,8 @@ CSA_API csa_status_t csa_tree_decode_step(const uint8_t *q_idx, const float *q_i
                                           size_t workspace_bytes, int32_t *status, cudaStream_t stream);
 
 /* Verification of a tree's drafted tokens against the target's distribution, given
- * the random numbers: what is emitted is distributed as if drawn from the target.
+ * the random numbers: what is emitted is distributed as if drawn from the target
+ * whose logits are passed (of a tree's attention, see above for what these know).
  * Token 0 is the sequence's newest known token (the last one emitted), the others
  * are drafts. With z = logits[b,j,.], t = temperature[b] and
  *   p_j(v) = exp(z_v / t) / sum_w exp(z_w / t),   q_j(v) = draft_probs[b,j,v]
@@ -594,7 +602,9 @@ CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_t logits_dt
  *   cache, fmt, ring, first, count   as in csa_cache_append (base is written; of more
  *            than seq_capacity tokens only the last are kept in a ring)
  *   records  [B,N, record bytes], not part of the cache
- *   select   [B,T] int32 in [0,N) (entries behind count are not read), or NULL for t
+ *   select   [B,T] int32 in [0,N) (entries behind count are not read), or NULL for t. As
+ *            every pointer of this call it begins on 16 bytes, and so has a path that
+ *            csa_verify_drafts (which asks for 4) writes for it
  * An entry outside the cache or a select outside [0,N) is not stored
  * (CSA_ERR_BAD_INDEX); every other record of the cache is left as it was. Sequences of one
  * call must not share a page that it writes. Requires
