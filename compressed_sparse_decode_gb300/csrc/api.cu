@@ -34,7 +34,6 @@ cudaError_t launch_tree_attention(const void *, const float *, float, const csa_
                                   const int32_t *, int, const int32_t *, int, int, int, bool, void *, float *,
                                   const csa_attention_epilogue *, void *, size_t, int *, cudaStream_t);
 size_t tree_attention_workspace_bytes(int B, int N, int max_selected, int W);
-size_t verify_workspace_bytes(int B, int N, int V);
 }  // namespace csa
 
 namespace csa {
@@ -212,7 +211,7 @@ size_t csa_workspace_bytes(csa_op_t op, int B, int T, int Ncap, int k) {
     case CSA_OP_HCA_TREE_ATTENTION: return tree_attention_workspace_bytes(B, T, Ncap, CSA_MAX_SWA_WINDOW);
     case CSA_OP_TREE_STEP:
         return decode_step_bytes(B, T, Ncap, k, tree_attention_workspace_bytes(B, T, k, CSA_MAX_SWA_WINDOW));
-    case CSA_OP_VERIFY: return verify_workspace_bytes(B, T, Ncap);
+    case CSA_OP_VERIFY: return 0;
     }
     return 0;
 }
@@ -393,12 +392,12 @@ namespace {
 // last call, attention_bytes what that needs.
 template <class Attention>
 csa_status_t decode_step(size_t (*attention_bytes)(int, int, int, int), const Attention &attention,
-                         const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx, const uint8_t *k_idx, const float *k_idx_scale, const void *q, const float *sink,
-                         float softmax_scale, const csa_cache_desc &comp, const void *swa_ring, int R, int W,
-                         const int32_t *q_pos, const int32_t *n_comp, int B, int T, int Ncap, int m, int k,
-                         void *out, float *lse, int32_t *topk_idx, int32_t *topk_cnt,
-                         const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
-                         int32_t *status, cudaStream_t stream) {
+                         const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx, const uint8_t *k_idx,
+                         const float *k_idx_scale, const void *q, const float *sink, float softmax_scale,
+                         const csa_cache_desc &comp, const void *swa_ring, int R, int W, const int32_t *q_pos,
+                         const int32_t *n_comp, int B, int T, int Ncap, int m, int k, void *out, float *lse,
+                         int32_t *topk_idx, int32_t *topk_cnt, const csa_attention_epilogue *epilogue,
+                         void *workspace, size_t workspace_bytes, int32_t *status, cudaStream_t stream) {
     // every argument of the three calls is checked before the first launch
     csa_status_t a = epilogue_status(epilogue, out);
     if (a != CSA_OK) return a;
@@ -456,8 +455,8 @@ csa_status_t csa_decode_step_ex(const uint8_t *q_idx, const float *q_idx_scale, 
                                 const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                 int32_t *status, cudaStream_t stream) {
     return sink_step(kFp8Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
-                       swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
-                       workspace, workspace_bytes, status, stream);
+                     swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
+                     workspace, workspace_bytes, status, stream);
 }
 
 csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale, const float *w_idx,
@@ -468,8 +467,8 @@ csa_status_t csa_decode_step_fp4(const uint8_t *q_idx, const float *q_idx_scale,
                                  const csa_attention_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                                  int32_t *status, cudaStream_t stream) {
     return sink_step(kFp4Attention, q_idx, q_idx_scale, w_idx, k_idx, k_idx_scale, q, sink, softmax_scale, comp,
-                       swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
-                       workspace, workspace_bytes, status, stream);
+                     swa_ring, R, W, q_pos, n_comp, B, T, Ncap, m, k, out, lse, topk_idx, topk_cnt, epilogue,
+                     workspace, workspace_bytes, status, stream);
 }
 
 namespace {

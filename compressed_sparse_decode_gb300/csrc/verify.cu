@@ -555,8 +555,6 @@ bool off(const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % byt
 
 }  // namespace
 
-size_t verify_workspace_bytes(int, int, int) { return 0; }
-
 }  // namespace csa
 
 extern "C" CSA_API csa_status_t csa_verify_drafts(const void *logits, csa_dtype_t logits_dtype, int64_t seq_stride,

@@ -140,7 +140,7 @@ typedef enum {
     CSA_OP_TREE_ATTENTION = 5,     /* csa_tree_attention_decode, T = N */
     CSA_OP_HCA_TREE_ATTENTION = 6, /* hca_tree_attention_decode, T = N, `k` ignored */
     CSA_OP_TREE_STEP = 7,          /* csa_tree_decode_step, T = N */
-    CSA_OP_VERIFY = 8              /* csa_verify_drafts, T = N, Ncap = V, `k` ignored */
+    CSA_OP_VERIFY = 8              /* csa_verify_drafts, T = N, Ncap = V, `k` ignored: 0 so far */
 } csa_op_t;
 
 /* Workspace bytes that `op` needs for these sizes (0 if none). A workspace
