@@ -35,9 +35,9 @@
 // one issues the MMAs, QK(i + 1) before PV(i); eight do the softmax and the
 // epilogue, two threads a head.
 //
-// Measured: 32 queries of 2176 candidates 44.3 us (412 TFLOP/s, 0.22 of the cuBLAS
+// Measured: 32 queries of 2176 candidates 44.1 us (414 TFLOP/s, 0.22 of the cuBLAS
 // rate; FP8 records: 57), 64 queries of 8320 candidates 198 us (703 TFLOP/s, 0.38;
-// FP8 records: 313), 24 ragged queries 20.8 us, one query of 192 candidates 14.7.
+// FP8 records: 313), 24 ragged queries 20.5 us, one query of 192 candidates 14.3.
 // A block takes 5700 cycles, of which the tensor core works a third. What sets the
 // pace is the way of a block through its buffer, two of which are all that fits:
 // unpacking 2 x 950 cycles, QK 1300, the exchange of the partial sums 1700, softmax

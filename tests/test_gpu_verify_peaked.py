@@ -16,8 +16,8 @@ MOST = 1 - 2.0 ** -24  # the largest uniform number
 
 
 def peaked(B, V, rests, dtype, seed):
-    """Stars of len(rests) + 1 drafts: draft i has all but rests[i] of what the drafts before it left, and the
-    last one about half."""
+    """Stars of len(rests) + 1 drafts: draft i weighs 1 / rests[i] of all that comes after it, and the last one
+    0.5 to 1.5 of the other tokens."""
     g = torch.Generator().manual_seed(seed)
     N = len(rests) + 2
     logits = torch.randn((B, 1, V), generator=g, dtype=torch.float64) * 0.5
