@@ -781,8 +781,8 @@ def csa_tree_attention_decode(q, sink, softmax_scale: float, comp: csa_cache_des
     its ancestors among ``draft`` [B, N, record bytes] and to the committed tokens of its window in ``swa_ring``.
     ``comp``, ring and drafts hold records of the cache's format, FP8 or 4-bit. Entries that the tree's own tokens
     complete are not among the compressed ones (see include/csa.h). Tokens with q_pos < 0 are padding: what their rows
-    of the selection hold does not matter, and their rows are left as they were (pass outputs of your own). Returns (out, lse); with fp4_out,
-    ((out_fp4, out_fp4_scale), lse)."""
+    of the selection hold does not matter, and their rows are left as they were (pass outputs of your own). Returns
+    (out, lse); with fp4_out, ((out_fp4, out_fp4_scale), lse)."""
     B, N, k = topk_idx.shape
     dev = _dev(q, "q")
     out, lse, out_fp4, out_fp4_scale = _attention_outputs(B, N, q.device, stream, out, lse, fp4_out, out_fp4,

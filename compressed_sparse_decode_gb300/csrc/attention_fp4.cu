@@ -98,7 +98,8 @@ constexpr uint32_t kColO = 256;  // 256 columns: O half, fp32
 constexpr uint32_t kTmemCols = 512;
 
 // (The rests take their 24 KB with FP8 records alone: the longest 4-bit calls took 198.6 us
-// instead of 198.0 with them.)
+// instead of 198.0 with them. With 4-bit records their place is 1 KB, so that what follows
+// stays on its 128-byte lines: off them, behind 16 bytes, the same calls took 204.)
 template <int FMT>
 struct AttSmem {
     alignas(1024) uint8_t x[2][kBlockBytes];
